@@ -35,7 +35,9 @@ SYMBOLS = ("dict_pack_csc_workspace_size", "dict_pack_csc", "nvfp4_pack_workspac
            "dict_gram_inverse_workspace_size", "dict_gram_inverse", "dict_obs_prune",
            "dict_refit_workspace_size", "dict_refit", "dict_pack_bcsc", "dfs_probe_mfma",
            "dfs_probe_read",
-           "dict_multi_workspace_size", "dict_multi_forward", "dict_group_forward_noalloc")
+           "dict_multi_workspace_size", "dict_multi_forward", "dict_group_forward_noalloc",
+           "dict_adapter_workspace_size", "dict_adapter_forward", "kv8_append",
+           "kv8_attention_workspace_size", "kv8_attention")
 
 
 class NV(C.Structure):
@@ -52,6 +54,19 @@ class Csc(C.Structure):
                 ("block_rows", C.c_int32), ("colptr", C.c_void_p), ("rowidx", C.c_void_p),
                 ("vals", C.c_void_p), ("nv", NV), ("col_scale", C.c_void_p),
                 ("capacity", C.c_int64)]
+
+
+class Adapters(C.Structure):
+    _fields_ = [("n", C.c_int32), ("r_max", C.c_int32), ("d_in", C.c_int32), ("d_out", C.c_int32),
+                ("A", C.c_void_p), ("lda", C.c_int64), ("stride_a", C.c_int64),
+                ("B", C.c_void_p), ("ldb", C.c_int64), ("stride_b", C.c_int64),
+                ("rank", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class KV8(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page", C.c_int32), ("dtype", C.c_int32), ("_pad", C.c_int32), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("kscale", C.c_void_p), ("vscale", C.c_void_p)]
 
 
 class DfsError(RuntimeError):
@@ -108,6 +123,14 @@ def lib():
                                    C.POINTER(Csc), C.POINTER(vp), i32, i64, vp, sz, vp],
             "dict_group_forward_noalloc": [i32, C.POINTER(vp), i32, i32, i64, C.POINTER(Dict),
                                            C.POINTER(Csc), C.POINTER(vp), i32, i64, vp],
+            "dict_adapter_workspace_size": [i32, C.POINTER(Adapters), psz],
+            "dict_adapter_forward": [vp, i32, i32, i64, C.POINTER(Adapters), vp, vp, i64, vp, i32,
+                                     i64, vp, sz, vp],
+            "kv8_append": [C.POINTER(KV8), i32, i32, vp, vp, vp, i64, i32, vp, i64, vp, i64, i32,
+                           vp],
+            "kv8_attention_workspace_size": [C.POINTER(KV8), i32, i32, i32, psz],
+            "kv8_attention": [C.POINTER(KV8), i32, i32, vp, vp, vp, i64, i32, vp, i64, i32,
+                              C.c_float, i32, i32, vp, i32, i64, vp, sz, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -523,6 +546,198 @@ def dict_zc_forward(Z, T: int, Cs, Ys=None, ydtype=torch.float16, stream=None):
            lib().dict_zc_forward(n, Z.data_ptr(), _dt(Z), T, cs, yp, _dt(Ys[0]),
                                  Ys[0].stride(0), _stream(stream)))
     return Ys
+
+
+# ----------------------------------------------------------------- adapters, 8-bit cache
+
+@dataclass
+class DeviceAdapters:
+    """A pool of low-rank adapters: ``A`` (n, >= r_max rows, d_in) and ``B``
+    (n, d_out, r_max) f16, ``rank`` int32[n], ``scale`` float32[n].  r_max is
+    B's last dimension, or ``r_max`` where B's rows are padded."""
+    A: torch.Tensor
+    B: torch.Tensor
+    rank: torch.Tensor
+    scale: torch.Tensor
+    r_max: int | None = None
+
+    def __post_init__(self):
+        A, Bm = self.A, self.B
+        if A.dim() != 3 or Bm.dim() != 3 or A.stride(2) != 1 or Bm.stride(2) != 1:
+            raise ValueError("A (n, r, d_in) and B (n, d_out, r) with unit stride in the last "
+                             "dimension required")
+        if A.dtype != torch.float16 or Bm.dtype != torch.float16:
+            raise TypeError("A and B must be float16")
+        n, r = A.shape[0], self.r_max or Bm.shape[2]
+        if Bm.shape[0] != n or A.shape[1] < r or Bm.shape[2] < r:
+            raise ValueError("A and B disagree in the number of adapters or in rank")
+        for t, dt, what in ((self.rank, torch.int32, "rank"), (self.scale, torch.float32, "scale")):
+            if t.dtype != dt or t.shape != (n,) or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous {dt} of {n} values required")
+        _same_device((A, Bm, self.rank, self.scale), "adapters")
+        self.r_max, self.d_in, self.d_out = r, A.shape[2], Bm.shape[1]
+        self._desc = Adapters(n, r, self.d_in, self.d_out, A.data_ptr(), A.stride(1), A.stride(0),
+                              Bm.data_ptr(), Bm.stride(1), Bm.stride(0), self.rank.data_ptr(),
+                              self.scale.data_ptr())
+
+    def desc(self) -> Adapters:
+        return self._desc
+
+
+@dataclass
+class DeviceKV8:
+    """A paged cache of keys and values in 8 bits: ``k`` (n_pages, heads, page,
+    head_dim) and ``v`` (n_pages, heads, head_dim, page) uint8 codes, ``kscale``
+    and ``vscale`` float32 (n_pages, heads); ``kind`` "fp8" or "int8"."""
+    k: torch.Tensor
+    v: torch.Tensor
+    kscale: torch.Tensor
+    vscale: torch.Tensor
+    kind: str
+
+    def __post_init__(self):
+        if self.kind not in CODE8:
+            raise ValueError(self.kind)
+        if self.k.dim() != 4:
+            raise ValueError("k: (n_pages, heads, page, head_dim) required")
+        n, h, p, d = self.k.shape
+        want = ((self.k, torch.uint8, (n, h, p, d), "k"), (self.v, torch.uint8, (n, h, d, p), "v"),
+                (self.kscale, torch.float32, (n, h), "kscale"),
+                (self.vscale, torch.float32, (n, h), "vscale"))
+        for t, dt, shape, what in want:
+            if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous {dt} of shape {shape} required")
+        _same_device((self.k, self.v, self.kscale, self.vscale), "cache")
+        self.n_pages, self.heads, self.page, self.head_dim = n, h, p, d
+        self._desc = KV8(n, h, d, p, CODE8[self.kind], 0, self.k.data_ptr(), self.v.data_ptr(),
+                         self.kscale.data_ptr(), self.vscale.data_ptr())
+
+    def desc(self) -> KV8:
+        return self._desc
+
+    @staticmethod
+    def empty(n_pages: int, heads: int, head_dim: int, page: int, kind: str, device) -> "DeviceKV8":
+        z = lambda dt, *s: torch.zeros(*s, dtype=dt, device=device)  # noqa: E731
+        return DeviceKV8(z(torch.uint8, n_pages, heads, page, head_dim),
+                         z(torch.uint8, n_pages, heads, head_dim, page),
+                         z(torch.float32, n_pages, heads), z(torch.float32, n_pages, heads), kind)
+
+
+def _same_device(ts, what: str) -> None:
+    if any(t.device != ts[0].device for t in ts):
+        raise ValueError(f"{what}: every tensor on one device required")
+
+
+def _matrix(t: torch.Tensor, what: str, rows: int | None, cols: int) -> None:
+    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D tensor of {cols} columns with unit stride required")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{what}: {t.shape[0]} rows, expected {rows}")
+
+
+def _ints(t: torch.Tensor, what: str, n: int) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 of {n} values required")
+
+
+def adapter_workspace(T: int, ad: DeviceAdapters, device) -> torch.Tensor:
+    """Workspace of dict_adapter_forward for up to T tokens."""
+    n = C.c_size_t(0)
+    _check("dict_adapter_workspace_size",
+           lib().dict_adapter_workspace_size(T, C.byref(ad.desc()), C.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def dict_adapter_forward(X, ad: DeviceAdapters, ids, base=None, Y=None, ydtype=torch.float16,
+                         ws=None, stream=None):
+    """Y[t] = base[t] + scale[a] (X[t] A_a^T) B_a^T with a = ids[t], and base[t]
+    where ids[t] names no adapter.  ``base`` None stands for zeros; ``Y`` may be
+    ``base`` (the adapters are added in place)."""
+    T = X.shape[0]
+    _matrix(X, "X", None, ad.d_in)
+    if Y is None:
+        Y = torch.empty(T, ad.d_out, dtype=ydtype, device=X.device)
+    _matrix(Y, "Y", T, ad.d_out)
+    _ints(ids, "ids", T)
+    if base is not None:
+        _matrix(base, "base", T, ad.d_out)
+        if base.dtype != Y.dtype:
+            raise TypeError("base and Y must have the same type")
+    _same_device((X, ad.A, ids, Y) if base is None else (X, ad.A, ids, Y, base), "adapters")
+    if ws is None:
+        ws = adapter_workspace(T, ad, X.device)
+    _check("dict_adapter_forward",
+           lib().dict_adapter_forward(X.data_ptr(), _dt(X), T, X.stride(0), C.byref(ad.desc()),
+                                      ids.data_ptr(), None if base is None else base.data_ptr(),
+                                      0 if base is None else base.stride(0), Y.data_ptr(), _dt(Y),
+                                      Y.stride(0), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return Y
+
+
+def _kv_batch(kv: DeviceKV8, tok_start, have, table) -> int:
+    n_req = have.shape[0]
+    _ints(have, "tokens per request", n_req)
+    _ints(tok_start, "tok_start", n_req + 1)
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_req or (
+            table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table: int32 of {n_req} rows with unit column stride required")
+    _same_device((kv.k, tok_start, have, table), "cache")
+    return n_req
+
+
+def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> None:
+    """Append the rows of K and V (heads * head_dim columns) to the cache, in
+    place: request r's rows are tok_start[r] .. tok_start[r+1]-1 and go to the
+    positions from cached[r] on, in the pages of table[r]."""
+    n_req = _kv_batch(kv, tok_start, cached, table)
+    _matrix(K, "K", None, kv.heads * kv.head_dim)
+    _matrix(V, "V", K.shape[0], kv.heads * kv.head_dim)
+    if K.dtype != V.dtype:
+        raise TypeError("K and V must have the same type")
+    _same_device((kv.k, K, V), "cache")
+    _check("kv8_append",
+           lib().kv8_append(C.byref(kv.desc()), n_req, K.shape[0], tok_start.data_ptr(),
+                            cached.data_ptr(), table.data_ptr(), table.stride(0), table.shape[1],
+                            K.data_ptr(), K.stride(0), V.data_ptr(), V.stride(0), _dt(K),
+                            _stream(stream)))
+
+
+def kv8_attention_workspace(kv: DeviceKV8, n_req: int, n_tok: int, q_heads: int,
+                            device) -> torch.Tensor:
+    """Workspace of kv8_attention, zeroed (its first part must be zero before
+    its first use)."""
+    n = C.c_size_t(0)
+    _check("kv8_attention_workspace_size",
+           lib().kv8_attention_workspace_size(C.byref(kv.desc()), n_req, n_tok, q_heads,
+                                              C.byref(n)))
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
+
+
+def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_scale=None,
+                  window: int = 0, sinks: int = 0, O=None, odtype=torch.float16, ws=None,
+                  stream=None):
+    """Causal attention of the rows of Q (q_heads * head_dim columns) over the
+    cache: request r's rows are the last of its length[r] tokens.  ``sm_scale``
+    None is 1/sqrt(head_dim); ``window`` 0 is no window.  Returns O."""
+    n_req = _kv_batch(kv, tok_start, length, table)
+    n_tok = Q.shape[0]
+    _matrix(Q, "Q", None, q_heads * kv.head_dim)
+    if Q.dtype != torch.float16:
+        raise TypeError("Q must be float16")
+    if O is None:
+        O = torch.empty(n_tok, q_heads * kv.head_dim, dtype=odtype, device=Q.device)
+    _matrix(O, "O", n_tok, q_heads * kv.head_dim)
+    _same_device((kv.k, Q, O), "cache")
+    if ws is None:
+        ws = kv8_attention_workspace(kv, n_req, n_tok, q_heads, Q.device)
+    _check("kv8_attention",
+           lib().kv8_attention(C.byref(kv.desc()), n_req, n_tok, tok_start.data_ptr(),
+                               length.data_ptr(), table.data_ptr(), table.stride(0),
+                               table.shape[1], Q.data_ptr(), Q.stride(0), q_heads,
+                               kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window,
+                               sinks, O.data_ptr(), _dt(O), O.stride(0), ws.data_ptr(),
+                               ws.numel(), _stream(stream)))
+    return O
 
 
 # ----------------------------------------------------------------- producer steps

@@ -5,9 +5,9 @@ then linked into ``dictionary_factored_sparse_amd/libdictfs.so``.  hipcc
 cross-compiles for gfx950 without a GPU.
 
 Flags: -O3, no fast-math, fp32 denormals kept, correctly rounded fp32
-division (hipcc's default), packed-fp32 instructions disabled.  The NVFP4
-encoder is compiled with -ffp-contract=off so that each step of its recipe
-is one rounded operation.
+division (hipcc's default), packed-fp32 instructions disabled.  The encoders
+(NVFP4, 8-bit coefficients, 8-bit cache) are compiled with -ffp-contract=off
+so that each step of their recipes is one rounded operation.
 """
 from __future__ import annotations
 
@@ -28,7 +28,8 @@ ARCH = os.environ.get("DFS_OFFLOAD_ARCH", "gfx950")
 COMMON = ["-std=c++17", "-O3", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,
           "-Wall", "-Wno-unused-function",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-PER_FILE = {"nvfp4.hip": ["-ffp-contract=off"], "quant8.hip": ["-ffp-contract=off"]}
+PER_FILE = {"nvfp4.hip": ["-ffp-contract=off"], "quant8.hip": ["-ffp-contract=off"],
+            "kv8_append.hip": ["-ffp-contract=off"]}
 
 
 def _hipcc() -> str:

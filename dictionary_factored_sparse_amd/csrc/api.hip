@@ -271,6 +271,50 @@ size_t refit_ws_bytes(int32_t d_in, int32_t k) {
   return spd_inverse_ws_bytes(k) + round256((size_t)k * k * 4) + round256((size_t)d_in * k * 4);
 }
 
+// ---- adapters and the 8-bit cache
+
+bool elem_aligned(const void* p, int32_t dt) { return (uintptr_t)p % esize(dt) == 0; }
+
+dfs_status check_adapters(const dfs_adapters* ad) {
+  if (!ad || ad->n <= 0 || ad->r_max <= 0 || ad->d_in <= 0 || ad->d_out <= 0)
+    return DFS_E_INVALID;
+  if (ad->r_max > kMaxAdapterRank) return DFS_E_RANGE;
+  if (!ad->A || !ad->B || !ad->rank || !ad->scale) return DFS_E_INVALID;
+  if (ad->lda < ad->d_in || ad->ldb < ad->r_max) return DFS_E_INVALID;
+  if (ad->stride_a < 0 || ad->stride_b < 0) return DFS_E_INVALID;
+  if (!aligned16(ad->A) || !aligned16(ad->B) || ad->lda % 8 != 0 || ad->ldb % 8 != 0 ||
+      ad->stride_a % 8 != 0 || ad->stride_b % 8 != 0)
+    return DFS_E_ALIGN;
+  if ((uintptr_t)ad->rank % 4 != 0 || (uintptr_t)ad->scale % 4 != 0) return DFS_E_ALIGN;
+  return DFS_OK;
+}
+
+dfs_status check_kv8(const dfs_kv8* kv) {
+  if (!kv || kv->n_pages <= 0 || kv->heads <= 0) return DFS_E_INVALID;
+  if (!is_code8(kv->dtype)) return DFS_E_UNSUPPORTED;
+  if (kv->head_dim != 64 && kv->head_dim != 96 && kv->head_dim != 128 && kv->head_dim != 256)
+    return DFS_E_UNSUPPORTED;
+  if (kv->page != 16 && kv->page != 32 && kv->page != 64 && kv->page != 128)
+    return DFS_E_UNSUPPORTED;
+  if (kv->heads > kMaxKvHeads) return DFS_E_RANGE;
+  if (!kv->k || !kv->v || !kv->kscale || !kv->vscale) return DFS_E_INVALID;
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return DFS_E_ALIGN;
+  if ((uintptr_t)kv->kscale % 4 != 0 || (uintptr_t)kv->vscale % 4 != 0) return DFS_E_ALIGN;
+  return DFS_OK;
+}
+
+dfs_status check_kv_batch(const dfs_kv8* kv, const KvBatch& b) {
+  if (b.n_req < 0 || b.n_tok < 0) return DFS_E_INVALID;
+  if (b.n_req > kMaxKvRequests) return DFS_E_RANGE;
+  if (b.n_req == 0 || b.n_tok == 0) return DFS_OK;
+  if (!b.tok_start || !b.have || !b.table) return DFS_E_INVALID;
+  if (b.table_pages <= 0 || b.ldt < b.table_pages) return DFS_E_INVALID;
+  if ((int64_t)b.table_pages * kv->page >= (int64_t)1 << 31) return DFS_E_RANGE;
+  if ((uintptr_t)b.tok_start % 4 != 0 || (uintptr_t)b.have % 4 != 0 || (uintptr_t)b.table % 4 != 0)
+    return DFS_E_ALIGN;
+  return DFS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -771,6 +815,102 @@ dfs_status dict_proj_forward(const void* X, int32_t xdt, int32_t T, int64_t ldx,
   const void* xs[1] = {X};
   void* ys[1] = {Y};
   return dict_group_forward(1, xs, xdt, T, ldx, D, C, ys, ydt, ldy, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ adapters
+
+dfs_status dict_adapter_workspace_size(int32_t T, const dfs_adapters* ad, size_t* bytes) {
+  if (!bytes || T < 0) return DFS_E_INVALID;
+  DFS_TRY(check_adapters(ad));
+  *bytes = adapter_ws_bytes(T, *ad);
+  return DFS_OK;
+}
+
+dfs_status dict_adapter_forward(const void* X, int32_t xdt, int32_t T, int64_t ldx,
+                                const dfs_adapters* ad, const int32_t* ids, const void* base,
+                                int64_t ldbase, void* Y, int32_t ydt, int64_t ldy, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (T < 0) return DFS_E_INVALID;
+  DFS_TRY(check_adapters(ad));
+  if (xdt != DFS_F16) return DFS_E_UNSUPPORTED;
+  DFS_TRY(check_x(&X, T > 0 ? 1 : 0, xdt, ldx, ad->d_in));
+  DFS_TRY(check_y(&Y, T > 0 ? 1 : 0, ydt, ldy, ad->d_out));
+  if (base) {
+    if (ldbase < ad->d_out) return DFS_E_INVALID;
+    if (!elem_aligned(base, ydt)) return DFS_E_ALIGN;
+    if (base == Y && ldbase != ldy) return DFS_E_INVALID;
+  }
+  if (T == 0) return DFS_OK;
+  if (!ids) return DFS_E_INVALID;
+  if ((uintptr_t)ids % 4 != 0) return DFS_E_ALIGN;
+  const size_t need = adapter_ws_bytes(T, *ad);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return DFS_E_WORKSPACE;
+    if (!aligned16(ws)) return DFS_E_ALIGN;
+  }
+  const AdapterLaunch a = {(const _Float16*)X, ldx, T, *ad, ids, base, ldbase, Y, ydt, ldy};
+  DFS_HIP(launch_adapter(a, ws, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+// ------------------------------------------------------------------ 8-bit cache
+
+dfs_status kv8_append(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int32_t* tok_start,
+                      const int32_t* cached, const int32_t* table, int64_t ldt,
+                      int32_t table_pages, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                      int32_t dtype, void* stream) {
+  DFS_TRY(check_kv8(kv));
+  const KvBatch b = {n_req, n_tok, tok_start, cached, table, ldt, table_pages};
+  DFS_TRY(check_kv_batch(kv, b));
+  if (!is_act_dtype(dtype)) return DFS_E_UNSUPPORTED;
+  const int64_t row = (int64_t)kv->heads * kv->head_dim;
+  if (ldk < row || ldv < row) return DFS_E_INVALID;
+  if (n_req == 0 || n_tok == 0) return DFS_OK;
+  if (!K || !V) return DFS_E_INVALID;
+  if (!elem_aligned(K, dtype) || !elem_aligned(V, dtype)) return DFS_E_ALIGN;
+  DFS_HIP(launch_kv8_append(*kv, b, K, ldk, V, ldv, dtype, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                        int32_t q_heads, size_t* bytes) {
+  if (!bytes || n_req < 0 || n_tok < 0) return DFS_E_INVALID;
+  DFS_TRY(check_kv8(kv));
+  if (n_req > kMaxKvRequests) return DFS_E_RANGE;
+  if (q_heads <= 0 || q_heads % kv->heads != 0) return DFS_E_INVALID;
+  if (q_heads > kMaxKvHeads) return DFS_E_RANGE;
+  *bytes = kv8_attention_ws_bytes(*kv, n_req, n_tok, q_heads);
+  return DFS_OK;
+}
+
+dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int32_t* tok_start,
+                         const int32_t* length, const int32_t* table, int64_t ldt,
+                         int32_t table_pages, const void* Q, int64_t ldq, int32_t q_heads,
+                         float sm_scale, int32_t window, int32_t sinks, void* O, int32_t odt,
+                         int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  DFS_TRY(check_kv8(kv));
+  const KvBatch b = {n_req, n_tok, tok_start, length, table, ldt, table_pages};
+  DFS_TRY(check_kv_batch(kv, b));
+  if (q_heads <= 0 || q_heads % kv->heads != 0) return DFS_E_INVALID;
+  if (q_heads > kMaxKvHeads) return DFS_E_RANGE;
+  if (!(sm_scale > 0.0f) || !(sm_scale < 3.0e38f)) return DFS_E_INVALID;
+  if (sinks < 0) return DFS_E_INVALID;
+  if (!is_act_dtype(odt)) return DFS_E_UNSUPPORTED;
+  const int64_t row = (int64_t)q_heads * kv->head_dim;
+  if (ldq < row || ldo < row) return DFS_E_INVALID;
+  if (ldq % 8 != 0) return DFS_E_ALIGN;
+  if (n_req == 0 || n_tok == 0) return DFS_OK;
+  if (!Q || !O) return DFS_E_INVALID;
+  if (!aligned16(Q) || !elem_aligned(O, odt)) return DFS_E_ALIGN;
+  const size_t need = kv8_attention_ws_bytes(*kv, n_req, n_tok, q_heads);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return DFS_E_WORKSPACE;
+    if (!aligned16(ws)) return DFS_E_ALIGN;
+  }
+  const KvAttnLaunch a = {*kv, b, (const _Float16*)Q, ldq, q_heads, sm_scale, window, sinks, O,
+                          odt, ldo};
+  DFS_HIP(launch_kv8_attention(a, ws, (hipStream_t)stream));
+  return DFS_OK;
 }
 
 }  // extern "C"

@@ -233,6 +233,52 @@ hipError_t launch_obs_prune(const float* C, int64_t ldc, const float* P, int64_t
 hipError_t launch_atoms_to_f32(const _Float16* D, int64_t ldd, int d_in, int k, float* out,
                                hipStream_t s);
 
+// Low-rank adapters of many requests beside a projection
+constexpr int kMaxAdapterRank = 256;
+struct AdapterLaunch {
+  const _Float16* X;
+  int64_t ldx;
+  int32_t T;
+  dfs_adapters ad;
+  const int32_t* ids;
+  const void* base;  // may be null (zeros) or Y
+  int64_t ldbase;
+  void* Y;
+  int32_t ydt;
+  int64_t ldy;
+};
+size_t adapter_ws_bytes(int32_t T, const dfs_adapters& ad);
+hipError_t launch_adapter(const AdapterLaunch& a, void* ws, hipStream_t s);
+
+constexpr int kMaxKvRequests = 65535;
+constexpr int kMaxKvHeads = 4096;
+// The rows of a batch and the page table of its requests, as the cache's
+// writer and reader take them.
+struct KvBatch {
+  int32_t n_req, n_tok;
+  const int32_t* tok_start;  // n_req + 1
+  const int32_t* have;       // tokens cached before (append), or in all (attention)
+  const int32_t* table;
+  int64_t ldt;
+  int32_t table_pages;
+};
+hipError_t launch_kv8_append(const dfs_kv8& kv, const KvBatch& b, const void* K, int64_t ldk,
+                             const void* V, int64_t ldv, int32_t dtype, hipStream_t s);
+struct KvAttnLaunch {
+  dfs_kv8 kv;
+  KvBatch b;
+  const _Float16* Q;
+  int64_t ldq;
+  int32_t q_heads;
+  float sm_scale;
+  int32_t window, sinks;
+  void* O;
+  int32_t odt;
+  int64_t ldo;
+};
+size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
+hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s);
+
 // NVFP4 packing
 size_t nvfp4_ws_bytes(int64_t n);
 hipError_t launch_nvfp4_amax(const float* x, int64_t n, void* ws, hipStream_t s);

@@ -357,6 +357,153 @@ dfs_status dict_zc_forward(int32_t n_layers, const void* Z, int32_t zdt, int32_t
                            void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Serving a layer: adapters, 8-bit key/value cache, attention             */
+/* ---------------------------------------------------------------------- */
+/* The operators next to the projections when a compressed layer is served:
+ * low-rank adapters of many requests beside a shared projection (the pages
+ * recover quality with such adapters), the cache that the k and v projections
+ * write, and the attention that reads it. */
+
+/* A pool of low-rank adapters over one projection (device pointers):
+ *   A: F16, adapter a, rank row i: d_in elements from element
+ *      a*stride_a + i*lda (r_max rows allocated per adapter, lda >= d_in);
+ *   B: F16, adapter a, output j: r_max elements from a*stride_b + j*ldb
+ *      (ldb >= r_max);
+ *   rank[n] int32, each in 0 .. r_max (values outside are clamped): the rows
+ *      of A and elements of B rows that adapter a uses; the rest may hold
+ *      anything, NaN included;
+ *   scale[n] fp32.
+ * 1 <= r_max <= 256.  A and B 16-byte aligned; lda, ldb, stride_a and
+ * stride_b multiples of 8 elements (DFS_E_ALIGN). */
+typedef struct {
+  int32_t n;
+  int32_t r_max;
+  int32_t d_in;
+  int32_t d_out;
+  const void* A;
+  int64_t lda;
+  int64_t stride_a;
+  const void* B;
+  int64_t ldb;
+  int64_t stride_b;
+  const int32_t* rank;
+  const float* scale;
+} dfs_adapters;
+
+/* Workspace bytes of dict_adapter_forward for T tokens.  Need not be zeroed. */
+dfs_status dict_adapter_workspace_size(int32_t T, const dfs_adapters* ad, size_t* bytes);
+
+/* Low-rank adapters of many requests beside a shared projection: for every
+ * token t with a = ids[t],
+ *   Y[t] = base[t] + scale[a] * ((X[t] A_a^T) B_a^T),
+ * and Y[t] = base[t] where a is outside 0 .. n-1 (no adapter).  base holds the
+ * projection's output (dict_proj_forward's Y, for instance); base == Y with
+ * the same leading dimension adds in place, base == NULL stands for zeros;
+ * any other overlap of base, X and Y is not allowed.
+ *   X: T x d_in row-major F16 (F32 gives DFS_E_UNSUPPORTED), ldx % 8 == 0,
+ *   16-byte aligned; base and Y: T x d_out, dtype ydt F16 or F32, aligned to
+ *   their element, any leading dimension >= d_out; ids[T] int32, device.
+ * Sums are fp32; X A^T is carried into the second product as the sum of two
+ * f16 values (22 bits), so the result is rounded once, to Y's type.
+ * T = 0 is a no-op.  Tokens of one adapter need not stand together. */
+dfs_status dict_adapter_forward(const void* X, int32_t xdt, int32_t T, int64_t ldx,
+                                const dfs_adapters* ad, const int32_t* ids, const void* base,
+                                int64_t ldbase, void* Y, int32_t ydt, int64_t ldy, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* A paged cache of keys and values in 8 bits, one fp32 scale per page (block
+ * of `page` tokens) and head, for keys and for values (device pointers):
+ *   k[n_pages][heads][page][head_dim] codes, kscale[n_pages][heads];
+ *   v[n_pages][heads][head_dim][page] codes, vscale[n_pages][heads].
+ * Entry = value(code) * scale, dtype DFS_FP8 (E4M3) or DFS_INT8 (two's
+ * complement).  Values are stored with the tokens of a page contiguous per
+ * dimension, so that the attention's second product reads its operand in the
+ * order in which the matrix instructions take it.
+ * head_dim is 64, 96, 128 or 256, page 16, 32, 64 or 128 (DFS_E_UNSUPPORTED
+ * otherwise); k and v 16-byte aligned.
+ * A request's tokens live in the pages that its row of a page table names:
+ * table[r*ldt + i] (int32, device) holds positions i*page .. i*page+page-1 of
+ * request r; table_pages entries per row are read at most (ldt >= table_pages,
+ * table_pages * page < 2^31).  An entry outside 0 .. n_pages-1 is no page:
+ * nothing is stored there and nothing read. */
+typedef struct {
+  int32_t n_pages;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t page;
+  int32_t dtype;
+  int32_t _pad;
+  uint8_t* k;
+  uint8_t* v;
+  float* kscale;
+  float* vscale;
+} dfs_kv8;
+
+/* Append new keys and values to the cache: request r's new tokens are rows
+ * tok_start[r] .. tok_start[r+1]-1 of K and V (tok_start[n_req+1] int32,
+ * device, non-decreasing; values are clamped to 0 .. n_tok) and take the
+ * positions cached[r], cached[r]+1, ... (cached[n_req] int32, device: the
+ * tokens that request r has in the cache; negative counts as 0).
+ *   K, V: n_tok rows of heads * head_dim elements (head after head, as a
+ *   projection writes them), dtype F16 or F32, leading dimensions ldk, ldv,
+ *   aligned to their element.
+ * For each page and head that gets tokens, for keys and values alike, each
+ * step one correctly rounded fp32 operation:
+ *   need = max |new values| / 448 (FP8) or / 127 (INT8);
+ *   old = the stored scale if the page already holds tokens of the request
+ *         (positions < cached[r]), else 0;
+ *   scale = max(need, old);
+ *   if need > old, codes of tokens already there become the code nearest to
+ *   (value(code) * old) / scale; a new value's code is the nearest to
+ *   value / scale (0 where scale is 0), ties to even, at most 448 or 127 in
+ *   size.
+ * A NaN counts as 0 and values beyond +-65504 (infinities too) as +-65504, so
+ * that one bad value cannot spoil the scale that its page's tokens share.
+ * Slots past the new tokens keep what they hold.  Two requests of one call
+ * must not both write the same page. */
+dfs_status kv8_append(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int32_t* tok_start,
+                      const int32_t* cached, const int32_t* table, int64_t ldt,
+                      int32_t table_pages, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                      int32_t dtype, void* stream);
+
+/* Workspace bytes of kv8_attention for n_req requests with n_tok query tokens
+ * in all. */
+dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                        int32_t q_heads, size_t* bytes);
+
+/* Causal attention of new tokens over the cache (which holds their keys and
+ * values already: kv8_append comes first).  Request r has length[r] tokens in
+ * the cache (int32, device); its n = tok_start[r+1] - tok_start[r] query
+ * tokens are the last n of them: row tok_start[r] + i stands at position
+ * p = length[r] - n + i.  A key at position j < length[r] is visible to it if
+ *   j <= p and (window <= 0 or p - j < window or j < sinks):
+ * a sliding window of `window` tokens (the query's own included) with the
+ * first `sinks` tokens of the request always visible; pages that no query
+ * sees are not read.  For query head h and kv head h / (q_heads / heads):
+ *   O[row, h] = sum_j softmax_j(q . k_j * sm_scale) v_j
+ * over the visible keys, and 0 where none is visible.
+ *   Q: n_tok rows of q_heads * head_dim F16 elements (head after head),
+ *   16-byte aligned, ldq % 8 == 0; O: n_tok rows of q_heads * head_dim, dtype
+ *   F16 or F32, aligned to its element, ldo >= q_heads * head_dim;
+ *   q_heads % heads == 0.  tok_start as for kv8_append; rows of O that belong
+ *   to no request are not written.  length below 0 counts as 0, and positions
+ *   from table_pages * page on hold no key.
+ * Scores, softmax statistics and sums are fp32.  The softmax weights enter
+ * the second product as f16 for F16 output (their rounding is below that of
+ * the output) and as the sum of two f16 values for F32 output.  Non-finite
+ * cache contents outside the visible positions do not reach the output.
+ * The workspace's first 64 KiB must be zero before its first use; every call
+ * leaves them zero again.  Calls sharing a workspace must not run
+ * concurrently.  Work is split over the keys by lengths read on the device,
+ * so a captured call follows later lengths; results do not change from run to
+ * run. */
+dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int32_t* tok_start,
+                         const int32_t* length, const int32_t* table, int64_t ldt,
+                         int32_t table_pages, const void* Q, int64_t ldq, int32_t q_heads,
+                         float sm_scale, int32_t window, int32_t sinks, void* O, int32_t odt,
+                         int64_t ldo, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Producer steps (offline, fp32)                                          */
 /* ---------------------------------------------------------------------- */
 /* The steps that produce D_g and C_l ("DictLLM: Shared Dictionaries for
