@@ -1,89 +1,769 @@
-// kv8_attention.hip -- attention over the 8-bit paged cache, with a sliding
-// window and first tokens that stay visible.  One wave per query token and
-// head, 64 keys at a time: one pass with the running maximum and sum of the
-// softmax.
+// kv8_attention.hip -- attention of new tokens over the 8-bit paged cache,
+// with a sliding window and first tokens that stay visible.
+//
+// For query row q of a kv head: o = sum_j w_j v_j / sum_j w_j with
+// w_j = 2^(t_j - m), t_j = (q . code_j) kscale_j sm_scale log2(e), m the
+// running maximum of t: one pass over the keys.
+//
+// Layout of the products.  A wave takes 64 keys and NQ groups of 16 query
+// rows (a row is one query token of one query head; the heads that share a kv
+// head, and the tokens of a request, are rows of the same item, so a cached
+// byte is read once for all of them).  Both products are
+// v_mfma_f32_16x16x32_f16 on transposed operands, S^T = K Q^T and
+// O^T = V^T W^T, so that the codes come from memory straight into the A
+// operand in 16-byte loads and the softmax weights pass from the first
+// product's result to the second one's B operand in their own lanes:
+//   - K row of A row x in key group mm: key 16 (x / 4) + 4 mm + x % 4.  Then
+//     lane (r = lane % 16, q = lane / 16) of S^T holds, for query row r, the
+//     keys 16 q .. 16 q + 15: mm and the accumulator index count them.
+//   - the second product takes k slots q * 8 + e as keys 16 q + 8 kk + e,
+//     which is what that lane holds, and V^T rows are dims whose 16 keys
+//     16 q .. are contiguous in a page (dfs_kv8 stores values so).
+// Codes become f16 exactly (every E4M3 and int8 value is an f16 value); the
+// page scales multiply the fp32 scores, and for values they enter the weights:
+// w' = w * vscale / 2^E <= 2^15, E the running maximum of the exponents of
+// vscale, an exact power of two in which the sums are kept.
+//
+// Rounding.  w' is rounded to f16 for the second product: relative 2^-12,
+// below the f16 output's own rounding; for fp32 output it enters as the sum of
+// two f16 values.  Weights are kept at 2^13 times their value so that f16's
+// normal range reaches 2^-27 of the largest, and m is raised only when a score
+// passes it by more than 2 (weights stay below 2^15), which spares most
+// rescales of the sums.
+//
+// Work split.  The tiles of 64 keys of all items (request, block of query
+// rows, kv head) form one line, cut into equal slices, one per workgroup: the
+// lengths are read on the device, and a batch of uneven lengths or a single
+// long request loads every CU alike.  An item that lies in several slices is
+// joined by the workgroup that finishes last, in slice order, so results do
+// not depend on which that is.
+#include <algorithm>
+
 #include "dfs_internal.hpp"
 
 namespace dfs {
 namespace {
 
-template <int KIND>
-__device__ __forceinline__ float decode8(uint8_t c) {
-  if constexpr (KIND == DFS_FP8) return e4m3_to_f32(c);
-  return (float)(int8_t)c;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kTile = 64;                // keys per tile
+constexpr int kInlinePlan = 256;         // entries up to which every workgroup plans for itself
+constexpr int kCounterBytes = 65536;     // per-slice counters at the start of the workspace
+constexpr float kWeightBits = 13.0f;     // weights are held at 2^13 times their value
+constexpr float kSlack = 2.0f;           // the running maximum may lag by this (log2)
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttnWs {
+  uint32_t* count;   // per slice: parts of the item that starts in it that are done
+  int64_t* first;    // plan: first tile of each entry, then the total
+  int32_t* req;      // plan: request of each entry
+  int32_t* qblk;     // plan: its block of query rows
+  int32_t* n_entries;
+  int32_t max_entries;
+  float* part_o;     // [2 * slices][rows][D]
+  float* part_ml;    // [2 * slices][rows][2]
+};
+
+// A request's rows in the batch, clamped to what the arrays hold.
+struct Req {
+  int t0, n, len, keys;
+};
+__device__ __forceinline__ Req get_req(const KvBatch& b, int page, int r) {
+  Req q;
+  q.t0 = min(max(b.tok_start[r], 0), b.n_tok);
+  q.n = min(max(b.tok_start[r + 1], q.t0), b.n_tok) - q.t0;
+  q.len = max(b.have[r], 0);
+  q.keys = min(q.len, b.table_pages * page);
+  return q;
 }
 
-template <int KIND, typename OT>
-__global__ __launch_bounds__(kWave) void attn_kernel(KvAttnLaunch a) {
-  const dfs_kv8& kv = a.kv;
-  const KvBatch& b = a.b;
-  const int P = kv.page, D = kv.head_dim, row = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-  const int kh = h / (a.q_heads / kv.heads);
-  __shared__ float q[256];
-  int r = 0;
-  for (; r < b.n_req; ++r)
-    if (row >= b.tok_start[r] && row < b.tok_start[r + 1]) break;
-  if (r == b.n_req) return;
-  const int n = min(b.tok_start[r + 1], b.n_tok) - max(b.tok_start[r], 0);
-  const int64_t len = max(b.have[r], 0), pos = len - n + (row - max(b.tok_start[r], 0));
-  const int64_t keys = min(len, (int64_t)b.table_pages * P);
-  for (int d = lane; d < D; d += kWave)
-    q[d] = (float)a.Q[row * a.ldq + (int64_t)h * D + d] * a.sm_scale;
+// Tiles that some row of an entry sees: the first `ns` tiles hold first
+// tokens, the others run from tile `ta`.
+struct Span {
+  int ns, ta, n;
+  __device__ __forceinline__ int tile(int u) const { return u < ns ? u : u - ns + ta; }
+};
+__device__ __forceinline__ Span get_span(const Req& q, int p0, int p1, int window, int sinks) {
+  Span s;
+  const int hi = min(p1, q.keys - 1);                                // last visible key
+  const int lo = window > 0 && p0 >= window ? p0 - window + 1 : 0;   // first one of the window
+  const int sk = min(sinks, hi + 1);
+  s.ta = lo / kTile;
+  s.ns = sk > 0 ? min((sk - 1) / kTile + 1, s.ta) : 0;
+  s.n = s.ns + (hi >= lo ? hi / kTile - s.ta + 1 : 0);
+  if (s.n <= 0) s = {0, 0, 1};  // rows that see nothing still get their zeros
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* tmp, T* total, int threads) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const T y = __shfl_up(x, o, kWave);
+    if (lane >= o) x += y;
+  }
+  if (lane == kWave - 1) tmp[wave] = x;
   __syncthreads();
-  float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
-  for (int64_t j0 = 0; j0 < keys; j0 += kWave) {
-    const int64_t j = j0 + lane;
-    bool seen = j < keys && j <= pos && (a.window <= 0 || pos - j < a.window || j < a.sinks);
-    int pg = -1;
-    if (seen) pg = b.table[r * b.ldt + j / P];
-    seen = pg >= 0 && pg < kv.n_pages;
-    if (__ballot(seen) == 0) continue;
-    float s = -INFINITY, vs = 0.0f;
-    const int64_t ph = (int64_t)pg * kv.heads + kh;
-    if (seen) {
-      const uint8_t* k = kv.k + (ph * P + j % P) * D;
-      s = 0.0f;
-      for (int d = 0; d < D; ++d) s += q[d] * decode8<KIND>(k[d]);
-      s *= kv.kscale[ph];
-      vs = kv.vscale[ph];
+  T base = 0, sum = 0;
+  for (int w = 0; w < threads / kWave; ++w) {
+    if (w < wave) base += tmp[w];
+    sum += tmp[w];
+  }
+  __syncthreads();
+  *total = sum;
+  return base + x - v;  // exclusive
+}
+
+// Entries (request, block of qb query rows) in order and the first tile of
+// each, by one workgroup; first[entries] is the total.  Returns the entries:
+// at most `most`, which a tok_start that is not ascending could pass.
+template <typename T>  // of the entry counts: 256 requests of at most 256 entries fit int
+__device__ int make_plan(const KvAttnLaunch& a, int qb, int most, int64_t* first, int32_t* req,
+                         int32_t* qblk, int64_t* tmp, int threads) {
+  const int g = a.q_heads / a.kv.heads;
+  int n_entries = 0;
+  for (int r0 = 0; r0 < a.b.n_req; r0 += threads) {
+    const int r = r0 + (int)threadIdx.x;
+    int nb = 0;
+    if (r < a.b.n_req)
+      nb = (int)min<int64_t>(((int64_t)get_req(a.b, a.kv.page, r).n * g + qb - 1) / qb, most);
+    T total;
+    const T at = n_entries + block_scan<T>(nb, (T*)tmp, &total, threads);
+    for (int i = 0; i < nb && at + i < most; ++i) {
+      req[at + i] = r;
+      qblk[at + i] = i;
     }
-    float mx = s;
-    for (int x = 32; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x, kWave));
-    const float mn = fmaxf(m, mx), alpha = expf(m - mn);
-    const float p = seen ? expf(s - mn) : 0.0f;
-    m = mn;
-    l = l * alpha + wave_sum(p);
-    for (int i = 0; i < 4; ++i) o[i] *= alpha;
-    const float pv = p * vs;
-    for (int x = 0; x < kWave; ++x) {
-      const float w = __shfl(pv, x, kWave);
-      const int64_t pj = __shfl((int)seen, x, kWave) ? __shfl(ph, x, kWave) : -1;
-      if (pj < 0) continue;
-      for (int i = 0; i < 4; ++i)
-        if (lane + i * kWave < D)
-          o[i] += w * decode8<KIND>(kv.v[(pj * D + lane + i * kWave) * P + (j0 + x) % P]);
+    n_entries = (int)min<T>(n_entries + total, most);
+  }
+  __syncthreads();
+  int64_t base = 0;
+  for (int e0 = 0; e0 < n_entries; e0 += threads) {
+    const int e = e0 + (int)threadIdx.x;
+    int64_t t = 0;
+    if (e < n_entries) {
+      const Req q = get_req(a.b, a.kv.page, req[e]);
+      const int i0 = (int)((int64_t)qblk[e] * qb / g);
+      const int i1 = (int)min<int64_t>(((int64_t)(qblk[e] + 1) * qb - 1) / g, q.n - 1);
+      t = (int64_t)get_span(q, q.len - q.n + i0, q.len - q.n + i1, a.window, a.sinks).n *
+          a.kv.heads;
+    }
+    int64_t total;
+    const int64_t at = base + block_scan<int64_t>(t, tmp, &total, threads);
+    if (e < n_entries) first[e] = at;
+    base += total;
+  }
+  if (threadIdx.x == 0) first[n_entries] = base;
+  __syncthreads();
+  return n_entries;
+}
+
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvAttnLaunch a, AttnWs w, int qb) {
+  __shared__ int64_t tmp[kPlanThreads / kWave];
+  const int n = make_plan<int64_t>(a, qb, w.max_entries, w.first, w.req, w.qblk, tmp, kPlanThreads);
+  if (threadIdx.x == 0) *w.n_entries = n;
+}
+
+// Eight codes to f16, exactly.
+template <int KIND>
+__device__ __forceinline__ h8 codes_h8(uint32_t lo, uint32_t hi) {
+  h8 v;
+  if constexpr (KIND == DFS_FP8) {
+    const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    v = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+  } else {
+    // byte b ^ 0x80 = b + 128 under the exponent of 1024: 1152 + b, exactly
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
+    u4 w;
+    w.x = __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u);
+    w.y = __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u);
+    w.z = __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u);
+    w.w = __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u);
+    v = __builtin_bit_cast(h8, w) - (_Float16)1152.0f;
+  }
+  return v;
+}
+
+// Maximum and sum over the four lanes that hold one query row (lane % 16).
+__device__ __forceinline__ float max4(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum4(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ int max4i(int v) {
+  auto a = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = max((int)a[0], (int)a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  return max((int)b[0], (int)b[1]);
+}
+
+// SPLIT: the waves of a workgroup take the tiles of an item in turn, all for
+// the same NQ * 16 query rows (few rows, long caches).  Otherwise each wave
+// has NQ * 16 rows of its own and all take every tile (prompts).
+// HILO: the weights enter the second product as two f16 values.
+template <int KIND, int D, int NQ, bool SPLIT, bool HILO>
+struct Attn {
+  static constexpr int kRows = 16 * NQ;                      // per wave
+  static constexpr int kQb = SPLIT ? kRows : kRows * kWaves;  // per item
+  static constexpr int kSteps = D / 32;                      // first product, per key group
+  static constexpr int kDims = D / 16;                       // 16-dim groups of the second
+  static constexpr int kWide = D / 64;                       // 16-byte pieces of a lane's K row
+
+  struct Shared {
+    union {
+      float o[SPLIT ? kRows * D : 1];
+      int64_t tmp[kWaves];
+    };
+    float m[kWaves][kRows], l[kWaves][kRows];
+    int e[kWaves];
+    int last;
+    int64_t first[kInlinePlan + 1];
+    int32_t req[kInlinePlan], qblk[kInlinePlan];
+  };
+
+  // one wave's state
+  h8 qf[NQ][kSteps];
+  f4 o[NQ][kDims];
+  float m[NQ], l[NQ];
+  int ev;  // sums are in units of 2^ev (and 2^13)
+  uint32_t kraw[4][D / 16];
+  float ks, vs;
+  int pk, pv;  // page of this lane's K rows and of its key block
+
+  const KvAttnLaunch& a;
+  const int lane, wave, r16, q4;
+  Req rq;
+  Span sp;
+  int kh, row0, nrows;      // this wave's first row of the request, its rows (may be <= 0)
+  int pos[NQ], pmin, pmax;  // positions of the rows
+  const int32_t* tab;
+
+  __device__ __forceinline__ Attn(const KvAttnLaunch& a_)
+      : a(a_), lane(threadIdx.x % kWave), wave(threadIdx.x / kWave), r16(lane & 15),
+        q4(lane >> 4) {}
+
+  __device__ __forceinline__ void load_pages(int u) {
+    const int kb = sp.tile(u) * kTile;
+    const int sh = __builtin_ctz(a.kv.page);
+    const int last = a.b.table_pages - 1;
+    pk = tab[min((kb + 16 * (r16 >> 2)) >> sh, last)];
+    pv = tab[min((kb + 16 * q4) >> sh, last)];
+  }
+  // A page that is none is read as page 0 and masked.
+  __device__ __forceinline__ bool valid(int pg) const { return pg >= 0 && pg < a.kv.n_pages; }
+
+  __device__ __forceinline__ void load_k(int u) {
+    const int kb = sp.tile(u) * kTile;
+    const int P = a.kv.page;
+    const int pg = valid(pk) ? pk : 0;
+    const uint8_t* base =
+        a.kv.k + (((int64_t)pg * a.kv.heads + kh) * P + ((kb + 16 * (r16 >> 2)) & (P - 1)) +
+                  (r16 & 3)) * D + q4 * 16;
+#pragma unroll
+    for (int mm = 0; mm < 4; ++mm) {
+      const uint8_t* p = base + 4 * mm * D;
+#pragma unroll
+      for (int c = 0; c < kWide; ++c) {
+        const u4 w = ld16<u4>(p + 64 * c);
+        kraw[mm][4 * c] = w.x;
+        kraw[mm][4 * c + 1] = w.y;
+        kraw[mm][4 * c + 2] = w.z;
+        kraw[mm][4 * c + 3] = w.w;
+      }
+      if constexpr (D % 64 != 0) {
+        const u2 w = *gptr((const u2*)(p + 64 * kWide - 8 * q4));
+        kraw[mm][4 * kWide] = w.x;
+        kraw[mm][4 * kWide + 1] = w.y;
+      }
+    }
+    const int64_t ph = (int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh;
+    ks = a.kv.kscale[ph];
+    vs = a.kv.vscale[ph];
+  }
+
+  __device__ __forceinline__ void begin(int req, int qblk, int kh_) {
+    const int g = a.q_heads / a.kv.heads;
+    kh = kh_;
+    rq = get_req(a.b, a.kv.page, req);
+    tab = a.b.table + (int64_t)req * a.b.ldt;
+    const int rows = rq.n * g;  // < 2^31: n_tok rows of q_heads * head_dim elements exist
+    const int item0 = qblk * kQb, item1 = min(item0 + kQb, rows);
+    row0 = item0 + (SPLIT ? 0 : wave * kRows);
+    nrows = min(item1 - row0, kRows);
+    const int pos0 = rq.len - rq.n;
+    sp = get_span(rq, pos0 + item0 / g, pos0 + (item1 - 1) / g, a.window, a.sinks);
+    pmin = pos0 + min(row0, item1 - 1) / g;
+    pmax = pos0 + (min(row0 + kRows, item1) - 1) / g;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      // rows past the end repeat the last one and are not written
+      const int row = min(row0 + 16 * i + r16, item1 - 1);
+      const int tok = row / g, h = kh * g + row - tok * g;
+      pos[i] = pos0 + tok;
+      const _Float16* qp = a.Q + (int64_t)(rq.t0 + tok) * a.ldq + (int64_t)h * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = s < 2 * kWide ? (s >> 1) * 64 + q4 * 16 + (s & 1) * 8 : 64 * kWide + q4 * 8;
+        qf[i][s] = ld16<h8>(qp + d);
+      }
+      m[i] = -1e30f;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[i][d] = f4{0, 0, 0, 0};
+    }
+    ev = -126;
+  }
+
+  // Which of this lane's 16 keys some row of the wave sees.
+  __device__ __forceinline__ uint32_t seen_by_any(int kb) const {
+    uint32_t bits = 0;
+    const int hi = min(pmax, rq.keys - 1);
+    for (int x = 0; x < 16; ++x) {
+      const int j = kb + 16 * q4 + x;
+      const bool see = j <= hi && (a.window <= 0 || j > pmin || pmin - j < a.window || j < a.sinks);
+      bits |= (see ? 1u : 0u) << x;
+    }
+    return valid(pv) ? bits : 0u;
+  }
+
+  // The tile whose K codes are in kraw.  `next`: the tile to load meanwhile,
+  // or -1.
+  __device__ __forceinline__ void tile(int u, int next, int after) {
+    const int kb = sp.tile(u) * kTile;
+    const int P = a.kv.page;
+    u4 vraw[kDims];
+    {
+      const uint8_t* base =
+          a.kv.v + (((int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh) * D + r16) * P +
+          ((kb + 16 * q4) & (P - 1));
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) vraw[d] = ld16<u4>(base + d * 16 * P);
+    }
+    f4 s[NQ][4];
+#pragma unroll
+    for (int mm = 0; mm < 4; ++mm) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) s[i][mm] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const h8 kf = codes_h8<KIND>(kraw[mm][2 * st], kraw[mm][2 * st + 1]);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+          s[i][mm] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][st], s[i][mm], 0, 0, 0);
+      }
+    }
+    float kscale = ks * (a.sm_scale * kLog2e), vscale = vs;
+    const bool plain = kb + kTile - 1 <= pmin && kb + kTile <= rq.keys &&
+                       (a.window <= 0 || pmax - kb < a.window || kb + kTile <= a.sinks) &&
+                       __ballot(!valid(pv)) == 0;
+    uint32_t any = 0xFFFFu;
+    if (!plain) {
+      any = seen_by_any(kb);
+      if (any == 0) vscale = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int j = kb + 16 * q4 + x;
+          const bool see = (any >> x & 1u) && j <= pos[i] &&
+                           (a.window <= 0 || pos[i] - j < a.window || j < a.sinks);
+          s[i][x >> 2][x & 3] = see ? s[i][x >> 2][x & 3] * kscale : -INFINITY;
+        }
+      }
+      kscale = 1.0f;
+      if constexpr (KIND == DFS_FP8) {
+        // codes of keys that nobody sees may be NaN: make them 0
+        u4 keep;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t b = any >> (4 * w);
+          keep[w] = (b & 1u ? 0xFFu : 0u) | (b & 2u ? 0xFF00u : 0u) | (b & 4u ? 0xFF0000u : 0u) |
+                    (b & 8u ? 0xFF000000u : 0u);
+        }
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
+      }
+    }
+    if (next >= 0) {
+      load_k_next(next, after);
+    }
+    // value scales as (mantissa part) * 2^(ev): exact
+    const int e_here = max4i(vscale > 0.0f ? __builtin_amdgcn_frexp_expf(vscale) : -126);
+    const int e_new = max(ev, e_here);
+    float grow = __builtin_amdgcn_ldexpf(1.0f, max(ev - e_new, -300));
+    const float vf = __builtin_amdgcn_ldexpf(vscale, -e_new);
+    bool rescale = e_new != ev;
+    ev = e_new;
+    h8 w[NQ][2], wl[NQ][2];
+    float alpha[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float mx = s[i][0][0];
+#pragma unroll
+      for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[i][x >> 2][x & 3]);
+      mx = max4(mx * kscale);
+      const bool up = mx > m[i] + kSlack;
+      alpha[i] = grow;
+      if (up) {
+        const float f = __builtin_amdgcn_exp2f(m[i] - mx);
+        l[i] *= f;
+        alpha[i] *= f;
+        m[i] = mx;
+      }
+      rescale = rescale || up;
+      const float ref = m[i] - kWeightBits;
+      float sum = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x >> 2][x & 3], kscale, -ref));
+        sum += p;
+        s[i][x >> 2][x & 3] = p * vf;
+      }
+      l[i] += sum;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int x = 0; x < 8; x += 2) {
+          const f2 p = {s[i][2 * h + (x >> 2)][x & 3], s[i][2 * h + (x >> 2)][(x & 3) + 1]};
+          const h2 hi = __builtin_convertvector(p, h2);
+          w[i][h][x] = hi.x;
+          w[i][h][x + 1] = hi.y;
+          if constexpr (HILO) {
+            const f2 rest = {p.x - (float)hi.x, p.y - (float)hi.y};
+            const h2 lo = __builtin_convertvector(rest, h2);
+            wl[i][h][x] = lo.x;
+            wl[i][h][x + 1] = lo.y;
+          }
+        }
+      }
+    }
+    if (__ballot(rescale) != 0) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) o[i][d] *= alpha[i];
+    }
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      const h8 v0 = codes_h8<KIND>(vraw[d].x, vraw[d].y);
+      const h8 v1 = codes_h8<KIND>(vraw[d].z, vraw[d].w);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[i][0], o[i][d], 0, 0, 0);
+        o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[i][1], o[i][d], 0, 0, 0);
+        if constexpr (HILO) {
+          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[i][0], o[i][d], 0, 0, 0);
+          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[i][1], o[i][d], 0, 0, 0);
+        }
+      }
     }
   }
-  for (int i = 0; i < 4; ++i)
-    if (lane + i * kWave < D)
-      ((OT*)a.O)[row * a.ldo + (int64_t)h * D + lane + i * kWave] =
-          (OT)(l > 0.0f ? o[i] / l : 0.0f);
+
+  int pk2, pv2;  // pages of the tile after the one that is loaded next
+  __device__ __forceinline__ void load_k_next(int next, int after) {
+    pk = pk2;
+    pv = pv2;
+    load_k(next);
+    if (after >= 0) {
+      const int a0 = pk, a1 = pv;
+      load_pages(after);
+      pk2 = pk;
+      pv2 = pv;
+      pk = a0;
+      pv = a1;
+    }
+  }
+
+  // tiles u0, u0 + step, ... below u1
+  __device__ __forceinline__ void tiles(int u0, int u1, int step) {
+    if (u0 >= u1) return;
+    if (u0 + step < u1) {
+      load_pages(u0 + step);
+      pk2 = pk;
+      pv2 = pv;
+    }
+    load_pages(u0);
+    load_k(u0);
+    for (int u = u0; u < u1; u += step)
+      tile(u, u + step < u1 ? u + step : -1, u + 2 * step < u1 ? u + 2 * step : -1);
+  }
+
+  // One row's destination.
+  __device__ __forceinline__ int64_t out_at(int row) const {
+    const int g = a.q_heads / a.kv.heads;
+    const int tok = row / g, h = kh * g + row - tok * g;
+    return (int64_t)(rq.t0 + tok) * a.ldo + (int64_t)h * D;
+  }
+  __device__ __forceinline__ void store(int64_t at, float v) const {
+    if (a.odt == DFS_F16)
+      ((_Float16*)a.O)[at] = (_Float16)v;
+    else
+      ((float*)a.O)[at] = v;
+  }
+};
+
+template <int KIND, int D, int NQ, bool SPLIT, bool HILO>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(KvAttnLaunch a, AttnWs ws,
+                                                                         int least, int slices,
+                                                                         int inline_plan) {
+  using A = Attn<KIND, D, NQ, SPLIT, HILO>;
+  __shared__ typename A::Shared sh;
+  A t(a);
+  const int64_t* first = sh.first;
+  const int32_t *req = sh.req, *qblk = sh.qblk;
+  int n_entries;
+  if (inline_plan) {
+    n_entries = make_plan<int>(a, A::kQb, ws.max_entries, sh.first, sh.req, sh.qblk, sh.tmp, kThreads);
+  } else {
+    first = ws.first;
+    req = ws.req;
+    qblk = ws.qblk;
+    n_entries = *ws.n_entries;
+  }
+  if (n_entries == 0) return;
+  const int64_t total = first[n_entries];
+  const int64_t per = max((int64_t)least, (total + slices - 1) / slices);
+  const int64_t xs = blockIdx.x * per, xe = min(xs + per, total);
+  if (xs >= total) return;
+  int e = 0;  // the entry with first[e] <= xs < first[e + 1]
+  for (int n = n_entries; n > 1;) {
+    const int half = n / 2;
+    if (first[e + half] <= xs) {
+      e += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  for (int64_t x = xs; x < xe;) {
+    while (first[e + 1] <= x) ++e;
+    const int64_t in = x - first[e];
+    const int n_tiles = (int)((first[e + 1] - first[e]) / a.kv.heads);
+    const int kh = (int)(in / n_tiles);
+    const int64_t item0 = first[e] + (int64_t)kh * n_tiles, item1 = item0 + n_tiles;
+    const int u0 = (int)(x - item0), u1 = (int)(min(item1, xe) - item0);
+    x = item0 + u1;
+    t.begin(req[e], qblk[e], kh);
+    if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
+    else if (t.nrows > 0) t.tiles(u0, u1, 1);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) t.l[i] = sum4(t.l[i]);
+    const bool whole = u0 == 0 && u1 == n_tiles;
+    // a slice has at most two items that are not whole: its first and its last
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0);
+    const int rows = min(A::kQb, t.rq.n * (a.q_heads / a.kv.heads) - qblk[e] * A::kQb);
+    if constexpr (SPLIT) {
+      // join the waves: weights of each row and wave, then the sums in turn
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+        if (t.q4 == 0) {
+          sh.m[t.wave][16 * i + t.r16] = t.m[i];
+          sh.l[t.wave][16 * i + t.r16] = t.l[i];
+        }
+      if (t.lane == 0) sh.e[t.wave] = t.ev;
+      __syncthreads();
+      int ev = sh.e[0];
+      for (int w = 1; w < kWaves; ++w) ev = max(ev, sh.e[w]);
+      float f[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        float mm = sh.m[0][16 * i + t.r16];
+        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][16 * i + t.r16]);
+        f[i] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(t.m[i] - mm), max(t.ev - ev, -300));
+      }
+      for (int w = 0; w < kWaves; ++w) {
+        if (t.wave == w) {
+#pragma unroll
+          for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int d = 0; d < A::kDims; ++d) {
+              f4* p = (f4*)&sh.o[(16 * i + t.r16) * D + d * 16 + t.q4 * 4];
+              const f4 v = t.o[i][d] * f[i];
+              *p = w == 0 ? v : *p + v;
+            }
+        }
+        __syncthreads();
+      }
+      for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+        const int row = idx / (D / 4), d = idx % (D / 4) * 4;
+        float mm = sh.m[0][row];
+        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][row]);
+        float l = 0.0f;
+        for (int w = 0; w < kWaves; ++w) l += sh.l[w][row] * __builtin_amdgcn_exp2f(sh.m[w][row] - mm);
+        f4 v = *(f4*)&sh.o[row * D + d];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = __builtin_amdgcn_ldexpf(v[c], ev);
+        if (whole) {
+          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+          const int64_t at = t.out_at(t.row0 + row) + d;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t.store(at + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
+        } else {
+          *(f4*)&ws.part_o[(slot * A::kQb + row) * D + d] = v;
+          if (d == 0) {
+            ws.part_ml[(slot * A::kQb + row) * 2] = mm;
+            ws.part_ml[(slot * A::kQb + row) * 2 + 1] = l;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int row = 16 * i + t.r16;
+        if (row < t.nrows) {
+          const float l = t.l[i], inv = l > 0.0f ? 1.0f / l : 0.0f;
+          const int64_t at = whole ? t.out_at(t.row0 + row) : 0;
+          const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
+#pragma unroll
+          for (int d = 0; d < A::kDims; ++d) {
+            f4 v = t.o[i][d];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = __builtin_amdgcn_ldexpf(v[c], t.ev);
+            if (whole) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                t.store(at + d * 16 + t.q4 * 4 + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
+            } else {
+              *(f4*)&ws.part_o[pr * D + d * 16 + t.q4 * 4] = v;
+            }
+          }
+          if (!whole && t.q4 == 0) {
+            ws.part_ml[pr * 2] = t.m[i];
+            ws.part_ml[pr * 2 + 1] = l;
+          }
+        }
+      }
+    }
+    if (!whole) {
+      // the last of the item's slices to come here joins them, in order
+      const int w0 = (int)(item0 / per), w1 = (int)((item1 - 1) / per);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        __threadfence();
+        const uint32_t before = atomicAdd(&ws.count[w0], 1u);
+        sh.last = before == (uint32_t)(w1 - w0);
+        if (sh.last) atomicExch(&ws.count[w0], 0u);
+        __threadfence();
+      }
+      __syncthreads();
+      if (sh.last) {
+        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+          const int row = idx / (D / 4), d = idx % (D / 4) * 4;
+          // the item starts in slice w0 as that slice's last item, and is the
+          // first one of the others
+          float mm = -INFINITY;
+          for (int w = w0; w <= w1; ++w)
+            mm = fmaxf(mm, ws.part_ml[((2 * (int64_t)w + (w == w0)) * A::kQb + row) * 2]);
+          float l = 0.0f;
+          f4 v = {0, 0, 0, 0};
+          for (int w = w0; w <= w1; ++w) {
+            const int64_t pr = (2 * (int64_t)w + (w == w0)) * A::kQb + row;
+            const float f = __builtin_amdgcn_exp2f(ws.part_ml[pr * 2] - mm);
+            l += ws.part_ml[pr * 2 + 1] * f;
+            v += *(const f4*)&ws.part_o[pr * D + d] * f;
+          }
+          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+          // row of the request: the item's rows start at its block
+          const int64_t at = t.out_at(qblk[e] * A::kQb + row) + d;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t.store(at + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// How a call is cut: query rows per item, workgroups, entries at most.
+struct Cut {
+  bool split;
+  int nq, qb;
+  int slices;
+  int64_t entries;
+};
+Cut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
+  Cut c;
+  const int64_t g = q_heads / kv.heads;
+  const double rows = (double)n_tok * g / std::max(n_req, 1);  // rows of a request, on average
+  c.split = rows <= 32;
+  c.nq = c.split && rows <= 16 ? 1 : 2;
+  c.qb = c.split ? 16 * c.nq : 16 * c.nq * kWaves;
+  c.entries = std::min<int64_t>(n_req, n_tok) + (int64_t)n_tok * g / c.qb;
+  c.slices = kv.head_dim == 256 ? 256 : 512;
+  return c;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t first, req, qblk, n, part_ml, part_o, total;
+};
+Layout get_layout(const Cut& c, int D) {
+  Layout l;
+  l.first = kCounterBytes;
+  l.req = l.first + up((c.entries + 1) * 8);
+  l.qblk = l.req + up(c.entries * 4);
+  l.n = l.qblk + up(c.entries * 4);
+  l.part_ml = l.n + 256;
+  l.part_o = l.part_ml + up((size_t)2 * c.slices * c.qb * 8);
+  l.total = l.part_o + (size_t)2 * c.slices * c.qb * D * 4;
+  return l;
+}
+
+template <int KIND, int D, int NQ, bool SPLIT>
+void go(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
+  const int in = c.entries <= kInlinePlan && a.b.n_req <= kInlinePlan;
+  if (!in) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w, c.qb);
+  const int least = SPLIT ? kWaves : 1;
+  if (a.odt == DFS_F32)
+    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, true>), dim3(c.slices), dim3(kThreads), 0,
+                       s, a, w, least, c.slices, in);
+  else
+    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, false>), dim3(c.slices), dim3(kThreads), 0,
+                       s, a, w, least, c.slices, in);
+}
+template <int KIND, int D>
+void go_d(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
+  if (!c.split) go<KIND, D, 2, false>(a, w, c, s);
+  else if (c.nq == 1) go<KIND, D, 1, true>(a, w, c, s);
+  else go<KIND, D, 2, true>(a, w, c, s);
+}
+template <int KIND>
+void go_kind(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
+  if (a.kv.head_dim == 64) go_d<KIND, 64>(a, w, c, s);
+  else if (a.kv.head_dim == 96) go_d<KIND, 96>(a, w, c, s);
+  else if (a.kv.head_dim == 128) go_d<KIND, 128>(a, w, c, s);
+  else go_d<KIND, 256>(a, w, c, s);
 }
 
 }  // namespace
 
-size_t kv8_attention_ws_bytes(const dfs_kv8&, int32_t, int32_t, int32_t) { return 65536; }
+size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
+  return get_layout(get_cut(kv, n_req, n_tok, q_heads), kv.head_dim).total;
+}
 
-hipError_t launch_kv8_attention(const KvAttnLaunch& a, void*, hipStream_t s) {
-  const dim3 grid(a.b.n_tok, a.q_heads);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kWave), 0, s, a); };
-  if (a.odt == DFS_F16) {
-    if (a.kv.dtype == DFS_FP8) go(attn_kernel<DFS_FP8, _Float16>);
-    else go(attn_kernel<DFS_INT8, _Float16>);
-  } else {
-    if (a.kv.dtype == DFS_FP8) go(attn_kernel<DFS_FP8, float>);
-    else go(attn_kernel<DFS_INT8, float>);
-  }
+hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s) {
+  const Cut c = get_cut(a.kv, a.b.n_req, a.b.n_tok, a.q_heads);
+  const Layout l = get_layout(c, a.kv.head_dim);
+  char* p = (char*)ws;
+  const AttnWs w = {(uint32_t*)p,          (int64_t*)(p + l.first), (int32_t*)(p + l.req),
+                    (int32_t*)(p + l.qblk), (int32_t*)(p + l.n),     (int32_t)c.entries,
+                    (float*)(p + l.part_o), (float*)(p + l.part_ml)};
+  if (a.kv.dtype == DFS_FP8) go_kind<DFS_FP8>(a, w, c, s);
+  else go_kind<DFS_INT8>(a, w, c, s);
   return hipGetLastError();
 }
 
