@@ -38,6 +38,7 @@
 // joined by the workgroup that finishes last, in slice order, so results do
 // not depend on which that is.
 #include <algorithm>
+#include <type_traits>
 
 #include "dfs_internal.hpp"
 
@@ -54,14 +55,15 @@ constexpr float kSlack = 2.0f;           // the running maximum may lag by this 
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttnWs {
-  uint32_t* count;   // per slice: parts of the item that starts in it that are done
+  uint32_t* count;   // [3 * slices]: parts of a group that are done, groups of an item
   int64_t* first;    // plan: first tile of each entry, then the total
   int32_t* req;      // plan: request of each entry
   int32_t* qblk;     // plan: its block of query rows
   int32_t* n_entries;
   int32_t max_entries;
   float* part_o;     // [2 * slices][rows][D]
-  float* part_ml;    // [2 * slices][rows][2]
+  f2* part_ml;       // [2 * slices][rows]: reference of the weights, their sum
+  f2* group_ml;      // the same of a group of slices, at its first slice's slot
 };
 
 // A request's rows in the batch, clamped to what the arrays hold.
@@ -190,6 +192,80 @@ __device__ __forceinline__ h8 codes_h8(uint32_t lo, uint32_t hi) {
   return v;
 }
 
+// Parts of an item pass between workgroups of different XCDs, whose L2s are
+// not coherent for plain accesses: they are written and read by accesses of
+// device scope, which do not stay in an L2, so no cache has to be written back
+// or invalidated (a fence of device scope does both: measured below).  A part
+// counts as done when its stores have completed (stores_done, then the
+// barrier, then the counter).
+__device__ __forceinline__ void put2(f2* p, f2 v) {
+  __hip_atomic_store((uint64_t*)p, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f2 get2(const f2* p) {
+  return __builtin_bit_cast(f2, __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void put4(float* p, f4 v) {
+  put2((f2*)p, f2{v.x, v.y});
+  put2((f2*)p + 1, f2{v.z, v.w});
+}
+__device__ __forceinline__ f4 get4(const float* p) {
+  const f2 a = get2((const f2*)p), b = get2((const f2*)p + 1);
+  return f4{a.x, a.y, b.x, b.y};
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Called by a whole workgroup after its stores: whether it is the last of n.
+// That one leaves the counter zero.
+__device__ __forceinline__ bool arrive(uint32_t* count, int n, int* last) {
+  stores_done();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+            (uint32_t)(n - 1);
+    if (*last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *last != 0;
+}
+
+// Sums v of four dims of a row over n parts, and the reference of their
+// weights with the sum of these; several parts' loads are in flight at once.
+constexpr int kJoin = 8;
+template <int D, typename F>
+__device__ __forceinline__ f2 join(const f2* ml, const float* o, int rows, int row, int d, int n,
+                                   F slot, f4& v) {
+  float mm = -INFINITY, l = 0.0f;
+  v = f4{0, 0, 0, 0};
+  for (int b = 0; b < n; b += kJoin) {
+    f2 pm[kJoin];
+    f4 po[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      const int64_t pr = slot(min(b + i, n - 1)) * rows + row;
+      pm[i] = get2(ml + pr);
+      po[i] = get4(o + pr * D + d);
+    }
+    float mb = mm;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) mb = fmaxf(mb, pm[i].x);
+    const float old = __builtin_amdgcn_exp2f(mm - mb);
+    l *= old;
+    v *= old;
+    mm = mb;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      const float f = b + i < n ? __builtin_amdgcn_exp2f(pm[i].x - mb) : 0.0f;
+      l += pm[i].y * f;
+      v += po[i] * f;
+    }
+  }
+  return f2{mm, l};
+}
+
 // Maximum and sum over the four lanes that hold one query row (lane % 16).
 __device__ __forceinline__ float max4(float v) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -224,7 +300,7 @@ struct Attn {
 
   struct Shared {
     union {
-      float o[SPLIT ? kRows * D : 1];
+      float o[SPLIT ? kWaves * kRows * D : 1];  // each wave's sums
       int64_t tmp[kWaves];
     };
     float m[kWaves][kRows], l[kWaves][kRows];
@@ -239,9 +315,12 @@ struct Attn {
   f4 o[NQ][kDims];
   float m[NQ], l[NQ];
   int ev;  // sums are in units of 2^ev (and 2^13)
-  uint32_t kraw[4][D / 16];
-  float ks, vs;
-  int pk, pv;  // page of this lane's K rows and of its key block
+  uint32_t kraw[4][D / 16];  // K codes of the tile to come
+  float ks, vs;              // and the scales of this lane's key block in it
+  // pages of a tile: of this lane's K rows, and of its key block
+  struct Pages {
+    int k, v;
+  } pg0, pg1;  // of that tile, and of the one after it
 
   const KvAttnLaunch& a;
   const int lane, wave, r16, q4;
@@ -255,23 +334,26 @@ struct Attn {
       : a(a_), lane(threadIdx.x % kWave), wave(threadIdx.x / kWave), r16(lane & 15),
         q4(lane >> 4) {}
 
-  __device__ __forceinline__ void load_pages(int u) {
+  __device__ __forceinline__ Pages load_pages(int u) const {
     const int kb = sp.tile(u) * kTile;
     const int sh = __builtin_ctz(a.kv.page);
     const int last = a.b.table_pages - 1;
-    pk = tab[min((kb + 16 * (r16 >> 2)) >> sh, last)];
-    pv = tab[min((kb + 16 * q4) >> sh, last)];
+    return {*gptr(tab + min((kb + 16 * (r16 >> 2)) >> sh, last)),
+            *gptr(tab + min((kb + 16 * q4) >> sh, last))};
   }
   // A page that is none is read as page 0 and masked.
   __device__ __forceinline__ bool valid(int pg) const { return pg >= 0 && pg < a.kv.n_pages; }
 
-  __device__ __forceinline__ void load_k(int u) {
+  // K codes and the scales of tile u; if there is none (!real) every lane
+  // reads the same bytes at the start of the cache, which costs nothing.
+  __device__ __forceinline__ void load_k(int u, bool real) {
     const int kb = sp.tile(u) * kTile;
     const int P = a.kv.page;
-    const int pg = valid(pk) ? pk : 0;
-    const uint8_t* base =
-        a.kv.k + (((int64_t)pg * a.kv.heads + kh) * P + ((kb + 16 * (r16 >> 2)) & (P - 1)) +
-                  (r16 & 3)) * D + q4 * 16;
+    const int pg = valid(pg0.k) ? pg0.k : 0;
+    const int64_t at = (((int64_t)pg * a.kv.heads + kh) * P + ((kb + 16 * (r16 >> 2)) & (P - 1)) +
+                        (r16 & 3)) * D + q4 * 16;
+    const uint8_t* base = a.kv.k + (real ? at : 0);
+    const int q8 = real ? 8 * q4 : 0;
 #pragma unroll
     for (int mm = 0; mm < 4; ++mm) {
       const uint8_t* p = base + 4 * mm * D;
@@ -284,14 +366,14 @@ struct Attn {
         kraw[mm][4 * c + 3] = w.w;
       }
       if constexpr (D % 64 != 0) {
-        const u2 w = *gptr((const u2*)(p + 64 * kWide - 8 * q4));
+        const u2 w = *gptr((const u2*)(p + 64 * kWide - q8));
         kraw[mm][4 * kWide] = w.x;
         kraw[mm][4 * kWide + 1] = w.y;
       }
     }
-    const int64_t ph = (int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh;
-    ks = a.kv.kscale[ph];
-    vs = a.kv.vscale[ph];
+    const int64_t ph = (int64_t)(valid(pg0.v) ? pg0.v : 0) * a.kv.heads + kh;
+    ks = *gptr(a.kv.kscale + ph);
+    vs = *gptr(a.kv.vscale + ph);
   }
 
   __device__ __forceinline__ void begin(int req, int qblk, int kh_) {
@@ -327,23 +409,27 @@ struct Attn {
     ev = -126;
   }
 
-  // Which of this lane's 16 keys some row of the wave sees.
-  __device__ __forceinline__ uint32_t seen_by_any(int kb) const {
-    uint32_t bits = 0;
-    const int hi = min(pmax, rq.keys - 1);
-    for (int x = 0; x < 16; ++x) {
-      const int j = kb + 16 * q4 + x;
-      const bool see = j <= hi && (a.window <= 0 || j > pmin || pmin - j < a.window || j < a.sinks);
-      bits |= (see ? 1u : 0u) << x;
-    }
-    return valid(pv) ? bits : 0u;
+  // Bits of this lane's 16 keys, from j0 on, that lie below key `end`.
+  static __device__ __forceinline__ uint32_t below(int end, int j0) {
+    return (1u << min(max(end - j0, 0), 16)) - 1u;
+  }
+  // Bits of the keys from j0 on that a row whose window starts at `low` and
+  // whose keys end before `high` sees.
+  __device__ __forceinline__ uint32_t seen(int low, int high, int j0) const {
+    return below(high, j0) & (~below(low, j0) | below(a.sinks, j0));
+  }
+  // First key of the window of a row at position p.
+  __device__ __forceinline__ int window_low(int p) const {
+    return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
   }
 
-  // The tile whose K codes are in kraw.  `next`: the tile to load meanwhile,
-  // or -1.
-  __device__ __forceinline__ void tile(int u, int next, int after) {
+  // Tile u, whose K codes are in kraw.  The tile `next` is loaded meanwhile,
+  // and the pages of the tile `after`.  The loads are in the order in which
+  // they are waited for, with no branch around them: a wait then leaves the
+  // later ones in flight.
+  __device__ __forceinline__ void tile(int u, int next, int after, bool more) {
     const int kb = sp.tile(u) * kTile;
-    const int P = a.kv.page;
+    const int P = a.kv.page, pv = pg0.v;
     u4 vraw[kDims];
     {
       const uint8_t* base =
@@ -366,39 +452,35 @@ struct Attn {
       }
     }
     float kscale = ks * (a.sm_scale * kLog2e), vscale = vs;
+    pg0 = pg1;
+    load_k(next, more);
+    pg1 = load_pages(after);
     const bool plain = kb + kTile - 1 <= pmin && kb + kTile <= rq.keys &&
                        (a.window <= 0 || pmax - kb < a.window || kb + kTile <= a.sinks) &&
                        __ballot(!valid(pv)) == 0;
-    uint32_t any = 0xFFFFu;
     if (!plain) {
-      any = seen_by_any(kb);
+      const int j0 = kb + 16 * q4;
+      // what some row of the wave sees
+      const uint32_t any =
+          valid(pv) ? seen(window_low(pmin), min(pmax + 1, rq.keys), j0) : 0u;
       if (any == 0) vscale = 0.0f;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
+        const uint32_t see = any & seen(window_low(pos[i]), pos[i] + 1, j0);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int j = kb + 16 * q4 + x;
-          const bool see = (any >> x & 1u) && j <= pos[i] &&
-                           (a.window <= 0 || pos[i] - j < a.window || j < a.sinks);
-          s[i][x >> 2][x & 3] = see ? s[i][x >> 2][x & 3] * kscale : -INFINITY;
-        }
+        for (int x = 0; x < 16; ++x)
+          s[i][x >> 2][x & 3] = see >> x & 1u ? s[i][x >> 2][x & 3] * kscale : -INFINITY;
       }
       kscale = 1.0f;
       if constexpr (KIND == DFS_FP8) {
         // codes of keys that nobody sees may be NaN: make them 0
         u4 keep;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t b = any >> (4 * w);
-          keep[w] = (b & 1u ? 0xFFu : 0u) | (b & 2u ? 0xFF00u : 0u) | (b & 4u ? 0xFF0000u : 0u) |
-                    (b & 8u ? 0xFF000000u : 0u);
-        }
+        for (int w = 0; w < 4; ++w)
+          keep[w] = ((any >> (4 * w) & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
 #pragma unroll
         for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
       }
-    }
-    if (next >= 0) {
-      load_k_next(next, after);
     }
     // value scales as (mantissa part) * 2^(ev): exact
     const int e_here = max4i(vscale > 0.0f ? __builtin_amdgcn_frexp_expf(vscale) : -126);
@@ -472,33 +554,15 @@ struct Attn {
     }
   }
 
-  int pk2, pv2;  // pages of the tile after the one that is loaded next
-  __device__ __forceinline__ void load_k_next(int next, int after) {
-    pk = pk2;
-    pv = pv2;
-    load_k(next);
-    if (after >= 0) {
-      const int a0 = pk, a1 = pv;
-      load_pages(after);
-      pk2 = pk;
-      pv2 = pv;
-      pk = a0;
-      pv = a1;
-    }
-  }
-
   // tiles u0, u0 + step, ... below u1
   __device__ __forceinline__ void tiles(int u0, int u1, int step) {
     if (u0 >= u1) return;
-    if (u0 + step < u1) {
-      load_pages(u0 + step);
-      pk2 = pk;
-      pv2 = pv;
-    }
-    load_pages(u0);
-    load_k(u0);
-    for (int u = u0; u < u1; u += step)
-      tile(u, u + step < u1 ? u + step : -1, u + 2 * step < u1 ? u + 2 * step : -1);
+    const int last = u0 + (u1 - 1 - u0) / step * step;
+    pg0 = load_pages(u0);
+    pg1 = load_pages(min(u0 + step, last));
+    load_k(u0, true);
+    for (int u = u0; u <= last; u += step)
+      tile(u, min(u + step, last), min(u + 2 * step, last), u < last);
   }
 
   // One row's destination.
@@ -507,56 +571,51 @@ struct Attn {
     const int tok = row / g, h = kh * g + row - tok * g;
     return (int64_t)(rq.t0 + tok) * a.ldo + (int64_t)h * D;
   }
-  __device__ __forceinline__ void store(int64_t at, float v) const {
-    if (a.odt == DFS_F16)
-      ((_Float16*)a.O)[at] = (_Float16)v;
-    else
-      ((float*)a.O)[at] = v;
+  __device__ __forceinline__ void store(int64_t at, const f4& v, float l) const {
+    using T = typename std::conditional<HILO, float, _Float16>::type;
+    // rows that see nothing are 0; a sum that is NaN stays so
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *gptr_w((T*)a.O + at + c) = (T)(v[c] * inv);
   }
 };
 
 template <int KIND, int D, int NQ, bool SPLIT, bool HILO>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(KvAttnLaunch a, AttnWs ws,
-                                                                         int least, int slices,
-                                                                         int inline_plan) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_plan) {
   using A = Attn<KIND, D, NQ, SPLIT, HILO>;
   __shared__ typename A::Shared sh;
   A t(a);
-  const int64_t* first = sh.first;
-  const int32_t *req = sh.req, *qblk = sh.qblk;
-  int n_entries;
-  if (inline_plan) {
-    n_entries = make_plan<int>(a, A::kQb, ws.max_entries, sh.first, sh.req, sh.qblk, sh.tmp, kThreads);
-  } else {
-    first = ws.first;
-    req = ws.req;
-    qblk = ws.qblk;
-    n_entries = *ws.n_entries;
-  }
+  const int n_entries =
+      inline_plan ? make_plan<int>(a, A::kQb, ws.max_entries, sh.first, sh.req, sh.qblk, sh.tmp,
+                                   kThreads)
+                  : *gptr(ws.n_entries);
+  auto first = [&](int e) { return inline_plan ? sh.first[e] : *gptr(ws.first + e); };
   if (n_entries == 0) return;
-  const int64_t total = first[n_entries];
+  const int64_t total = first(n_entries);
   const int64_t per = max((int64_t)least, (total + slices - 1) / slices);
   const int64_t xs = blockIdx.x * per, xe = min(xs + per, total);
   if (xs >= total) return;
-  int e = 0;  // the entry with first[e] <= xs < first[e + 1]
+  // the entry e with first(e) <= xs < first(e + 1)
+  int e = 0;
   for (int n = n_entries; n > 1;) {
-    const int half = n / 2;
-    if (first[e + half] <= xs) {
-      e += half;
-      n -= half;
-    } else {
-      n = half;
-    }
+    const int stride = (n + kThreads - 1) / kThreads;
+    const int at = (int)threadIdx.x * stride;
+    const int below = __syncthreads_count(at < n && first(e + at) <= xs);
+    e += (below - 1) * stride;
+    n = min(stride, n_entries - e);
   }
   for (int64_t x = xs; x < xe;) {
-    while (first[e + 1] <= x) ++e;
-    const int64_t in = x - first[e];
-    const int n_tiles = (int)((first[e + 1] - first[e]) / a.kv.heads);
-    const int kh = (int)(in / n_tiles);
-    const int64_t item0 = first[e] + (int64_t)kh * n_tiles, item1 = item0 + n_tiles;
+    while (first(e + 1) <= x) ++e;
+    const int64_t fe = first(e);
+    const int n_tiles = (int)((first(e + 1) - fe) / a.kv.heads);
+    const int kh = (int)((x - fe) / n_tiles);
+    const int64_t item0 = fe + (int64_t)kh * n_tiles, item1 = item0 + n_tiles;
+    const int req = inline_plan ? sh.req[e] : *gptr(ws.req + e);
+    const int qblk = inline_plan ? sh.qblk[e] : *gptr(ws.qblk + e);
     const int u0 = (int)(x - item0), u1 = (int)(min(item1, xe) - item0);
     x = item0 + u1;
-    t.begin(req[e], qblk[e], kh);
+    t.begin(req, qblk, kh);
     if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
     else if (t.nrows > 0) t.tiles(u0, u1, 1);
 #pragma unroll
@@ -564,59 +623,42 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(KvAttn
     const bool whole = u0 == 0 && u1 == n_tiles;
     // a slice has at most two items that are not whole: its first and its last
     const int64_t slot = 2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0);
-    const int rows = min(A::kQb, t.rq.n * (a.q_heads / a.kv.heads) - qblk[e] * A::kQb);
+    const int rows = min(A::kQb, t.rq.n * (a.q_heads / a.kv.heads) - qblk * A::kQb);
     if constexpr (SPLIT) {
-      // join the waves: weights of each row and wave, then the sums in turn
-#pragma unroll
-      for (int i = 0; i < NQ; ++i)
-        if (t.q4 == 0) {
-          sh.m[t.wave][16 * i + t.r16] = t.m[i];
-          sh.l[t.wave][16 * i + t.r16] = t.l[i];
-        }
-      if (t.lane == 0) sh.e[t.wave] = t.ev;
-      __syncthreads();
-      int ev = sh.e[0];
-      for (int w = 1; w < kWaves; ++w) ev = max(ev, sh.e[w]);
-      float f[NQ];
+      // join the waves
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        float mm = sh.m[0][16 * i + t.r16];
-        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][16 * i + t.r16]);
-        f[i] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(t.m[i] - mm), max(t.ev - ev, -300));
-      }
-      for (int w = 0; w < kWaves; ++w) {
-        if (t.wave == w) {
+        const int row = 16 * i + t.r16;
+        if (row < rows) {
+          if (t.q4 == 0) {
+            sh.m[t.wave][row] = t.m[i];
+            sh.l[t.wave][row] = t.l[i];
+          }
 #pragma unroll
-          for (int i = 0; i < NQ; ++i)
-#pragma unroll
-            for (int d = 0; d < A::kDims; ++d) {
-              f4* p = (f4*)&sh.o[(16 * i + t.r16) * D + d * 16 + t.q4 * 4];
-              const f4 v = t.o[i][d] * f[i];
-              *p = w == 0 ? v : *p + v;
-            }
+          for (int d = 0; d < A::kDims; ++d)
+            *(f4*)&sh.o[(t.wave * A::kRows + row) * D + d * 16 + t.q4 * 4] = t.o[i][d];
         }
-        __syncthreads();
       }
+      if (t.lane == 0) sh.e[t.wave] = t.ev;
+      __syncthreads();
       for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
         const int row = idx / (D / 4), d = idx % (D / 4) * 4;
         float mm = sh.m[0][row];
+#pragma unroll
         for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][row]);
         float l = 0.0f;
-        for (int w = 0; w < kWaves; ++w) l += sh.l[w][row] * __builtin_amdgcn_exp2f(sh.m[w][row] - mm);
-        f4 v = *(f4*)&sh.o[row * D + d];
+        f4 v = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = __builtin_amdgcn_ldexpf(v[c], ev);
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - mm);
+          l += sh.l[w][row] * f;
+          v += *(f4*)&sh.o[(w * A::kRows + row) * D + d] * __builtin_amdgcn_ldexpf(f, sh.e[w]);
+        }
         if (whole) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          const int64_t at = t.out_at(t.row0 + row) + d;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) t.store(at + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
+          t.store(t.out_at(t.row0 + row) + d, v, l);
         } else {
-          *(f4*)&ws.part_o[(slot * A::kQb + row) * D + d] = v;
-          if (d == 0) {
-            ws.part_ml[(slot * A::kQb + row) * 2] = mm;
-            ws.part_ml[(slot * A::kQb + row) * 2 + 1] = l;
-          }
+          put4(&ws.part_o[(slot * A::kQb + row) * D + d], v);
+          if (d == 0) put2(&ws.part_ml[slot * A::kQb + row], f2{mm, l});
         }
       }
     } else {
@@ -624,7 +666,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(KvAttn
       for (int i = 0; i < NQ; ++i) {
         const int row = 16 * i + t.r16;
         if (row < t.nrows) {
-          const float l = t.l[i], inv = l > 0.0f ? 1.0f / l : 0.0f;
           const int64_t at = whole ? t.out_at(t.row0 + row) : 0;
           const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
 #pragma unroll
@@ -632,54 +673,46 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(KvAttn
             f4 v = t.o[i][d];
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[c] = __builtin_amdgcn_ldexpf(v[c], t.ev);
-            if (whole) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                t.store(at + d * 16 + t.q4 * 4 + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
-            } else {
-              *(f4*)&ws.part_o[pr * D + d * 16 + t.q4 * 4] = v;
-            }
+            if (whole) t.store(at + d * 16 + t.q4 * 4, v, t.l[i]);
+            else put4(&ws.part_o[pr * D + d * 16 + t.q4 * 4], v);
           }
-          if (!whole && t.q4 == 0) {
-            ws.part_ml[pr * 2] = t.m[i];
-            ws.part_ml[pr * 2 + 1] = l;
-          }
+          if (!whole && t.q4 == 0) put2(&ws.part_ml[pr], f2{t.m[i], t.l[i]});
         }
       }
     }
     if (!whole) {
-      // the last of the item's slices to come here joins them, in order
+      // The parts of an item are joined in groups of kJoin slices, each by the
+      // slice of the group that comes last, then the groups' results by the
+      // group that comes last: always in slice order.
       const int w0 = (int)(item0 / per), w1 = (int)((item1 - 1) / per);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const uint32_t before = atomicAdd(&ws.count[w0], 1u);
-        sh.last = before == (uint32_t)(w1 - w0);
-        if (sh.last) atomicExch(&ws.count[w0], 0u);
-        __threadfence();
-      }
-      __syncthreads();
-      if (sh.last) {
+      const int me = (int)blockIdx.x - w0;
+      const int groups = (w1 - w0) / kJoin + 1, grp = me / kJoin;
+      const int g0 = w0 + grp * kJoin, g1 = min(g0 + kJoin - 1, w1);
+      // the item starts in slice w0 as that slice's last item (slot 1), and is
+      // the first one of the others
+      auto slot_of = [&](int w) { return 2 * (int64_t)w + (w == w0); };
+      if (arrive(&ws.count[slot_of(g0)], g1 - g0 + 1, &sh.last)) {
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
           const int row = idx / (D / 4), d = idx % (D / 4) * 4;
-          // the item starts in slice w0 as that slice's last item, and is the
-          // first one of the others
-          float mm = -INFINITY;
-          for (int w = w0; w <= w1; ++w)
-            mm = fmaxf(mm, ws.part_ml[((2 * (int64_t)w + (w == w0)) * A::kQb + row) * 2]);
-          float l = 0.0f;
-          f4 v = {0, 0, 0, 0};
-          for (int w = w0; w <= w1; ++w) {
-            const int64_t pr = (2 * (int64_t)w + (w == w0)) * A::kQb + row;
-            const float f = __builtin_amdgcn_exp2f(ws.part_ml[pr * 2] - mm);
-            l += ws.part_ml[pr * 2 + 1] * f;
-            v += *(const f4*)&ws.part_o[pr * D + d] * f;
+          f4 v;
+          const f2 ml = join<D>(ws.part_ml, ws.part_o, A::kQb, row, d, g1 - g0 + 1,
+                                [&](int i) { return slot_of(g0 + i); }, v);
+          if (groups == 1) {
+            t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
+          } else {
+            const int64_t pr = slot_of(g0) * A::kQb + row;
+            put4(ws.part_o + pr * D + d, v);
+            if (d == 0) put2(ws.group_ml + pr, ml);
           }
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          // row of the request: the item's rows start at its block
-          const int64_t at = t.out_at(qblk[e] * A::kQb + row) + d;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) t.store(at + c, l > 0.0f ? v[c] * inv : (l == l ? 0.0f : l));
+        }
+        if (groups > 1 && arrive(&ws.count[2 * gridDim.x + w0], groups, &sh.last)) {
+          for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+            const int row = idx / (D / 4), d = idx % (D / 4) * 4;
+            f4 v;
+            const f2 ml = join<D>(ws.group_ml, ws.part_o, A::kQb, row, d, groups,
+                                  [&](int i) { return slot_of(w0 + i * kJoin); }, v);
+            t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
+          }
         }
       }
     }
@@ -700,8 +733,10 @@ Cut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
   const double rows = (double)n_tok * g / std::max(n_req, 1);  // rows of a request, on average
   c.split = rows <= 32;
   c.nq = c.split && rows <= 16 ? 1 : 2;
-  c.qb = c.split ? 16 * c.nq : 16 * c.nq * kWaves;
+  c.qb = c.split ? 16 * c.nq : 16 * c.nq * 4;
   c.entries = std::min<int64_t>(n_req, n_tok) + (int64_t)n_tok * g / c.qb;
+  // as many workgroups as the device holds at once: two per CU, one where a
+  // wave needs more than half of a SIMD's registers
   c.slices = kv.head_dim == 256 ? 256 : 512;
   return c;
 }
@@ -709,7 +744,7 @@ Cut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t first, req, qblk, n, part_ml, part_o, total;
+  size_t first, req, qblk, n, part_ml, group_ml, part_o, total;
 };
 Layout get_layout(const Cut& c, int D) {
   Layout l;
@@ -718,7 +753,8 @@ Layout get_layout(const Cut& c, int D) {
   l.qblk = l.req + up(c.entries * 4);
   l.n = l.qblk + up(c.entries * 4);
   l.part_ml = l.n + 256;
-  l.part_o = l.part_ml + up((size_t)2 * c.slices * c.qb * 8);
+  l.group_ml = l.part_ml + up((size_t)2 * c.slices * c.qb * 8);
+  l.part_o = l.group_ml + up((size_t)2 * c.slices * c.qb * 8);
   l.total = l.part_o + (size_t)2 * c.slices * c.qb * D * 4;
   return l;
 }
@@ -727,13 +763,15 @@ template <int KIND, int D, int NQ, bool SPLIT>
 void go(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
   const int in = c.entries <= kInlinePlan && a.b.n_req <= kInlinePlan;
   if (!in) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w, c.qb);
+  using A = Attn<KIND, D, NQ, SPLIT, false>;
+  static_assert(A::kQb == (SPLIT ? 16 * NQ : 64 * NQ), "get_cut");
   const int least = SPLIT ? kWaves : 1;
   if (a.odt == DFS_F32)
-    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, true>), dim3(c.slices), dim3(kThreads), 0,
-                       s, a, w, least, c.slices, in);
+    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, true>), dim3(c.slices), dim3(kThreads),
+                       0, s, a, w, least, c.slices, in);
   else
-    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, false>), dim3(c.slices), dim3(kThreads), 0,
-                       s, a, w, least, c.slices, in);
+    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, false>), dim3(c.slices), dim3(kThreads),
+                       0, s, a, w, least, c.slices, in);
 }
 template <int KIND, int D>
 void go_d(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
@@ -761,7 +799,8 @@ hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s) 
   char* p = (char*)ws;
   const AttnWs w = {(uint32_t*)p,          (int64_t*)(p + l.first), (int32_t*)(p + l.req),
                     (int32_t*)(p + l.qblk), (int32_t*)(p + l.n),     (int32_t)c.entries,
-                    (float*)(p + l.part_o), (float*)(p + l.part_ml)};
+                    (float*)(p + l.part_o), (f2*)(p + l.part_ml),
+                    (f2*)(p + l.group_ml)};
   if (a.kv.dtype == DFS_FP8) go_kind<DFS_FP8>(a, w, c, s);
   else go_kind<DFS_INT8>(a, w, c, s);
   return hipGetLastError();
