@@ -278,7 +278,7 @@ bool elem_aligned(const void* p, int32_t dt) { return (uintptr_t)p % esize(dt) =
 dfs_status check_adapters(const dfs_adapters* ad) {
   if (!ad || ad->n <= 0 || ad->r_max <= 0 || ad->d_in <= 0 || ad->d_out <= 0)
     return DFS_E_INVALID;
-  if (ad->r_max > kMaxAdapterRank) return DFS_E_RANGE;
+  if (ad->r_max > kMaxAdapterRank || ad->n > kMaxAdapters) return DFS_E_RANGE;
   if (!ad->A || !ad->B || !ad->rank || !ad->scale) return DFS_E_INVALID;
   if (ad->lda < ad->d_in || ad->ldb < ad->r_max) return DFS_E_INVALID;
   if (ad->stride_a < 0 || ad->stride_b < 0) return DFS_E_INVALID;

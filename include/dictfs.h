@@ -373,7 +373,7 @@ dfs_status dict_zc_forward(int32_t n_layers, const void* Z, int32_t zdt, int32_t
  *      of A and elements of B rows that adapter a uses; the rest may hold
  *      anything, NaN included;
  *   scale[n] fp32.
- * 1 <= r_max <= 256.  A and B 16-byte aligned; lda, ldb, stride_a and
+ * 1 <= r_max <= 256 and n <= 16383 (DFS_E_RANGE).  A and B 16-byte aligned; lda, ldb, stride_a and
  * stride_b multiples of 8 elements (DFS_E_ALIGN). */
 typedef struct {
   int32_t n;
@@ -404,7 +404,7 @@ dfs_status dict_adapter_workspace_size(int32_t T, const dfs_adapters* ad, size_t
  *   16-byte aligned; base and Y: T x d_out, dtype ydt F16 or F32, aligned to
  *   their element, any leading dimension >= d_out; ids[T] int32, device.
  * Sums are fp32; X A^T is carried into the second product as the sum of two
- * f16 values (22 bits), so the result is rounded once, to Y's type.
+ * f16 values (22 bits) under a power-of-two scale per token, so the result is rounded once, to Y's type.
  * T = 0 is a no-op.  Tokens of one adapter need not stand together. */
 dfs_status dict_adapter_forward(const void* X, int32_t xdt, int32_t T, int64_t ldx,
                                 const dfs_adapters* ad, const int32_t* ids, const void* base,
