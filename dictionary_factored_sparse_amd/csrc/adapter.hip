@@ -27,31 +27,56 @@
 namespace dfs {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTok = 16;       // tokens per tile
 constexpr int kChunk = 64;     // elements of d_in, or outputs, that a wave takes at once
 constexpr int kGroup = 64;     // ranks that one pass over X computes
-constexpr int kSmallT = 256;   // tokens up to which every workgroup finds its own tile
+constexpr int kSmallT = 256;   // tokens up to which a workgroup stands for a token
+constexpr int kMidT = 8192;    // tokens and
+constexpr int kMidN = 4095;    // adapters up to which every workgroup finds its own tile
 constexpr int kPartLd = kGroup + 4;
 constexpr int kULd = kMaxAdapterRank + 8;
 
+// A tile as it passes from one launch to the next.
+struct Tile {
+  int32_t key, count;  // adapter (-1: none), tokens; no tokens: no tile
+  int32_t tok[kTok];
+};
 struct AdapterWs {
   int32_t* perm;    // tokens in order of their adapter
-  int32_t* tiles;   // per tile: first place in perm, tokens, adapter (-1: none)
+  int32_t* plan;    // per tile: first place in perm, tokens, adapter
   int32_t* n_tiles;
+  Tile* tiles;
   float* u;         // [slices][T][rank_ld] partial products X A^T of the split form
-  int32_t slices;   // of d_in; 0: not split
+  int32_t slices;   // of d_in
+  int32_t planned;  // whether plan_kernel has found the tiles
   int32_t rank_ld;
 };
 
-struct Shared {
-  float part[kWaves][kTok][kPartLd];
+template <int W>
+struct FindShared {
+  int32_t hist[kMidN + 1];  // tokens of no adapter, and of each
+  int32_t scan[kMidT / kWave + W];
+  int32_t first;
+};
+template <int W>
+struct ShrinkShared {
+  Tile tile;
+  union {
+    float part[W][kTok][kPartLd];
+    FindShared<W> find;
+  };
+};
+template <int W>
+struct ExpandShared {
+  Tile tile;
+  float stage[W][kTok][kChunk + 4];  // a step's outputs, where they are written one by one
   float u[kTok][kULd];
   _Float16 hi[kTok][kULd], lo[kTok][kULd];
   int32_t exp[kTok];  // hi + lo = u 2^-exp
-  int32_t tok[kTok];
-  int32_t key, count;
+};
+template <int W>
+struct BothShared : ExpandShared<W> {
+  float part[W][kTok][kPartLd];
 };
 
 __device__ __forceinline__ int key_of(const AdapterLaunch& a, int t) {
@@ -59,79 +84,160 @@ __device__ __forceinline__ int key_of(const AdapterLaunch& a, int t) {
   return id >= 0 && id < a.ad.n ? id : -1;
 }
 
-// The tile of workgroup `x` of the tile axis: its adapter and tokens.  For few
-// tokens workgroup x stands for token x and has a tile if that token's place
-// among those of its adapter is a multiple of 16; for many, x indexes the
-// plan's tiles.
-__device__ bool find_tile(const AdapterLaunch& a, const AdapterWs& ws, int x, Shared& sh) {
-  if (a.T <= kSmallT) {
-    if (x >= a.T) return false;
-    if (threadIdx.x < kWave) {
-      const int lane = threadIdx.x;
-      int key[kSmallT / kWave];
-#pragma unroll
-      for (int c = 0; c < kSmallT / kWave; ++c) {
-        const int t = c * kWave + lane;
-        key[c] = t < a.T ? key_of(a, t) : -2;
-      }
-      int mine = -2, place = 0, before = 0;
-#pragma unroll
-      for (int c = 0; c < kSmallT / kWave; ++c)
-        if (c == x / kWave) mine = __builtin_amdgcn_readlane(key[c], x % kWave);
-      uint64_t match[kSmallT / kWave];
-#pragma unroll
-      for (int c = 0; c < kSmallT / kWave; ++c) {
-        match[c] = __ballot(key[c] == mine);
-        const int first = c * kWave;
-        if (x >= first + kWave) place += __popcll(match[c]);
-        else if (x >= first) place += __popcll(match[c] & ((1ull << (x - first)) - 1));
-      }
-      const bool leads = place % kTok == 0;
-#pragma unroll
-      for (int c = 0; c < kSmallT / kWave; ++c) {
-        const int at = before + __popcll(match[c] & ((1ull << lane) - 1)) - place;
-        if (key[c] == mine && at >= 0 && at < kTok) sh.tok[at] = c * kWave + lane;
-        before += __popcll(match[c]);
-      }
-      if (lane == 0) {
-        sh.key = mine;
-        sh.count = leads ? min(before - place, kTok) : 0;
-      }
-    }
-    __syncthreads();
-    return sh.count > 0;
+// Count a wave's keys (-1: none): one atomic where they are all equal, as in
+// the rows of one request.
+__device__ __forceinline__ void count_keys(int32_t* hist, int key) {
+  const uint64_t any = __ballot(key >= 0);
+  if (any == 0) return;
+  const int k = __builtin_amdgcn_readlane(key, __builtin_ctzll(any));
+  if (__ballot(key == k) == any) {
+    if ((int)(threadIdx.x % kWave) == __builtin_ctzll(any)) atomicAdd(&hist[k], __popcll(any));
+  } else if (key >= 0) {
+    atomicAdd(&hist[key], 1);
   }
-  if (x >= *ws.n_tiles) return false;
-  const int first = ws.tiles[3 * x], count = ws.tiles[3 * x + 1];
-  if (threadIdx.x < count) sh.tok[threadIdx.x] = ws.perm[first + threadIdx.x];
-  if (threadIdx.x == 0) {
-    sh.key = ws.tiles[3 * x + 2];
-    sh.count = count;
-  }
-  __syncthreads();
-  return true;
 }
 
-// Eight elements of a row from element d on, zero from `end` on.
-__device__ __forceinline__ h8 row8(const _Float16* row, int d, int end) {
-  if (d + 8 <= end) return ld16<h8>(row + d);
-  h8 v = {};
+// Exclusive sum over the workgroup's threads; *total gets the whole.
+template <int W>
+__device__ __forceinline__ int block_sum(int v, int32_t* tmp, int* total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  int x = v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (d + i < end) v[i] = *gptr(row + d + i);
-  return v;
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int y = __shfl_up(x, o, kWave);
+    if (lane >= o) x += y;
+  }
+  if (lane == kWave - 1) tmp[wave] = x;
+  __syncthreads();
+  int base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < wave) base += tmp[w];
+    sum += tmp[w];
+  }
+  __syncthreads();
+  *total = sum;
+  return base + x - v;
+}
+
+// Tile x of up to kMidT tokens: counts of every adapter say which one tile x
+// belongs to, and the places of that adapter's tokens, in order, which of them
+// it has.  Every workgroup does this for itself, for less than a launch that
+// does it for all of them would take.
+template <int W>
+__device__ void find_tile_mid(const AdapterLaunch& a, int x, Tile& tile, FindShared<W>& sh) {
+  constexpr int kThreads = W * kWave, kKeys = kMidT / kThreads;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int n = a.ad.n + 1;  // key 0: no adapter
+  int key[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int t = i * kThreads + (int)threadIdx.x;
+    key[i] = t < a.T ? key_of(a, t) + 1 : -1;
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads) sh.hist[i] = 0;
+  if (threadIdx.x == 0) tile.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) count_keys(sh.hist, key[i]);
+  __syncthreads();
+  int tile0 = 0;
+  for (int i0 = 0; i0 < n && tile0 <= x; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    const int c = i < n ? sh.hist[i] : 0, tiles = (c + kTok - 1) / kTok;
+    int total;
+    const int at = tile0 + block_sum<W>(tiles, sh.scan, &total);
+    if (x >= at && x < at + tiles) {
+      tile.key = i - 1;
+      sh.first = (x - at) * kTok;
+      tile.count = min(c - (x - at) * kTok, kTok);
+    }
+    tile0 += total;
+  }
+  __syncthreads();
+  if (tile.count == 0) return;
+  const int mine = tile.key + 1;
+  uint64_t match[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    match[i] = __ballot(key[i] == mine);
+    if (lane == 0) sh.scan[i * W + wave] = __popcll(match[i]);
+  }
+  __syncthreads();
+  // places of the tokens of each wave's part, in the order of the tokens
+  const int v = threadIdx.x < kMidT / kWave ? sh.scan[threadIdx.x] : 0;
+  int total;
+  const int before = block_sum<W>(v, sh.scan + kMidT / kWave, &total);
+  if (threadIdx.x < kMidT / kWave) sh.scan[threadIdx.x] = before;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int at = sh.scan[i * W + wave] + __popcll(match[i] & ((1ull << lane) - 1)) - sh.first;
+    if (key[i] == mine && at >= 0 && at < kTok) tile.tok[at] = i * kThreads + (int)threadIdx.x;
+  }
+  __syncthreads();
+}
+
+// Tile x of up to kSmallT tokens, by one wave: x stands for a token, which has
+// a tile if its place among those of its adapter is a multiple of 16.
+__device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, Tile& tile) {
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
+    int key[kSmallT / kWave];
+#pragma unroll
+    for (int c = 0; c < kSmallT / kWave; ++c) {
+      const int t = c * kWave + lane;
+      key[c] = t < a.T ? key_of(a, t) : -2;
+    }
+    int mine = -2, place = 0, before = 0;
+#pragma unroll
+    for (int c = 0; c < kSmallT / kWave; ++c)
+      if (c == x / kWave) mine = __builtin_amdgcn_readlane(key[c], x % kWave);
+    uint64_t match[kSmallT / kWave];
+#pragma unroll
+    for (int c = 0; c < kSmallT / kWave; ++c) {
+      match[c] = __ballot(key[c] == mine);
+      const int first = c * kWave;
+      if (x >= first + kWave) place += __popcll(match[c]);
+      else if (x >= first) place += __popcll(match[c] & ((1ull << (x - first)) - 1));
+    }
+#pragma unroll
+    for (int c = 0; c < kSmallT / kWave; ++c) {
+      const int at = before + __popcll(match[c] & ((1ull << lane) - 1)) - place;
+      if (key[c] == mine && at >= 0 && at < kTok) tile.tok[at] = c * kWave + lane;
+      before += __popcll(match[c]);
+    }
+    if (lane == 0) {
+      tile.key = mine;
+      tile.count = x < a.T && place % kTok == 0 ? min(before - place, kTok) : 0;
+    }
+  }
+  __syncthreads();
+}
+
+// Eight elements of a row from element d on (a multiple of 8), zero from `end`
+// on; rows are readable in whole pieces of eight.  No branch: a lane past the
+// end reads the last piece and drops it.
+__device__ __forceinline__ h8 row8(const _Float16* row, int d, int end) {
+  const u4 v = ld16<u4>(row + min(d, (end - 1) & ~7));
+  const int n = min(max(end - d, 0), 8);  // elements that count
+  u4 keep;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    keep[i] = n >= 2 * i + 2 ? 0xFFFFFFFFu : (n == 2 * i + 1 ? 0xFFFFu : 0u);
+  return __builtin_bit_cast(h8, v & keep);
 }
 
 // This wave's share of U^T for ranks g0 .. g0 + 16 NT - 1 over the 64-element
 // chunks c0 + wave, + kWaves, ... below c1, into sh.part.
-template <int NT>
-__device__ __forceinline__ void shrink_ranks(const AdapterLaunch& a, int r, int g0, int c0, int c1,
-                                             Shared& sh) {
-  constexpr int kAhead = 4 / NT;  // chunks whose loads are in flight together
+template <int NT, int W>
+__device__ __forceinline__ void shrink(const AdapterLaunch& a, const Tile& tile, int r, int g0,
+                                       int c0, int c1, float (*part)[kTok][kPartLd]) {
+  constexpr int kAhead = NT == 1 ? 4 : 2;  // chunks whose loads are in flight together
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const _Float16* x = a.X + (int64_t)sh.tok[min(r16, sh.count - 1)] * a.ldx;
-  const _Float16* A = (const _Float16*)a.ad.A + sh.key * a.ad.stride_a;
+  const _Float16* x = a.X + (int64_t)tile.tok[min(r16, tile.count - 1)] * a.ldx;
+  const _Float16* A = (const _Float16*)a.ad.A + tile.key * a.ad.stride_a;
   const _Float16* w[NT];
   f4 u[NT];
 #pragma unroll
@@ -141,16 +247,17 @@ __device__ __forceinline__ void shrink_ranks(const AdapterLaunch& a, int r, int 
   }
   const int full = min(c1, a.ad.d_in / kChunk);
   int c = c0 + wave;
-  for (; c + (kAhead - 1) * kWaves < full; c += kAhead * kWaves) {
+#pragma unroll 1
+  for (; c + (kAhead - 1) * W < full; c += kAhead * W) {
     h8 xv[kAhead][2], wv[kAhead][NT][2];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int d = (c + k * kWaves) * kChunk + q4 * 16;
+      const int d = (c + k * W) * kChunk + q4 * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        xv[k][h] = ld16<h8>(x + d + 8 * h);
+        xv[k][h] = ld16<h8>(x + d + 32 * h);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) wv[k][i][h] = ld16<h8>(w[i] + d + 8 * h);
+        for (int i = 0; i < NT; ++i) wv[k][i][h] = ld16<h8>(w[i] + d + 32 * h);
       }
     }
 #pragma unroll
@@ -161,10 +268,11 @@ __device__ __forceinline__ void shrink_ranks(const AdapterLaunch& a, int r, int 
         for (int i = 0; i < NT; ++i)
           u[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[k][i][h], xv[k][h], u[i], 0, 0, 0);
   }
-  for (; c < c1; c += kWaves) {  // what is left, and the piece at the end of the rows
+#pragma unroll 1
+  for (; c < c1; c += W) {  // what is left, and the piece at the end of the rows
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int d = c * kChunk + q4 * 16 + 8 * h;
+      const int d = c * kChunk + q4 * 8 + 32 * h;
       const h8 xv = row8(x, d, a.ad.d_in);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -172,18 +280,12 @@ __device__ __forceinline__ void shrink_ranks(const AdapterLaunch& a, int r, int 
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i) *(f4*)&sh.part[wave][r16][16 * i + 4 * q4] = u[i];
+  for (int i = 0; i < NT; ++i) *(f4*)&part[wave][r16][16 * i + 4 * q4] = u[i];
 }
-__device__ __forceinline__ void shrink(const AdapterLaunch& a, int r, int g0, int c0, int c1,
-                                       Shared& sh) {
-  if (r - g0 <= 16) shrink_ranks<1>(a, r, g0, c0, c1, sh);
-  else if (r - g0 <= 32) shrink_ranks<2>(a, r, g0, c0, c1, sh);
-  else shrink_ranks<4>(a, r, g0, c0, c1, sh);
-}
-
-// sh.u to sh.hi + sh.lo, zeros from rank r to r32 on (32 threads per token).
-__device__ __forceinline__ void halve_u(int r, int r32, Shared& sh) {
-  constexpr int kPer = kThreads / kTok;
+// sh.u to sh.hi + sh.lo, zeros from rank r to r32 on (some lanes per token).
+template <int W>
+__device__ __forceinline__ void halve_u(int r, int r32, ExpandShared<W>& sh) {
+  constexpr int kPer = W * kWave / kTok;
   const int tok = threadIdx.x / kPer, at = threadIdx.x % kPer;
   float top = 0.0f;
   for (int k = at; k < r; k += kPer) top = fmaxf(top, fabsf(sh.u[tok][k]));
@@ -200,219 +302,303 @@ __device__ __forceinline__ void halve_u(int r, int r32, Shared& sh) {
   if (at == 0) sh.exp[tok] = e;
 }
 
+// A lane's 16 outputs of a step, of 64: 16 bytes in a row at a time, so that the
+// four lanes of a token and one access cover 64 bytes.
 template <typename YT>
-__device__ __forceinline__ void load16(const YT* p, bool vec, int n, float* v) {
-  if (vec && n == 16) {
-    constexpr int kPer = 16 / sizeof(YT);
-    typedef YT VT __attribute__((ext_vector_type(kPer)));
-#pragma unroll
-    for (int i = 0; i < 16 / kPer; ++i) {
-      const VT w = *gptr((const VT*)p + i);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) v[i * kPer + k] = (float)w[k];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? (float)*gptr(p + i) : 0.0f;
+struct Row16 {
+  static constexpr int kPer = 16 / sizeof(YT);  // elements of one access
+  typedef YT VT __attribute__((ext_vector_type(16 / sizeof(YT))));
+  VT v[16 / kPer];
+  // Place in the step of the lane's first output of access i.
+  static __device__ __forceinline__ int at(int i, int q4) { return (4 * i + q4) * kPer; }
+  // The output of the step that row x of the operand of product m is.
+  static __device__ __forceinline__ int output(int m, int x) {
+    return kPer == 4 ? 16 * m + x : (m >> 1) * 32 + (x >> 2) * 8 + (m & 1) * 4 + (x & 3);
   }
-}
-template <typename YT>
-__device__ __forceinline__ void store16(YT* p, bool vec, int n, const float* v) {
-  if (vec && n == 16) {
-    constexpr int kPer = 16 / sizeof(YT);
-    typedef YT VT __attribute__((ext_vector_type(kPer)));
+  __device__ __forceinline__ void load(const YT* p, int q4) {
 #pragma unroll
-    for (int i = 0; i < 16 / kPer; ++i) {
-      VT w;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) w[k] = (YT)v[i * kPer + k];
-      *gptr_w((VT*)p + i) = w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) *gptr_w(p + i) = (YT)v[i];
+    for (int i = 0; i < 16 / kPer; ++i) v[i] = *gptr((const VT*)(p + at(i, q4)));
   }
-}
+  __device__ __forceinline__ void store(YT* p, int q4) const {
+#pragma unroll
+    for (int i = 0; i < 16 / kPer; ++i) *gptr_w((VT*)(p + at(i, q4))) = v[i];
+  }
+};
 
-// Outputs [j0, j1) of a tile from sh.hi + sh.lo, 64 per wave and step.
-template <typename YT>
-__device__ __forceinline__ void expand(const AdapterLaunch& a, int r, int j0, int j1, bool vec,
-                                       Shared& sh) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int r16 = lane & 15, q4 = lane >> 4;
-  const int steps = (r + 31) / 32;
-  const float scale = r > 0 ? a.ad.scale[sh.key] : 0.0f;
-  const bool mine = r16 < sh.count;
-  const int e = sh.exp[r16];
-  const int64_t t = sh.tok[min(r16, sh.count - 1)];
-  const _Float16* B = (const _Float16*)a.ad.B + max(sh.key, 0) * a.ad.stride_b;
-  for (int jb = j0 + wave * kChunk; jb < j1; jb += kWaves * kChunk) {
-    const int j = jb + 16 * q4, n = min(j1 - j, 16);  // this lane's outputs of its token
-    f4 acc[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) acc[m] = f4{0, 0, 0, 0};
-    float y[16];
-    if (a.base && mine && n > 0) {
-      load16((const YT*)a.base + t * a.ldbase + j, vec, n, y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-    }
-    for (int s = 0; s < steps; ++s) {
-      const int k = s * 32 + q4 * 8;
-      const h8 uh = *(const h8*)&sh.hi[r16][k], ul = *(const h8*)&sh.lo[r16][k];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        // A row x is output 16 (x / 4) + 4 m + x % 4: a lane's results are then
-        // 16 outputs in a row
-        const int row = min(jb + (r16 >> 2) * 16 + 4 * m + (r16 & 3), a.ad.d_out - 1);
-        const h8 w = k < r ? row8(B + row * a.ad.ldb, k, r) : h8{};
-        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, uh, acc[m], 0, 0, 0);
-        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, ul, acc[m], 0, 0, 0);
-      }
-    }
+// The second product: outputs of a tile, 64 per wave and step.  The operands
+// of a step (base, and B for the first KS blocks of 32 ranks) are loaded while
+// the one before it is worked on, and those of the first step before U is
+// known.
+template <typename YT, int KS, int W>
+struct Expand {
+  const AdapterLaunch& a;
+  ExpandShared<W>& sh;
+  const int r, j0, j1, steps, vec, wave, lane, r16, q4;
+  const bool mine;
+  const int64_t t;
+  const _Float16* B;
+  h8 wt[KS][4];
+  Row16<YT> y;
+
+  __device__ __forceinline__ Expand(const AdapterLaunch& a_, ExpandShared<W>& sh_, int r_, int j0_,
+                                    int j1_, int vec_)
+      : a(a_), sh(sh_), r(r_), j0(j0_), j1(j1_), steps((j1_ - j0_ + kChunk - 1) / kChunk),
+        vec(vec_), wave(threadIdx.x / kWave), lane(threadIdx.x % kWave), r16(lane & 15),
+        q4(lane >> 4), mine(r16 < sh_.tile.count),
+        t(sh_.tile.tok[min(r16, sh_.tile.count - 1)]),
+        B((const _Float16*)a_.ad.B + max(sh_.tile.key, 0) * a_.ad.stride_b) {}
+
+  // Steps start elsewhere in each tile: rows that lie a power of two apart
+  // would otherwise keep every workgroup on the same memory channels.
+  __device__ __forceinline__ int place(int i) const {
+    return j0 + (int)((i + 3u * blockIdx.x) % (unsigned)steps) * kChunk;
+  }
+  __device__ __forceinline__ h8 weight(int jb, int m, int s) const {
+    const int row = min(jb + Row16<YT>::output(m, r16), a.ad.d_out - 1);
+    return row8(B + row * a.ad.ldb, s * 32 + q4 * 8, r);
+  }
+  // Whether the step's outputs are read and written in 16-byte pieces.
+  __device__ __forceinline__ bool wide(int jb) const { return vec && jb + kChunk <= j1; }
+  __device__ __forceinline__ void load(int jb) {
     if (r > 0) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) 
-        y[i] = __builtin_fmaf(scale, __builtin_amdgcn_ldexpf(acc[i >> 2][i & 3], e), y[i]);
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) wt[s][m] = weight(jb, m, s);
     }
-    if (mine && n > 0) store16((YT*)a.Y + t * a.ldy + j, vec, n, y);
+    // columns past the tile's tokens repeat the last one and are not stored
+    if (a.base && wide(jb)) y.load((const YT*)a.base + t * a.ldbase + jb, q4);
   }
-}
+  __device__ __forceinline__ void load_first() {
+    if (wave < steps) load(place(wave));
+  }
+  __device__ __forceinline__ void run() {
+    const float scale = r > 0 ? a.ad.scale[sh.tile.key] : 0.0f;
+    const int e = r > 0 ? sh.exp[r16] : 0;
+    constexpr int kPer = Row16<YT>::kPer;
+#pragma unroll 1
+    for (int i = wave; i < steps; i += W) {
+      const int jb = place(i);
+      f4 acc[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[m] = f4{0, 0, 0, 0};
+      const Row16<YT> base = y;
+      if (r > 0) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const h8 uh = *(const h8*)&sh.hi[r16][s * 32 + q4 * 8];
+          const h8 ul = *(const h8*)&sh.lo[r16][s * 32 + q4 * 8];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[s][m], uh, acc[m], 0, 0, 0);
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[s][m], ul, acc[m], 0, 0, 0);
+          }
+        }
+        if constexpr (KS == 2) {
+#pragma unroll 1
+          for (int s = KS; s * 32 < r; ++s) {
+            const h8 uh = *(const h8*)&sh.hi[r16][s * 32 + q4 * 8];
+            const h8 ul = *(const h8*)&sh.lo[r16][s * 32 + q4 * 8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const h8 x = weight(jb, m, s);
+              acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, uh, acc[m], 0, 0, 0);
+              acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, ul, acc[m], 0, 0, 0);
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_ldexpf(acc[m][c], e);
+      }
+      if (i + W < steps) load(place(i + W));
+      if (wide(jb)) {
+        Row16<YT> out;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float b = a.base ? (float)base.v[c / kPer][c % kPer] : 0.0f;
+          out.v[c / kPer][c % kPer] = (YT)(r > 0 ? __builtin_fmaf(scale, acc[c >> 2][c & 3], b) : b);
+        }
+        if (mine) out.store((YT*)a.Y + t * a.ldy + jb, q4);
+      } else {
+        // the end of a row, or rows without 16-byte places: by single outputs,
+        // lane after lane
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sh.stage[wave][r16][Row16<YT>::output(m, 4 * q4 + c)] = acc[m][c];
+        __builtin_amdgcn_wave_barrier();
+        const int j = jb + lane;
+#pragma unroll 1
+        for (int k = 0; k < sh.tile.count; ++k) {
+          const int64_t row = sh.tile.tok[k];
+          if (j < j1) {
+            const float b = a.base ? (float)*gptr((const YT*)a.base + row * a.ldbase + j) : 0.0f;
+            const float v = sh.stage[wave][k][lane];
+            *gptr_w((YT*)a.Y + row * a.ldy + j) = (YT)(r > 0 ? __builtin_fmaf(scale, v, b) : b);
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ int rank_of(const AdapterLaunch& a, int key) {
   return key >= 0 ? min(max(a.ad.rank[key], 0), a.ad.r_max) : 0;
 }
 
-// SPLIT: U comes from the partial products of shrink_kernel.
-template <typename YT, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 4) void adapter_kernel(AdapterLaunch a, AdapterWs ws,
-                                                              int chunk, int vec) {
-  __shared__ Shared sh;
-  if (!find_tile(a, ws, blockIdx.x, sh)) return;
-  const int r = rank_of(a, sh.key);
-  const int r32 = (r + 31) / 32 * 32;
-  if constexpr (SPLIT) {
-    for (int e = threadIdx.x; e < kTok * r; e += kThreads) {
-      const int tok = e / r, rank = e % r;
+// One launch, for few tokens and r_max <= 16 NT: workgroup (x, y) computes U of
+// tile x, then chunk y of its outputs.
+constexpr int kBothWaves = 8;
+template <typename YT, int NT>
+__global__ __launch_bounds__(kBothWaves* kWave, 2) void adapter_kernel(AdapterLaunch a, int chunk,
+                                                                       int vec) {
+  constexpr int W = kBothWaves;
+  __shared__ BothShared<W> sh;
+  find_tile_small(a, blockIdx.x, sh.tile);
+  if (sh.tile.count == 0) return;
+  const int r = rank_of(a, sh.tile.key);
+  const int j0 = blockIdx.y * chunk;
+  Expand<YT, 1, W> x(a, sh, r, j0, min(j0 + chunk, a.ad.d_out), vec);
+  x.load_first();
+  if (r > 0) {
+    shrink<NT, W>(a, sh.tile, r, 0, 0, (a.ad.d_in + kChunk - 1) / kChunk, sh.part);
+    __syncthreads();
+    for (int e = threadIdx.x; e < kTok * 16 * NT; e += W * kWave) {
+      const int tok = e / (16 * NT), rank = e % (16 * NT);
       float v = 0.0f;
-      if (tok < sh.count) {
-        const float* p = ws.u + (int64_t)sh.tok[tok] * ws.rank_ld + rank;
-        for (int s = 0; s < ws.slices; ++s) v += *gptr(p + (int64_t)s * a.T * ws.rank_ld);
-      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += sh.part[w][tok][rank];
       sh.u[tok][rank] = v;
     }
     __syncthreads();
-  } else {
-    for (int g0 = 0; g0 < r; g0 += kGroup) {
-      shrink(a, r, g0, 0, (a.ad.d_in + kChunk - 1) / kChunk, sh);
-      __syncthreads();
-      for (int e = threadIdx.x; e < kTok * kGroup; e += kThreads) {
-        const int tok = e / kGroup, rank = e % kGroup;
-        if (g0 + rank >= r) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += sh.part[w][tok][rank];
-        sh.u[tok][g0 + rank] = v;
-      }
-      __syncthreads();
-    }
-  }
-  if (r > 0) {
-    halve_u(r, r32, sh);
+    halve_u<W>(r, (r + 31) / 32 * 32, sh);
     __syncthreads();
   }
-  const int j0 = blockIdx.y * chunk;
-  expand<YT>(a, r, j0, min(j0 + chunk, a.ad.d_out), vec != 0, sh);
+  x.run();
 }
 
-// Slice blockIdx.y of K of a tile's U, into ws.u.
-__global__ __launch_bounds__(kThreads, 4) void shrink_kernel(AdapterLaunch a, AdapterWs ws) {
-  __shared__ Shared sh;
-  if (!find_tile(a, ws, blockIdx.x, sh)) return;
-  const int r = rank_of(a, sh.key);
+// Two launches.  First: slice blockIdx.y of K of a tile's U into ws.u, and the
+// tile into ws.tiles.  FIND: how a workgroup comes by its tile.
+constexpr int kShrinkWaves = 8;
+enum { kFindSmall, kFindMid, kFindPlanned };
+template <int FIND, int NT>
+__global__ __launch_bounds__(kShrinkWaves* kWave, 4) void shrink_kernel(AdapterLaunch a,
+                                                                        AdapterWs ws) {
+  constexpr int W = kShrinkWaves;
+  __shared__ ShrinkShared<W> sh;
+  const int x = blockIdx.x;
+  if constexpr (FIND == kFindSmall) {
+    find_tile_small(a, x, sh.tile);
+  } else if constexpr (FIND == kFindMid) {
+    find_tile_mid<W>(a, x, sh.tile, sh.find);
+  } else {
+    const bool have = x < *ws.n_tiles;
+    const int count = have ? ws.plan[3 * x + 1] : 0;
+    if ((int)threadIdx.x < count) sh.tile.tok[threadIdx.x] = ws.perm[ws.plan[3 * x] + threadIdx.x];
+    if (threadIdx.x == 0) {
+      sh.tile.key = have ? ws.plan[3 * x + 2] : -1;
+      sh.tile.count = count;
+    }
+    __syncthreads();
+  }
+  if (blockIdx.y == 0 && threadIdx.x < sizeof(Tile) / 4)
+    ((int32_t*)(ws.tiles + x))[threadIdx.x] = ((const int32_t*)&sh.tile)[threadIdx.x];
+  if (sh.tile.count == 0) return;
+  const int r = rank_of(a, sh.tile.key);
   const int chunks = (a.ad.d_in + kChunk - 1) / kChunk;
   const int c0 = (int)((int64_t)chunks * blockIdx.y / ws.slices);
   const int c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / ws.slices);
-  for (int g0 = 0; g0 < r; g0 += kGroup) {
-    shrink(a, r, g0, c0, c1, sh);
+#pragma unroll 1
+  for (int g0 = 0; g0 < r; g0 += 16 * NT) {
+    shrink<NT, W>(a, sh.tile, r, g0, c0, c1, sh.part);
     __syncthreads();
-    for (int e = threadIdx.x; e < sh.count * kGroup; e += kThreads) {
-      const int tok = e / kGroup, rank = e % kGroup;
-      if (g0 + rank >= r) continue;
+    const int n = min(r - g0, 16 * NT);
+    for (int e = threadIdx.x; e < sh.tile.count * 16 * NT; e += W * kWave) {
+      const int tok = e / (16 * NT), rank = e % (16 * NT);
       float v = 0.0f;
-      for (int w = 0; w < kWaves; ++w) v += sh.part[w][tok][rank];
-      *gptr_w(ws.u + ((int64_t)blockIdx.y * a.T + sh.tok[tok]) * ws.rank_ld + g0 + rank) = v;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += sh.part[w][tok][rank];
+      if (rank < n)
+        *gptr_w(ws.u + ((int64_t)blockIdx.y * a.T + sh.tile.tok[tok]) * ws.rank_ld + g0 + rank) = v;
     }
     __syncthreads();
   }
+}
+
+// Second: chunk blockIdx.y of the outputs of a tile.
+constexpr int kExpandWaves = 4;
+template <typename YT, int KS>
+__global__ __launch_bounds__(kExpandWaves* kWave, 3) void expand_kernel(AdapterLaunch a,
+                                                                        AdapterWs ws, int chunk,
+                                                                        int vec) {
+  constexpr int W = kExpandWaves;
+  __shared__ ExpandShared<W> sh;
+  if (threadIdx.x < sizeof(Tile) / 4)
+    ((int32_t*)&sh.tile)[threadIdx.x] = ((const int32_t*)(ws.tiles + blockIdx.x))[threadIdx.x];
+  __syncthreads();
+  if (sh.tile.count == 0) return;
+  const int r = rank_of(a, sh.tile.key);
+  const int j0 = blockIdx.y * chunk;
+  Expand<YT, KS, W> x(a, sh, r, j0, min(j0 + chunk, a.ad.d_out), vec);
+  x.load_first();
+  if (r > 0) {
+    for (int e = threadIdx.x; e < sh.tile.count * r; e += W * kWave) {
+      const int tok = e / r, rank = e % r;
+      const float* p = ws.u + (int64_t)sh.tile.tok[tok] * ws.rank_ld + rank;
+      float v = 0.0f;
+#pragma unroll 4
+      for (int s = 0; s < ws.slices; ++s) v += *gptr(p + (int64_t)s * a.T * ws.rank_ld);
+      sh.u[tok][rank] = v;
+    }
+    __syncthreads();
+    halve_u<W>(r, (r + 31) / 32 * 32, sh);
+    __syncthreads();
+  }
+  x.run();
 }
 
 // The tokens in order of their adapter, and the tiles: one workgroup.  The
 // order of tokens within an adapter is free (a token's result does not depend
 // on its tile), so places are handed out by atomics.
-constexpr int kPlanThreads = 1024;
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(AdapterLaunch a, AdapterWs ws) {
+constexpr int kPlanWaves = 16;
+__global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a, AdapterWs ws) {
   extern __shared__ int32_t place[];  // per adapter, and for no adapter: its count, then its place
-  __shared__ int32_t tmp[2][kPlanThreads / kWave];
-  const int n = a.ad.n + 1, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) place[i] = 0;
+  __shared__ int32_t tmp[kPlanWaves];
+  const int n = a.ad.n + 1;
+  for (int i = threadIdx.x; i < n; i += kPlanWaves * kWave) place[i] = 0;
   __syncthreads();
   for (int pass = 0; pass < 2; ++pass) {
-    for (int t0 = 0; t0 < a.T; t0 += kPlanThreads) {
+    for (int t0 = 0; t0 < a.T; t0 += kPlanWaves * kWave) {
       const int t = t0 + (int)threadIdx.x;
       const int key = t < a.T ? key_of(a, t) + 1 : -1;
-      // one atomic per wave and key
-      for (uint64_t left = __ballot(key >= 0); left != 0;) {
-        const int k = __builtin_amdgcn_readlane(key, __builtin_ctzll(left));
-        const uint64_t same = __ballot(key == k);
-        left &= ~same;
-        int at = 0;
-        if (lane == __builtin_ctzll(same)) at = atomicAdd(&place[k], __popcll(same));
-        at = __builtin_amdgcn_readlane(at, __builtin_ctzll(same));
-        if (pass == 1 && key == k) ws.perm[at + __popcll(same & ((1ull << lane) - 1))] = t;
+      if (pass == 0) {
+        count_keys(place, key);
+      } else if (key >= 0) {
+        ws.perm[atomicAdd(&place[key], 1)] = t;
       }
     }
     __syncthreads();
     if (pass == 1) break;
     int tok0 = 0, tile0 = 0;
-    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    for (int i0 = 0; i0 < n; i0 += kPlanWaves * kWave) {
       const int i = i0 + (int)threadIdx.x;
       const int c = i < n ? place[i] : 0, tiles = (c + kTok - 1) / kTok;
-      int x = c, y = tiles;
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int p = __shfl_up(x, o, kWave), q = __shfl_up(y, o, kWave);
-        if (lane >= o) {
-          x += p;
-          y += q;
-        }
-      }
-      if (lane == kWave - 1) {
-        tmp[0][wave] = x;
-        tmp[1][wave] = y;
-      }
-      __syncthreads();
-      int st = tok0, sy = tile0;
-      for (int w = 0; w < kPlanThreads / kWave; ++w) {
-        if (w < wave) {
-          st += tmp[0][w];
-          sy += tmp[1][w];
-        }
-        tok0 += tmp[0][w];
-        tile0 += tmp[1][w];
-      }
-      st += x - c;
-      sy += y - tiles;
+      int st, sy;
+      const int at_tok = tok0 + block_sum<kPlanWaves>(c, tmp, &st), at_tile = tile0 + block_sum<kPlanWaves>(tiles, tmp, &sy);
+      tok0 += st;
+      tile0 += sy;
       if (i < n) {
-        place[i] = st;
+        place[i] = at_tok;
         for (int k = 0; k < tiles; ++k) {
-          ws.tiles[3 * (sy + k)] = st + k * kTok;
-          ws.tiles[3 * (sy + k) + 1] = min(c - k * kTok, kTok);
-          ws.tiles[3 * (sy + k) + 2] = i - 1;
+          ws.plan[3 * (at_tile + k)] = at_tok + k * kTok;
+          ws.plan[3 * (at_tile + k) + 1] = min(c - k * kTok, kTok);
+          ws.plan[3 * (at_tile + k) + 2] = i - 1;
         }
       }
-      __syncthreads();
     }
     if (threadIdx.x == 0) *ws.n_tiles = tile0;
     __syncthreads();
@@ -423,38 +609,55 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(AdapterLaunch a, Ada
 struct Cut {
   int tiles;   // workgroups of the tile axis
   int chunk;   // outputs per workgroup
-  int slices;  // of K in a launch of its own; 0: U is computed where it is used
+  int slices;  // of K in a launch of its own; 0: one launch
 };
 Cut get_cut(int32_t T, const dfs_adapters& ad) {
   Cut c;
-  c.tiles = T <= kSmallT ? (T + 7) / 8 * 8 : (int)(T / kTok + std::min<int64_t>(ad.n + 1, T));
   // tiles that have work, at most
-  const int busy = std::min<int64_t>(T, T / kTok + std::min<int64_t>(ad.n + 1, T));
-  const int most = (ad.d_out + kWaves * kChunk - 1) / (kWaves * kChunk);
-  const int chunks = std::max(1, std::min(most, 512 / busy));
+  const int busy = (int)std::min<int64_t>(T, T / kTok + std::min<int64_t>(ad.n + 1, T));
+  c.tiles = T <= kSmallT ? (T + 7) / 8 * 8 : busy;
+  const bool both =
+      T <= kSmallT && ad.r_max <= 32 && (int64_t)ad.r_max * ad.d_in <= 256 * 1024;
+  const int per = (both ? kBothWaves : kExpandWaves) * kChunk;  // outputs of one step
+  const int most = (ad.d_out + per - 1) / per;
+#ifndef EC
+#define EC 2048
+#define SC 768
+#endif
+  const int chunks = std::max(1, std::min(most, (both ? 512 : EC) / busy));
   c.chunk = ((ad.d_out + chunks - 1) / chunks + kChunk - 1) / kChunk * kChunk;
-  c.slices = 0;
-  if ((int64_t)ad.r_max * ad.d_in > 512 * 1024 / 2 && busy < 256)
-    c.slices = std::max(1, std::min((ad.d_in + kWaves * kChunk - 1) / (kWaves * kChunk),
-                                    512 / busy));
-  if (c.slices == 1) c.slices = 0;
+  const int k_most = (ad.d_in + kShrinkWaves * kChunk - 1) / (kShrinkWaves * kChunk);
+  c.slices = both ? 0 : std::max(1, std::min(k_most, SC / busy));
   return c;
+}
+
+bool planned(int32_t T, const dfs_adapters& ad) {
+  return T > kMidT || (T > kSmallT && ad.n > kMidN);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 struct Layout {
-  size_t tiles, n, u, total;
+  size_t plan, n, tiles, u, total;
   int rank_ld;
 };
 Layout get_layout(int32_t T, const dfs_adapters& ad, const Cut& c) {
   Layout l;
-  const bool plan = T > kSmallT;
-  l.tiles = plan ? up((size_t)T * 4) : 0;
-  l.n = l.tiles + (plan ? up((size_t)c.tiles * 12) : 0);
-  l.u = l.n + (plan ? 256 : 0);
+  const bool plan = planned(T, ad);
+  l.plan = plan ? up((size_t)T * 4) : 0;
+  l.n = l.plan + (plan ? up((size_t)c.tiles * 12) : 0);
+  l.tiles = l.n + (plan ? 256 : 0);
+  l.u = l.tiles + (c.slices > 0 ? up((size_t)c.tiles * sizeof(Tile)) : 0);
   l.rank_ld = (ad.r_max + 3) / 4 * 4;
   l.total = l.u + (size_t)c.slices * T * l.rank_ld * 4;
   return l;
+}
+
+template <int FIND>
+void go_shrink(const AdapterLaunch& a, const AdapterWs& w, const Cut& c, hipStream_t s) {
+  const dim3 grid(c.tiles, c.slices), block(kShrinkWaves * kWave);
+  if (a.ad.r_max <= 16) hipLaunchKernelGGL((shrink_kernel<FIND, 1>), grid, block, 0, s, a, w);
+  else if (a.ad.r_max <= 32) hipLaunchKernelGGL((shrink_kernel<FIND, 2>), grid, block, 0, s, a, w);
+  else hipLaunchKernelGGL((shrink_kernel<FIND, 4>), grid, block, 0, s, a, w);
 }
 
 template <typename YT>
@@ -462,13 +665,25 @@ void go(const AdapterLaunch& a, const AdapterWs& w, const Cut& c, hipStream_t s)
   const int vec = ((uintptr_t)a.Y | (uintptr_t)a.base) % 16 == 0 && a.ldy * sizeof(YT) % 16 == 0 &&
                   (!a.base || a.ldbase * sizeof(YT) % 16 == 0);
   const dim3 grid(c.tiles, (a.ad.d_out + c.chunk - 1) / c.chunk);
-  if (c.slices > 0) {
-    hipLaunchKernelGGL(shrink_kernel, dim3(c.tiles, c.slices), dim3(kThreads), 0, s, a, w);
-    hipLaunchKernelGGL((adapter_kernel<YT, true>), grid, dim3(kThreads), 0, s, a, w, c.chunk, vec);
-  } else {
-    hipLaunchKernelGGL((adapter_kernel<YT, false>), grid, dim3(kThreads), 0, s, a, w, c.chunk,
-                       vec);
+  if (c.slices == 0) {
+    const dim3 block(kBothWaves * kWave);
+    if (a.ad.r_max <= 16)
+      hipLaunchKernelGGL((adapter_kernel<YT, 1>), grid, block, 0, s, a, c.chunk, vec);
+    else
+      hipLaunchKernelGGL((adapter_kernel<YT, 2>), grid, block, 0, s, a, c.chunk, vec);
+    return;
   }
+  if (w.planned)
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanWaves * kWave), (size_t)(a.ad.n + 1) * 4, s,
+                       a, w);
+  if (a.T <= kSmallT) go_shrink<kFindSmall>(a, w, c, s);
+  else if (!w.planned) go_shrink<kFindMid>(a, w, c, s);
+  else go_shrink<kFindPlanned>(a, w, c, s);
+  const dim3 block(kExpandWaves * kWave);
+  if (a.ad.r_max <= 32)
+    hipLaunchKernelGGL((expand_kernel<YT, 1>), grid, block, 0, s, a, w, c.chunk, vec);
+  else
+    hipLaunchKernelGGL((expand_kernel<YT, 2>), grid, block, 0, s, a, w, c.chunk, vec);
 }
 
 }  // namespace
@@ -481,11 +696,9 @@ hipError_t launch_adapter(const AdapterLaunch& a, void* ws, hipStream_t s) {
   const Cut c = get_cut(a.T, a.ad);
   const Layout l = get_layout(a.T, a.ad, c);
   char* p = (char*)ws;
-  const AdapterWs w = {(int32_t*)p, (int32_t*)(p + l.tiles), (int32_t*)(p + l.n),
-                       (float*)(p + l.u), c.slices, l.rank_ld};
-  if (a.T > kSmallT)
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)(a.ad.n + 1) * 4, s, a,
-                       w);
+  const AdapterWs w = {(int32_t*)p,          (int32_t*)(p + l.plan), (int32_t*)(p + l.n),
+                       (Tile*)(p + l.tiles), (float*)(p + l.u),      c.slices,
+                       planned(a.T, a.ad),   l.rank_ld};
   if (a.ydt == DFS_F16) go<_Float16>(a, w, c, s);
   else go<float>(a, w, c, s);
   return hipGetLastError();

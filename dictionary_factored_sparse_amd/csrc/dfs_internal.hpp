@@ -235,7 +235,7 @@ hipError_t launch_atoms_to_f32(const _Float16* D, int64_t ldd, int d_in, int k, 
 
 // Low-rank adapters of many requests beside a projection
 constexpr int kMaxAdapterRank = 256;
-constexpr int kMaxAdapters = 16383;  // the plan of a large batch counts them in LDS
+constexpr int kMaxAdapters = 16000;  // the plan of a large batch counts them in LDS
 struct AdapterLaunch {
   const _Float16* X;
   int64_t ldx;

@@ -371,9 +371,11 @@ dfs_status dict_zc_forward(int32_t n_layers, const void* Z, int32_t zdt, int32_t
  *      (ldb >= r_max);
  *   rank[n] int32, each in 0 .. r_max (values outside are clamped): the rows
  *      of A and elements of B rows that adapter a uses; the rest may hold
- *      anything, NaN included;
+ *      anything, NaN included.  Rows are read in whole pieces of 8 elements:
+ *      every row, the last one too, must be allocated up to the next multiple
+ *      of 8 elements (so must X's rows), and what lies there is not used;
  *   scale[n] fp32.
- * 1 <= r_max <= 256 and n <= 16383 (DFS_E_RANGE).  A and B 16-byte aligned; lda, ldb, stride_a and
+ * 1 <= r_max <= 256 and n <= 16000 (DFS_E_RANGE).  A and B 16-byte aligned; lda, ldb, stride_a and
  * stride_b multiples of 8 elements (DFS_E_ALIGN). */
 typedef struct {
   int32_t n;

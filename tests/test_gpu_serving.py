@@ -95,6 +95,30 @@ def test_adapter_long_rows_and_many_tokens():
     check_adapter(1100, 1100, 8, 64, 24, "f32", [8] * 1100, rng.permutation(1100))
 
 
+@pytest.mark.parametrize("n", [3, 700, 2500])
+def test_adapter_very_many_tokens(n):
+    rng = np.random.default_rng(n)
+    ranks = rng.integers(0, 9, n)
+    for ids in (rng.integers(-1, n, 8300), np.repeat(rng.integers(-1, n, 30), 280)[:8193]):
+        check_adapter(len(ids), n, 8, 40, 24, "f32", ranks, ids)
+
+
+def test_adapter_large_and_small_products():
+    """X A^T far outside f16's range, and far below it."""
+    rng = np.random.default_rng(4)
+    ad, ref = make_adapters(rng, 2, 16, 256, 64, [16, 13])
+    for size in (2.0 ** 9, 2.0 ** -22):
+        X = (rng.standard_normal((18, 256)) * size).astype(np.float16)
+        big = B.DeviceAdapters(ad.A * 64, ad.B, ad.rank, ad.scale, r_max=16) if size > 1 else ad
+        want = (ref[0] * (64 if size > 1 else 1),) + ref[1:]
+        ids = np.arange(18) % 2
+        y = B.dict_adapter_forward(torch.from_numpy(X).to(DEV), big, ints(ids),
+                                   ydtype=torch.float32)
+        torch.cuda.synchronize()
+        ref_y, bound = R.adapter(X, *want, ids, None, "f32")
+        within(y, ref_y, bound, f"products of size {size}")
+
+
 def test_adapter_no_tokens():
     rng = np.random.default_rng(1)
     ad, _ = make_adapters(rng, 1, 8, 64, 32, [8])
