@@ -3,13 +3,12 @@
 // FMA contraction: each step of the recipe is one correctly rounded fp32
 // operation.
 //
-// One workgroup per page that gets tokens, head, and keys or values: a first
-// pass over the new elements for the largest size, a second (from L1: a page's
-// new elements are 4 to 128 KB) for the codes.  Workgroups of neighbouring
+// One workgroup per page that gets tokens and head: a first pass over the new
+// elements for the largest sizes, a second for the codes, with the elements
+// kept in registers between them where they fit.  Workgroups of neighbouring
 // heads read neighbouring bytes and are neighbours in the grid.  Values are
-// stored with the page's tokens contiguous, so a lane takes 16 tokens of a few
-// dims and packs codes across the tokens in registers: no transposition
-// through LDS.
+// stored with the page's tokens contiguous: a lane packs the codes of four
+// tokens into a word, and the words go out through LDS.
 //
 // What bounds it: prompts, the bytes (source read, codes written); single
 // tokens, the chain of dependent reads (requests, page table, scale).
@@ -103,15 +102,24 @@ struct Piece {
   }
 };
 
-__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+// Maxima of k and v over the workgroup.
+__device__ __forceinline__ void block_max(uint32_t& k, uint32_t& v, uint32_t (*red)[2]) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
+  for (int o = 32; o > 0; o >>= 1) {
+    k = max(k, (uint32_t)__shfl_xor((int)k, o, kWave));
+    v = max(v, (uint32_t)__shfl_xor((int)v, o, kWave));
+  }
   __syncthreads();
-  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = m;
+  if (threadIdx.x % kWave == 0) {
+    red[threadIdx.x / kWave][0] = k;
+    red[threadIdx.x / kWave][1] = v;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = max(m, red[w]);
-  return m;
+  for (int w = 0; w < kWaves; ++w) {
+    k = max(k, red[w][0]);
+    v = max(v, red[w][1]);
+  }
 }
 
 // The request and page that slot `slot` stands for (slots count the pages that
@@ -152,116 +160,158 @@ __device__ __forceinline__ bool find_job(const KvBatch& b, int P, int slot, Job&
   return false;
 }
 
+// Four slots' pieces of a few dims, zero for slots outside [lo, hi).
+template <typename T>
+struct Item {
+  Piece<T> x[4];
+  __device__ __forceinline__ void load(const T* src, int64_t ld, int s0, int lo, int hi, bool vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i].v = typename Piece<T>::VT{};
+      if (s0 + i >= lo && s0 + i < hi) x[i].load(src + (s0 + i) * ld, vec);
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(x[0].top(), x[1].top()), max(x[2].top(), x[3].top()));
+  }
+};
+
+// Four codes under a new scale.
+template <int KIND>
+__device__ __forceinline__ uint32_t again4(uint32_t c, float old, const Quotient& q) {
+  return encode4<KIND>(q(decode8<KIND>(c) * old), q(decode8<KIND>(c >> 8) * old),
+                       q(decode8<KIND>(c >> 16) * old), q(decode8<KIND>(c >> 24) * old));
+}
+
 template <int KIND, typename T>
 __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b, const T* K,
                                                           int64_t ldk, const T* V, int64_t ldv,
                                                           int vec, int slot0) {
   constexpr int kN = Piece<T>::kN;
-  __shared__ uint32_t red[kWaves];
+  __shared__ uint32_t red[kWaves][2];
+  extern __shared__ uint32_t words[];  // new value codes, [dim][word of four slots]
   const int P = kv.page, D = kv.head_dim, h = blockIdx.x;
-  const bool values = blockIdx.z != 0;
   Job j;
   if (!find_job(b, P, slot0 + (int)blockIdx.y, j) || j.page >= b.table_pages) return;
-  const int pg = *gptr(b.table + j.req * b.ldt + j.page);
+  const int32_t* entry = b.table + j.req * b.ldt + j.page;
+  const int pg = *gptr(entry);
   // slots lo .. hi - 1 of the page are new; slot s is row row0 + s of the source
-  const int64_t p0 = (int64_t)j.page * P;
+  const int64_t p0 = (int64_t)j.page * P, row0 = j.t0 + p0 - j.cached;
   const int lo = (int)max((int64_t)j.cached - p0, (int64_t)0);
   const int hi = (int)min((int64_t)j.cached + j.n - p0, (int64_t)P);
-  const int64_t ld = values ? ldv : ldk;
-  const T* src = (values ? V : K) + (int64_t)h * D + (j.t0 + p0 - j.cached) * ld;
-  const int per_row = D / kN;
-  uint32_t top = 0;
-#pragma unroll 4
-  for (int e = threadIdx.x; e < (hi - lo) * per_row; e += kThreads) {
-    const int s = e / per_row;
-    Piece<T> x;
-    x.load(src + (lo + s) * ld + (e - s * per_row) * kN, vec);
-    top = max(top, x.top());
+  const T* ksrc = K + (int64_t)h * D + row0 * ldk;
+  const T* vsrc = V + (int64_t)h * D + row0 * ldv;
+  // an item is four slots of kN dims; a thread's first one stays in registers
+  // (all of them do for up to 256 items: 64 tokens of 128 f16 dims)
+  const int per_row = D / kN, w0 = lo / 4, w1 = (hi + 3) / 4, items = (w1 - w0) * per_row;
+  auto slot_of = [&](int e) { return 4 * (w0 + e / per_row); };
+  auto dim_of = [&](int e) { return e % per_row * kN; };
+  Item<T> k0, v0;
+  uint32_t ktop = 0, vtop = 0;
+  if ((int)threadIdx.x < items) {
+    const int s0 = slot_of(threadIdx.x), d = dim_of(threadIdx.x);
+    k0.load(ksrc + d, ldk, s0, lo, hi, vec);
+    v0.load(vsrc + d, ldv, s0, lo, hi, vec);
   }
-  top = block_max(top, red);
-  const bool tame = top > kTop;
+  const bool real = pg >= 0 && pg < kv.n_pages;
+  const int64_t ph = (int64_t)(real ? pg : 0) * kv.heads + h;
+  const float kold = lo > 0 ? *gptr(kv.kscale + ph) : 0.0f;
+  const float vold = lo > 0 ? *gptr(kv.vscale + ph) : 0.0f;
+  if ((int)threadIdx.x < items) {
+    ktop = k0.top();
+    vtop = v0.top();
+  }
+#pragma unroll 1
+  for (int e = threadIdx.x + kThreads; e < items; e += kThreads) {
+    const int s0 = slot_of(e), d = dim_of(e);
+    Item<T> x, y;
+    x.load(ksrc + d, ldk, s0, lo, hi, vec);
+    y.load(vsrc + d, ldv, s0, lo, hi, vec);
+    ktop = max(ktop, x.top());
+    vtop = max(vtop, y.top());
+  }
+  block_max(ktop, vtop, red);
+  const bool tame = max(ktop, vtop) > kTop;
   if (tame) {  // something is not finite or too large: once more, with what it counts as
-    top = 0;
+    ktop = vtop = 0;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < (hi - lo) * D; e += kThreads)
-      top = max(top, __float_as_uint(fabsf(tamed((float)src[(lo + e / D) * ld + e % D]))));
-    top = block_max(top, red);
+    for (int e = threadIdx.x; e < (hi - lo) * D; e += kThreads) {
+      const int s = lo + e / D, d = e % D;
+      ktop = max(ktop, __float_as_uint(fabsf(tamed((float)ksrc[s * ldk + d]))));
+      vtop = max(vtop, __float_as_uint(fabsf(tamed((float)vsrc[s * ldv + d]))));
+    }
+    block_max(ktop, vtop, red);
   }
-  if (pg < 0 || pg >= kv.n_pages) return;
-  const int64_t ph = (int64_t)pg * kv.heads + h;
-  uint8_t* codes = (values ? kv.v : kv.k) + ph * P * D;
-  float* scale = (values ? kv.vscale : kv.kscale) + ph;
-  const float need = __uint_as_float(top) / (KIND == DFS_FP8 ? 448.0f : 127.0f);
-  const float old = lo > 0 ? *scale : 0.0f;
-  const float sc = need > old ? need : old;
-  const Quotient q(sc);
-  if (need > old && lo > 0) {
-    // a larger scale: the codes of the tokens already there, four at a time
-    // (keys: of four dims; values: of four tokens, of which some may be new or
-    // later and stay)
-    const int words = values ? (lo + 3) / 4 : D / 4, rows = values ? D : lo;
-#pragma unroll 1
-    for (int e = threadIdx.x; e < rows * words; e += kThreads) {
-      const int row = e / words, w = e - row * words;
-      uint32_t* p = (uint32_t*)(codes + row * (values ? P : D)) + w;
-      const uint32_t c = *p;
-      const int held = values ? lo - 4 * w : 4;  // bytes that are older tokens'
-      const uint32_t keep = held >= 4 ? 0u : 0xFFFFFFFFu << (8 * held);
-      const uint32_t n = encode4<KIND>(q(decode8<KIND>(c) * old), q(decode8<KIND>(c >> 8) * old),
-                                       q(decode8<KIND>(c >> 16) * old),
-                                       q(decode8<KIND>(c >> 24) * old));
-      *p = (c & keep) | (n & ~keep);
-    }
-    __syncthreads();  // new tokens' bytes go into the same words
+  if (!real) return;
+  constexpr float kMax = KIND == DFS_FP8 ? 448.0f : 127.0f;
+  const float kneed = __uint_as_float(ktop) / kMax, vneed = __uint_as_float(vtop) / kMax;
+  const Quotient kq(kneed > kold ? kneed : kold), vq(vneed > vold ? vneed : vold);
+  if (threadIdx.x == 0) {
+    kv.kscale[ph] = kq.scale;
+    kv.vscale[ph] = vq.scale;
   }
-  if (threadIdx.x == 0) *scale = sc;
-  if (!values) {
-#pragma unroll 2
-    for (int e = threadIdx.x; e < (hi - lo) * per_row; e += kThreads) {
-      const int s = e / per_row, d = (e - s * per_row) * kN;
-      Piece<T> x;
-      x.load(src + (lo + s) * ld + d, vec);
-      uint32_t* p = (uint32_t*)(codes + (lo + s) * D + d);
-#pragma unroll
-      for (int i = 0; i < kN; i += 4)
-        p[i / 4] = encode4<KIND>(q(x.at(i, tame)), q(x.at(i + 1, tame)), q(x.at(i + 2, tame)),
-                                 q(x.at(i + 3, tame)));
-    }
-  } else {
-    // groups of 16 slots: whole ones by 16-byte stores, others token by token
-    const int g0 = lo / 16, groups = (hi + 15) / 16 - g0;
+  uint8_t* kc = kv.k + ph * P * D;
+  uint8_t* vc = kv.v + ph * P * D;
+  if (kneed > kold && lo > 0) {
+    // a larger scale: the codes of the tokens already there
+    constexpr int kAhead = 8;
+    uint32_t* p = (uint32_t*)kc;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < groups * per_row; e += kThreads) {
-      const int g = e / per_row, d = (e - g * per_row) * kN, s0 = (g0 + g) * 16;
-      uint8_t* p = codes + d * P + s0;
-      if (s0 >= lo && s0 + 16 <= hi) {
-        Piece<T> x[16];
+    for (int e = threadIdx.x; e < lo * D / 4; e += kAhead * kThreads) {
+      uint32_t c[kAhead];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i].load(src + (s0 + i) * ld + d, vec);
+      for (int i = 0; i < kAhead; ++i) c[i] = *gptr(p + min(e + i * kThreads, lo * D / 4 - 1));
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          u4 w;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = encode4<KIND>(q(x[4 * i].at(k, tame)), q(x[4 * i + 1].at(k, tame)),
-                                 q(x[4 * i + 2].at(k, tame)), q(x[4 * i + 3].at(k, tame)));
-          *gptr_w((u4*)(p + k * P)) = w;
-        }
-      } else {
-#pragma unroll 1
-        for (int s = max(s0, lo); s < min(s0 + 16, hi); ++s) {
-          Piece<T> x;
-          x.load(src + s * ld + d, vec);
-#pragma unroll
-          for (int k = 0; k < kN; k += 4) {
-            const uint32_t w = encode4<KIND>(q(x.at(k, tame)), q(x.at(k + 1, tame)),
-                                             q(x.at(k + 2, tame)), q(x.at(k + 3, tame)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[(k + i) * P + s - s0] = (uint8_t)(w >> (8 * i));
-          }
-        }
-      }
+      for (int i = 0; i < kAhead; ++i)
+        if (e + i * kThreads < lo * D / 4) *gptr_w(p + e + i * kThreads) = again4<KIND>(c[i], kold, kq);
     }
+  }
+  const int ldw = P / 4 + 1;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < items; e += kThreads) {
+    const int s0 = slot_of(e), d = dim_of(e);
+    if (e >= kThreads) {
+      k0.load(ksrc + d, ldk, s0, lo, hi, vec);
+      v0.load(vsrc + d, ldv, s0, lo, hi, vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Piece<T>& x = k0.x[i];
+      if (s0 + i < lo || s0 + i >= hi) continue;
+      typedef uint32_t CT __attribute__((ext_vector_type(kN / 4)));
+      CT w;
+#pragma unroll
+      for (int c = 0; c < kN; c += 4)
+        w[c / 4] = encode4<KIND>(kq(x.at(c, tame)), kq(x.at(c + 1, tame)), kq(x.at(c + 2, tame)),
+                                 kq(x.at(c + 3, tame)));
+      *gptr_w((CT*)(kc + (s0 + i) * D + d)) = w;
+    }
+#pragma unroll
+    for (int c = 0; c < kN; ++c)
+      words[(d + c) * ldw + s0 / 4] =
+          encode4<KIND>(vq(v0.x[0].at(c, tame)), vq(v0.x[1].at(c, tame)), vq(v0.x[2].at(c, tame)),
+                        vq(v0.x[3].at(c, tame)));
+  }
+  __syncthreads();
+  // value codes by words of four slots, dim after dim.  A word may hold older
+  // tokens (first bytes) and later slots (last bytes), which stay.
+  const bool grown = vneed > vold && lo > 0;
+  const int first = grown ? 0 : w0, n = w1 - first;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < D * n; e += kThreads) {
+    const int d = e / n, w = first + e % n;
+    uint32_t* p = (uint32_t*)(vc + d * P) + w;
+    const int older = min(max(lo - 4 * w, 0), 4), later = min(max(4 * w + 4 - hi, 0), 4);
+    uint32_t c = w >= w0 ? words[d * ldw + w] : 0u;
+    if (older + later > 0) {
+      const uint32_t was = *gptr(p);
+      const uint32_t om = older == 4 ? 0xFFFFFFFFu : (1u << (8 * older)) - 1u;
+      const uint32_t lm = later == 0 ? 0u : 0xFFFFFFFFu << (8 * (4 - later));
+      c &= ~(om | lm);
+      c |= was & lm;
+      c |= (grown && older > 0 ? again4<KIND>(was, vold, vq) : was) & om;
+    }
+    *gptr_w(p) = c;
   }
 }
 
@@ -275,8 +325,8 @@ void go(const dfs_kv8& kv, const KvBatch& b, const void* K, int64_t ldk, const v
   // the y axis of a grid ends at 65535: one launch but for millions of tokens
   for (int64_t y = 0; y < most; y += 65535)
     hipLaunchKernelGGL((append_kernel<KIND, T>),
-                       dim3(kv.heads, (unsigned)std::min<int64_t>(most - y, 65535), 2),
-                       dim3(kThreads), 0, s, kv, b, (const T*)K, ldk, (const T*)V, ldv, vec, (int)y);
+                       dim3(kv.heads, (unsigned)std::min<int64_t>(most - y, 65535)),
+                       dim3(kThreads), (kv.page / 4 + 1) * kv.head_dim * 4, s, kv, b, (const T*)K, ldk, (const T*)V, ldv, vec, (int)y);
 }
 
 }  // namespace
