@@ -576,9 +576,15 @@ class DeviceAdapters:
                 raise ValueError(f"{what}: contiguous {dt} of {n} values required")
         _same_device((A, Bm, self.rank, self.scale), "adapters")
         self.r_max, self.d_in, self.d_out = r, A.shape[2], Bm.shape[1]
+        for t, what, cols in ((A, "A", self.d_in), (Bm, "B", r)):
+            end = t.storage_offset() + sum((n - 1) * st for n, st in zip(t.shape[:2], t.stride())
+                                           ) + -(-cols // 8) * 8
+            if end > t.untyped_storage().nbytes() // 2:
+                raise ValueError(f"{what}: rows must be allocated in whole pieces of 8 elements")
         self._desc = Adapters(n, r, self.d_in, self.d_out, A.data_ptr(), A.stride(1), A.stride(0),
                               Bm.data_ptr(), Bm.stride(1), Bm.stride(0), self.rank.data_ptr(),
                               self.scale.data_ptr())
+        self._ref = C.byref(self._desc)
 
     def desc(self) -> Adapters:
         return self._desc
@@ -611,6 +617,7 @@ class DeviceKV8:
         self.n_pages, self.heads, self.page, self.head_dim = n, h, p, d
         self._desc = KV8(n, h, d, p, CODE8[self.kind], 0, self.k.data_ptr(), self.v.data_ptr(),
                          self.kscale.data_ptr(), self.vscale.data_ptr())
+        self._ref = C.byref(self._desc)
 
     def desc(self) -> KV8:
         return self._desc
@@ -623,21 +630,36 @@ class DeviceKV8:
                          z(torch.float32, n_pages, heads), z(torch.float32, n_pages, heads), kind)
 
 
+# These calls take some microseconds on the device: their checks are kept short.
+
 def _same_device(ts, what: str) -> None:
-    if any(t.device != ts[0].device for t in ts):
-        raise ValueError(f"{what}: every tensor on one device required")
+    dev = ts[0].device
+    for t in ts:
+        if t.device != dev:
+            raise ValueError(f"{what}: every tensor on one device required")
 
 
-def _matrix(t: torch.Tensor, what: str, rows: int | None, cols: int) -> None:
-    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+def _matrix(t: torch.Tensor, what: str, rows: int | None, cols: int) -> int:
+    """Checks a row-major tensor; its row stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise ValueError(f"{what}: a 2-D tensor of {cols} columns with unit stride required")
-    if rows is not None and t.shape[0] != rows:
-        raise ValueError(f"{what}: {t.shape[0]} rows, expected {rows}")
+    if rows is not None and shape[0] != rows:
+        raise ValueError(f"{what}: {shape[0]} rows, expected {rows}")
+    return stride[0]
 
 
 def _ints(t: torch.Tensor, what: str, n: int) -> None:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype != torch.int32 or (t.stride() != (1,) and n > 1):
         raise ValueError(f"{what}: contiguous int32 of {n} values required")
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The stream to launch on: the given one, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
+
 
 
 def adapter_workspace(T: int, ad: DeviceAdapters, device) -> torch.Tensor:
@@ -654,52 +676,58 @@ def dict_adapter_forward(X, ad: DeviceAdapters, ids, base=None, Y=None, ydtype=t
     where ids[t] names no adapter.  ``base`` None stands for zeros; ``Y`` may be
     ``base`` (the adapters are added in place)."""
     T = X.shape[0]
-    _matrix(X, "X", None, ad.d_in)
+    ldx = _matrix(X, "X", None, ad.d_in)
+    if ad.d_in % 8 and T and (X.storage_offset() + (T - 1) * ldx + -(-ad.d_in // 8) * 8
+                              > X.untyped_storage().nbytes() // X.element_size()):
+        raise ValueError("X: rows must be allocated in whole pieces of 8 elements")
     if Y is None:
         Y = torch.empty(T, ad.d_out, dtype=ydtype, device=X.device)
-    _matrix(Y, "Y", T, ad.d_out)
+    ldy = _matrix(Y, "Y", T, ad.d_out)
     _ints(ids, "ids", T)
+    ptr, ldb = None, 0
     if base is not None:
-        _matrix(base, "base", T, ad.d_out)
+        ptr, ldb = base.data_ptr(), _matrix(base, "base", T, ad.d_out)
         if base.dtype != Y.dtype:
             raise TypeError("base and Y must have the same type")
     _same_device((X, ad.A, ids, Y) if base is None else (X, ad.A, ids, Y, base), "adapters")
     if ws is None:
         ws = adapter_workspace(T, ad, X.device)
-    _check("dict_adapter_forward",
-           lib().dict_adapter_forward(X.data_ptr(), _dt(X), T, X.stride(0), C.byref(ad.desc()),
-                                      ids.data_ptr(), None if base is None else base.data_ptr(),
-                                      0 if base is None else base.stride(0), Y.data_ptr(), _dt(Y),
-                                      Y.stride(0), ws.data_ptr(), ws.numel(), _stream(stream)))
+    st = lib().dict_adapter_forward(X.data_ptr(), _dt(X), T, ldx, ad._ref, ids.data_ptr(), ptr, ldb,
+                                    Y.data_ptr(), _dt(Y), ldy, ws.data_ptr(), ws.numel(),
+                                    _stream_of(X, stream))
+    if st:
+        raise DfsError("dict_adapter_forward", st)
     return Y
 
 
-def _kv_batch(kv: DeviceKV8, tok_start, have, table) -> int:
+def _kv_batch(kv: DeviceKV8, tok_start, have, table):
+    """Checks a batch's requests; how many there are, and the table's row stride and length."""
     n_req = have.shape[0]
     _ints(have, "tokens per request", n_req)
     _ints(tok_start, "tok_start", n_req + 1)
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_req or (
-            table.shape[1] > 1 and table.stride(1) != 1):
+    shape, stride = table.shape, table.stride()
+    if (len(shape) != 2 or shape[0] != n_req or (stride[1] != 1 and shape[1] > 1)
+            or table.dtype != torch.int32):
         raise ValueError(f"table: int32 of {n_req} rows with unit column stride required")
-    _same_device((kv.k, tok_start, have, table), "cache")
-    return n_req
+    return n_req, max(stride[0], shape[1]) if n_req <= 1 else stride[0], shape[1]
 
 
 def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> None:
     """Append the rows of K and V (heads * head_dim columns) to the cache, in
     place: request r's rows are tok_start[r] .. tok_start[r+1]-1 and go to the
     positions from cached[r] on, in the pages of table[r]."""
-    n_req = _kv_batch(kv, tok_start, cached, table)
-    _matrix(K, "K", None, kv.heads * kv.head_dim)
-    _matrix(V, "V", K.shape[0], kv.heads * kv.head_dim)
+    n_req, ldt, pages = _kv_batch(kv, tok_start, cached, table)
+    ldk = _matrix(K, "K", None, kv.heads * kv.head_dim)
+    n_tok = K.shape[0]
+    ldv = _matrix(V, "V", n_tok, kv.heads * kv.head_dim)
     if K.dtype != V.dtype:
         raise TypeError("K and V must have the same type")
-    _same_device((kv.k, K, V), "cache")
-    _check("kv8_append",
-           lib().kv8_append(C.byref(kv.desc()), n_req, K.shape[0], tok_start.data_ptr(),
-                            cached.data_ptr(), table.data_ptr(), table.stride(0), table.shape[1],
-                            K.data_ptr(), K.stride(0), V.data_ptr(), V.stride(0), _dt(K),
-                            _stream(stream)))
+    _same_device((kv.k, K, V, tok_start, cached, table), "cache")
+    st = lib().kv8_append(kv._ref, n_req, n_tok, tok_start.data_ptr(), cached.data_ptr(),
+                          table.data_ptr(), ldt, pages, K.data_ptr(), ldk, V.data_ptr(), ldv,
+                          _dt(K), _stream_of(K, stream))
+    if st:
+        raise DfsError("kv8_append", st)
 
 
 def kv8_attention_workspace(kv: DeviceKV8, n_req: int, n_tok: int, q_heads: int,
@@ -719,24 +747,24 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
     """Causal attention of the rows of Q (q_heads * head_dim columns) over the
     cache: request r's rows are the last of its length[r] tokens.  ``sm_scale``
     None is 1/sqrt(head_dim); ``window`` 0 is no window.  Returns O."""
-    n_req = _kv_batch(kv, tok_start, length, table)
-    n_tok = Q.shape[0]
-    _matrix(Q, "Q", None, q_heads * kv.head_dim)
+    n_req, ldt, pages = _kv_batch(kv, tok_start, length, table)
+    n_tok, cols = Q.shape[0], q_heads * kv.head_dim
+    ldq = _matrix(Q, "Q", None, cols)
     if Q.dtype != torch.float16:
         raise TypeError("Q must be float16")
     if O is None:
-        O = torch.empty(n_tok, q_heads * kv.head_dim, dtype=odtype, device=Q.device)
-    _matrix(O, "O", n_tok, q_heads * kv.head_dim)
-    _same_device((kv.k, Q, O), "cache")
+        O = torch.empty(n_tok, cols, dtype=odtype, device=Q.device)
+    ldo = _matrix(O, "O", n_tok, cols)
+    _same_device((kv.k, Q, O, tok_start, length, table), "cache")
     if ws is None:
         ws = kv8_attention_workspace(kv, n_req, n_tok, q_heads, Q.device)
-    _check("kv8_attention",
-           lib().kv8_attention(C.byref(kv.desc()), n_req, n_tok, tok_start.data_ptr(),
-                               length.data_ptr(), table.data_ptr(), table.stride(0),
-                               table.shape[1], Q.data_ptr(), Q.stride(0), q_heads,
-                               kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window,
-                               sinks, O.data_ptr(), _dt(O), O.stride(0), ws.data_ptr(),
-                               ws.numel(), _stream(stream)))
+    st = lib().kv8_attention(kv._ref, n_req, n_tok, tok_start.data_ptr(), length.data_ptr(),
+                             table.data_ptr(), ldt, pages, Q.data_ptr(), ldq, q_heads,
+                             kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window, sinks,
+                             O.data_ptr(), _dt(O), ldo, ws.data_ptr(), ws.numel(),
+                             _stream_of(Q, stream))
+    if st:
+        raise DfsError("kv8_attention", st)
     return O
 
 

@@ -217,6 +217,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b,
   const int64_t ph = (int64_t)(real ? pg : 0) * kv.heads + h;
   const float kold = lo > 0 ? *gptr(kv.kscale + ph) : 0.0f;
   const float vold = lo > 0 ? *gptr(kv.vscale + ph) : 0.0f;
+  // what the value codes' first word holds now, if it keeps some of it
+  uint32_t was0 = 0;
+  if ((int)threadIdx.x < D * (w1 - w0) && real) {
+    const int w = w0 + (int)threadIdx.x % (w1 - w0);
+    if (4 * w < lo || 4 * w + 4 > hi)
+      was0 = *gptr((uint32_t*)(kv.v + (ph * D + (int)threadIdx.x / (w1 - w0)) * P) + w);
+  }
   if ((int)threadIdx.x < items) {
     ktop = k0.top();
     vtop = v0.top();
@@ -304,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b,
     const int older = min(max(lo - 4 * w, 0), 4), later = min(max(4 * w + 4 - hi, 0), 4);
     uint32_t c = w >= w0 ? words[d * ldw + w] : 0u;
     if (older + later > 0) {
-      const uint32_t was = *gptr(p);
+      const uint32_t was = !grown && e < kThreads ? was0 : *gptr(p);
       const uint32_t om = older == 4 ? 0xFFFFFFFFu : (1u << (8 * older)) - 1u;
       const uint32_t lm = later == 0 ? 0u : 0xFFFFFFFFu << (8 * (4 - later));
       c &= ~(om | lm);
