@@ -27,56 +27,66 @@
 namespace dfs {
 namespace {
 
-constexpr int kTok = 16;       // tokens per tile
+constexpr int kTok = 16;       // tokens of one matrix instruction
+constexpr int kMany = 4;       // groups of 16 tokens in a tile of a large batch
 constexpr int kChunk = 64;     // elements of d_in, or outputs, that a wave takes at once
-constexpr int kGroup = 64;     // ranks that one pass over X computes
 constexpr int kSmallT = 256;   // tokens up to which a workgroup stands for a token
 constexpr int kMidT = 8192;    // tokens and
 constexpr int kMidN = 4095;    // adapters up to which every workgroup finds its own tile
-constexpr int kPartLd = kGroup + 4;
-constexpr int kULd = kMaxAdapterRank + 8;
 
-// A tile as it passes from one launch to the next.
-struct Tile {
+// A tile: up to 16 NG tokens of one adapter.
+struct TileHead {
   int32_t key, count;  // adapter (-1: none), tokens; no tokens: no tile
-  int32_t tok[kTok];
+  int32_t rank;
+  float scale;
+};
+template <int NG>
+struct Tile : TileHead {
+  int32_t tok[kTok * NG];
 };
 struct AdapterWs {
   int32_t* perm;    // tokens in order of their adapter
   int32_t* plan;    // per tile: first place in perm, tokens, adapter
   int32_t* n_tiles;
-  Tile* tiles;
+  char* tiles;      // of the first launch, for the second
   float* u;         // [slices][T][rank_ld] partial products X A^T of the split form
   int32_t slices;   // of d_in
-  int32_t planned;  // whether plan_kernel has found the tiles
   int32_t rank_ld;
 };
 
 template <int W>
 struct FindShared {
   int32_t hist[kMidN + 1];  // tokens of no adapter, and of each
-  int32_t scan[kMidT / kWave + W];
+  int32_t scan[W];
   int32_t first;
 };
-template <int W>
+// Ranks that one pass over X computes: 16 NT.
+template <int NT, int NG, int W>
+struct Part {
+  float u[W][kTok * NG][16 * NT + 4];
+};
+template <int NT, int NG, int W>
 struct ShrinkShared {
-  Tile tile;
+  Tile<NG> tile;
   union {
-    float part[W][kTok][kPartLd];
+    Part<NT, NG, W> part;
     FindShared<W> find;
   };
 };
-template <int W>
+template <int NG, int W>
 struct ExpandShared {
-  Tile tile;
-  float stage[W][kTok][kChunk + 4];  // a step's outputs, where they are written one by one
-  float u[kTok][kULd];
-  _Float16 hi[kTok][kULd], lo[kTok][kULd];
-  int32_t exp[kTok];  // hi + lo = u 2^-exp
+  static constexpr int kULd = (NG == 1 ? kMaxAdapterRank : 64) + 8;
+  Tile<NG> tile;
+  union {
+    float u[kTok * NG][kULd];          // until it is halved; then
+    float stage[W][kTok][kChunk + 4];  // a step's outputs, where they are written one by one
+  };
+  _Float16 hi[kTok * NG][kULd], lo[kTok * NG][kULd];
+  int32_t exp[kTok * NG];  // hi + lo = u 2^-exp
 };
-template <int W>
-struct BothShared : ExpandShared<W> {
-  float part[W][kTok][kPartLd];
+template <int NT, int W>
+struct BothShared : ExpandShared<1, W> {
+  Part<NT, 1, W> part;
 };
 
 __device__ __forceinline__ int key_of(const AdapterLaunch& a, int t) {
@@ -120,67 +130,90 @@ __device__ __forceinline__ int block_sum(int v, int32_t* tmp, int* total) {
   return base + x - v;
 }
 
+__device__ __forceinline__ int rank_of(const AdapterLaunch& a, int key) {
+  return key >= 0 ? min(max(*gptr(a.ad.rank + key), 0), a.ad.r_max) : 0;
+}
+
 // Tile x of up to kMidT tokens: counts of every adapter say which one tile x
 // belongs to, and the places of that adapter's tokens, in order, which of them
 // it has.  Every workgroup does this for itself, for less than a launch that
-// does it for all of them would take.
-template <int W>
-__device__ void find_tile_mid(const AdapterLaunch& a, int x, Tile& tile, FindShared<W>& sh) {
-  constexpr int kThreads = W * kWave, kKeys = kMidT / kThreads;
+// does it for all of them would take.  A wave holds the keys of tokens that
+// follow each other.
+template <int NG, int W>
+__device__ void find_tile_mid(const AdapterLaunch& a, int x, Tile<NG>& tile, FindShared<W>& sh) {
+  constexpr int kThreads = W * kWave, kKeys = kMidT / kThreads, kSize = kTok * NG;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int n = a.ad.n + 1;  // key 0: no adapter
+  const int keys = (a.T + kThreads - 1) / kThreads;  // of a lane
+  const int t0 = wave * keys * kWave + lane;
   int key[kKeys];
 #pragma unroll
   for (int i = 0; i < kKeys; ++i) {
-    const int t = i * kThreads + (int)threadIdx.x;
-    key[i] = t < a.T ? key_of(a, t) + 1 : -1;
+    const int t = t0 + i * kWave;
+    key[i] = i < keys && t < a.T ? key_of(a, t) + 1 : -1;
   }
   for (int i = threadIdx.x; i < n; i += kThreads) sh.hist[i] = 0;
   if (threadIdx.x == 0) tile.count = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) count_keys(sh.hist, key[i]);
+  for (int i = 0; i < kKeys; ++i)
+    if (i < keys) count_keys(sh.hist, key[i]);
   __syncthreads();
-  int tile0 = 0;
-  for (int i0 = 0; i0 < n && tile0 <= x; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    const int c = i < n ? sh.hist[i] : 0, tiles = (c + kTok - 1) / kTok;
-    int total;
-    const int at = tile0 + block_sum<W>(tiles, sh.scan, &total);
-    if (x >= at && x < at + tiles) {
-      tile.key = i - 1;
-      sh.first = (x - at) * kTok;
-      tile.count = min(c - (x - at) * kTok, kTok);
+  // every wave looks for the tile, 64 adapters at a time
+  int tile0 = 0, mine = -1, first = 0, count = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n && mine < 0; i0 += kWave) {
+    const int i = i0 + lane;
+    const int c = i < n ? sh.hist[i] : 0, tiles = (c + kSize - 1) / kSize;
+    int sum = tiles;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int y = __shfl_up(sum, o, kWave);
+      if (lane >= o) sum += y;
     }
-    tile0 += total;
+    const int at = tile0 + sum - tiles;
+    const uint64_t hit = __ballot(x >= at && x < at + tiles);
+    if (hit != 0) {
+      const int l = __builtin_ctzll(hit);
+      mine = i0 + l;
+      first = (x - __builtin_amdgcn_readlane(at, l)) * kSize;
+      count = min(__builtin_amdgcn_readlane(c, l) - first, kSize);
+    }
+    tile0 += __builtin_amdgcn_readlane(sum, kWave - 1);
   }
-  __syncthreads();
-  if (tile.count == 0) return;
-  const int mine = tile.key + 1;
-  uint64_t match[kKeys];
+  if (mine < 0) return;  // every wave leaves
+  const int r = rank_of(a, mine - 1);
+  const float scale = mine > 0 ? *gptr(a.ad.scale + mine - 1) : 0.0f;
+  int had = 0;  // this wave's tokens of the adapter
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
-    match[i] = __ballot(key[i] == mine);
-    if (lane == 0) sh.scan[i * W + wave] = __popcll(match[i]);
-  }
+  for (int i = 0; i < kKeys; ++i)
+    if (i < keys) had += __popcll(__ballot(key[i] == mine));
+  if (lane == 0) sh.scan[wave] = had;
   __syncthreads();
-  // places of the tokens of each wave's part, in the order of the tokens
-  const int v = threadIdx.x < kMidT / kWave ? sh.scan[threadIdx.x] : 0;
-  int total;
-  const int before = block_sum<W>(v, sh.scan + kMidT / kWave, &total);
-  if (threadIdx.x < kMidT / kWave) sh.scan[threadIdx.x] = before;
-  __syncthreads();
+  int at = -first;
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
-    const int at = sh.scan[i * W + wave] + __popcll(match[i] & ((1ull << lane) - 1)) - sh.first;
-    if (key[i] == mine && at >= 0 && at < kTok) tile.tok[at] = i * kThreads + (int)threadIdx.x;
+  for (int w = 0; w < W; ++w)
+    if (w < wave) at += sh.scan[w];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i)
+    if (i < keys) {
+      const uint64_t match = __ballot(key[i] == mine);
+      const int place = at + __popcll(match & ((1ull << lane) - 1));
+      if (key[i] == mine && place >= 0 && place < kSize) tile.tok[place] = t0 + i * kWave;
+      at += __popcll(match);
+    }
+  if (threadIdx.x == 0) {
+    tile.key = mine - 1;
+    tile.count = count;
+    tile.rank = r;
+    tile.scale = scale;
   }
   __syncthreads();
 }
 
 // Tile x of up to kSmallT tokens, by one wave: x stands for a token, which has
 // a tile if its place among those of its adapter is a multiple of 16.
-__device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, Tile& tile) {
+__device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, Tile<1>& tile) {
   if (threadIdx.x < kWave) {
     const int lane = threadIdx.x;
     int key[kSmallT / kWave];
@@ -193,6 +226,8 @@ __device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, T
 #pragma unroll
     for (int c = 0; c < kSmallT / kWave; ++c)
       if (c == x / kWave) mine = __builtin_amdgcn_readlane(key[c], x % kWave);
+    const int r = rank_of(a, mine);
+    const float scale = mine >= 0 ? *gptr(a.ad.scale + mine) : 0.0f;
     uint64_t match[kSmallT / kWave];
 #pragma unroll
     for (int c = 0; c < kSmallT / kWave; ++c) {
@@ -210,6 +245,8 @@ __device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, T
     if (lane == 0) {
       tile.key = mine;
       tile.count = x < a.T && place % kTok == 0 ? min(before - place, kTok) : 0;
+      tile.rank = r;
+      tile.scale = scale;
     }
   }
   __syncthreads();
@@ -229,35 +266,40 @@ __device__ __forceinline__ h8 row8(const _Float16* row, int d, int end) {
 }
 
 // This wave's share of U^T for ranks g0 .. g0 + 16 NT - 1 over the 64-element
-// chunks c0 + wave, + kWaves, ... below c1, into sh.part.
-template <int NT, int W>
-__device__ __forceinline__ void shrink(const AdapterLaunch& a, const Tile& tile, int r, int g0,
-                                       int c0, int c1, float (*part)[kTok][kPartLd]) {
-  constexpr int kAhead = NT == 1 ? 4 : 2;  // chunks whose loads are in flight together
+// chunks c0 + wave, + kWaves, ... below c1, into part.
+template <int NT, int NG, int W>
+__device__ __forceinline__ void shrink(const AdapterLaunch& a, const Tile<NG>& tile, int g0, int c0,
+                                       int c1, Part<NT, NG, W>& part) {
+  constexpr int kAhead = NG > 1 ? 1 : NT == 1 ? 4 : 2;  // chunks whose loads are in flight together
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const _Float16* x = a.X + (int64_t)tile.tok[min(r16, tile.count - 1)] * a.ldx;
+  const _Float16* x[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+    x[g] = a.X + (int64_t)tile.tok[min(g * kTok + r16, tile.count - 1)] * a.ldx;
   const _Float16* A = (const _Float16*)a.ad.A + tile.key * a.ad.stride_a;
   const _Float16* w[NT];
-  f4 u[NT];
+  f4 u[NG][NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    w[i] = A + (int64_t)min(g0 + 16 * i + r16, r - 1) * a.ad.lda;
-    u[i] = f4{0, 0, 0, 0};
+    w[i] = A + (int64_t)min(g0 + 16 * i + r16, tile.rank - 1) * a.ad.lda;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) u[g][i] = f4{0, 0, 0, 0};
   }
   const int full = min(c1, a.ad.d_in / kChunk);
   int c = c0 + wave;
 #pragma unroll 1
   for (; c + (kAhead - 1) * W < full; c += kAhead * W) {
-    h8 xv[kAhead][2], wv[kAhead][NT][2];
+    h8 xv[kAhead][2][NG], wv[kAhead][2][NT];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int d = (c + k * W) * kChunk + q4 * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        xv[k][h] = ld16<h8>(x + d + 32 * h);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) wv[k][i][h] = ld16<h8>(w[i] + d + 32 * h);
+        for (int g = 0; g < NG; ++g) xv[k][h][g] = ld16<h8>(x[g] + d + 32 * h);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) wv[k][h][i] = ld16<h8>(w[i] + d + 32 * h);
       }
     }
 #pragma unroll
@@ -266,27 +308,41 @@ __device__ __forceinline__ void shrink(const AdapterLaunch& a, const Tile& tile,
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          u[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[k][i][h], xv[k][h], u[i], 0, 0, 0);
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            u[g][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[k][h][i], xv[k][h][g], u[g][i], 0,
+                                                             0, 0);
   }
 #pragma unroll 1
   for (; c < c1; c += W) {  // what is left, and the piece at the end of the rows
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       const int d = c * kChunk + q4 * 8 + 32 * h;
-      const h8 xv = row8(x, d, a.ad.d_in);
+      h8 xv[NG];
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        u[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(row8(w[i], d, a.ad.d_in), xv, u[i], 0, 0, 0);
+      for (int g = 0; g < NG; ++g) xv[g] = row8(x[g], d, a.ad.d_in);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const h8 wv = row8(w[i], d, a.ad.d_in);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          u[g][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv[g], u[g][i], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i) *(f4*)&part[wave][r16][16 * i + 4 * q4] = u[i];
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *(f4*)&part.u[wave][g * kTok + r16][16 * i + 4 * q4] = u[g][i];
 }
-// sh.u to sh.hi + sh.lo, zeros from rank r to r32 on (some lanes per token).
-template <int W>
-__device__ __forceinline__ void halve_u(int r, int r32, ExpandShared<W>& sh) {
-  constexpr int kPer = W * kWave / kTok;
+
+// sh.u to sh.hi + sh.lo, zeros from the rank to the end of the blocks of 32 that
+// Expand takes (at least KS); some lanes per token.
+template <int KS, int NG, int W>
+__device__ __forceinline__ void halve_u(ExpandShared<NG, W>& sh) {
+  constexpr int kPer = W * kWave / (kTok * NG);
   const int tok = threadIdx.x / kPer, at = threadIdx.x % kPer;
+  const int r = sh.tile.rank, r32 = max((r + 31) / 32, KS) * 32;
   float top = 0.0f;
   for (int k = at; k < r; k += kPer) top = fmaxf(top, fabsf(sh.u[tok][k]));
 #pragma unroll
@@ -325,27 +381,24 @@ struct Row16 {
   }
 };
 
-// The second product: outputs of a tile, 64 per wave and step.  The operands
-// of a step (base, and B for the first KS blocks of 32 ranks) are loaded while
-// the one before it is worked on, and those of the first step before U is
-// known.
-template <typename YT, int KS, int W>
+// The second product: outputs of a tile, 64 per wave and step, one group of 16
+// tokens after the other.  What a group needs (base; B for the first KS blocks
+// of 32 ranks, kept for the groups of a step) is loaded while the one before
+// it is worked on, and the first one's before U is known.
+template <typename YT, int KS, int NG, int W>
 struct Expand {
   const AdapterLaunch& a;
-  ExpandShared<W>& sh;
+  ExpandShared<NG, W>& sh;
   const int r, j0, j1, steps, vec, wave, lane, r16, q4;
-  const bool mine;
-  const int64_t t;
   const _Float16* B;
   h8 wt[KS][4];
   Row16<YT> y;
 
-  __device__ __forceinline__ Expand(const AdapterLaunch& a_, ExpandShared<W>& sh_, int r_, int j0_,
+  __device__ __forceinline__ Expand(const AdapterLaunch& a_, ExpandShared<NG, W>& sh_, int j0_,
                                     int j1_, int vec_)
-      : a(a_), sh(sh_), r(r_), j0(j0_), j1(j1_), steps((j1_ - j0_ + kChunk - 1) / kChunk),
-        vec(vec_), wave(threadIdx.x / kWave), lane(threadIdx.x % kWave), r16(lane & 15),
-        q4(lane >> 4), mine(r16 < sh_.tile.count),
-        t(sh_.tile.tok[min(r16, sh_.tile.count - 1)]),
+      : a(a_), sh(sh_), r(sh_.tile.rank), j0(j0_), j1(j1_),
+        steps((j1_ - j0_ + kChunk - 1) / kChunk), vec(vec_), wave(threadIdx.x / kWave),
+        lane(threadIdx.x % kWave), r16(lane & 15), q4(lane >> 4),
         B((const _Float16*)a_.ad.B + max(sh_.tile.key, 0) * a_.ad.stride_b) {}
 
   // Steps start elsewhere in each tile: rows that lie a power of two apart
@@ -359,26 +412,35 @@ struct Expand {
   }
   // Whether the step's outputs are read and written in 16-byte pieces.
   __device__ __forceinline__ bool wide(int jb) const { return vec && jb + kChunk <= j1; }
-  __device__ __forceinline__ void load(int jb) {
+  __device__ __forceinline__ void load_w(int jb) {
     if (r > 0) {
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int m = 0; m < 4; ++m) wt[s][m] = weight(jb, m, s);
     }
-    // columns past the tile's tokens repeat the last one and are not stored
-    if (a.base && wide(jb)) y.load((const YT*)a.base + t * a.ldbase + jb, q4);
+  }
+  // Lanes past the tile's tokens repeat the last one and store nothing.
+  __device__ __forceinline__ int64_t token(int g) const {
+    return sh.tile.tok[min(g * kTok + r16, sh.tile.count - 1)];
+  }
+  __device__ __forceinline__ void load_y(int jb, int g) {
+    if (a.base && wide(jb)) y.load((const YT*)a.base + token(g) * a.ldbase + jb, q4);
   }
   __device__ __forceinline__ void load_first() {
-    if (wave < steps) load(place(wave));
+    if (wave < steps) {
+      load_w(place(wave));
+      load_y(place(wave), 0);
+    }
   }
   __device__ __forceinline__ void run() {
-    const float scale = r > 0 ? a.ad.scale[sh.tile.key] : 0.0f;
-    const int e = r > 0 ? sh.exp[r16] : 0;
+    const float scale = sh.tile.scale;
+    const int groups = (sh.tile.count + kTok - 1) / kTok;
     constexpr int kPer = Row16<YT>::kPer;
 #pragma unroll 1
-    for (int i = wave; i < steps; i += W) {
-      const int jb = place(i);
+    for (int i = wave, g = 0; i < steps;) {
+      const int jb = place(i), at = g * kTok;
+      const int e = r > 0 ? sh.exp[at + r16] : 0;
       f4 acc[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = f4{0, 0, 0, 0};
@@ -386,19 +448,19 @@ struct Expand {
       if (r > 0) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const h8 uh = *(const h8*)&sh.hi[r16][s * 32 + q4 * 8];
-          const h8 ul = *(const h8*)&sh.lo[r16][s * 32 + q4 * 8];
+          const h8 uh = *(const h8*)&sh.hi[at + r16][s * 32 + q4 * 8];
+          const h8 ul = *(const h8*)&sh.lo[at + r16][s * 32 + q4 * 8];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[s][m], uh, acc[m], 0, 0, 0);
             acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[s][m], ul, acc[m], 0, 0, 0);
           }
         }
-        if constexpr (KS == 2) {
+        if constexpr (KS == 2 && NG == 1) {
 #pragma unroll 1
           for (int s = KS; s * 32 < r; ++s) {
-            const h8 uh = *(const h8*)&sh.hi[r16][s * 32 + q4 * 8];
-            const h8 ul = *(const h8*)&sh.lo[r16][s * 32 + q4 * 8];
+            const h8 uh = *(const h8*)&sh.hi[at + r16][s * 32 + q4 * 8];
+            const h8 ul = *(const h8*)&sh.lo[at + r16][s * 32 + q4 * 8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const h8 x = weight(jb, m, s);
@@ -412,7 +474,14 @@ struct Expand {
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_ldexpf(acc[m][c], e);
       }
-      if (i + W < steps) load(place(i + W));
+      const int64_t t = token(g);
+      const bool mine = at + r16 < sh.tile.count;
+      if (++g == groups) {
+        g = 0;
+        i += W;
+        if (i < steps) load_w(place(i));
+      }
+      if (i < steps) load_y(place(i), g);
       if (wide(jb)) {
         Row16<YT> out;
 #pragma unroll
@@ -432,8 +501,8 @@ struct Expand {
         __builtin_amdgcn_wave_barrier();
         const int j = jb + lane;
 #pragma unroll 1
-        for (int k = 0; k < sh.tile.count; ++k) {
-          const int64_t row = sh.tile.tok[k];
+        for (int k = 0; k < min(sh.tile.count - at, kTok); ++k) {
+          const int64_t row = sh.tile.tok[at + k];
           if (j < j1) {
             const float b = a.base ? (float)*gptr((const YT*)a.base + row * a.ldbase + j) : 0.0f;
             const float v = sh.stage[wave][k][lane];
@@ -446,36 +515,31 @@ struct Expand {
   }
 };
 
-__device__ __forceinline__ int rank_of(const AdapterLaunch& a, int key) {
-  return key >= 0 ? min(max(a.ad.rank[key], 0), a.ad.r_max) : 0;
-}
-
-// One launch, for few tokens and r_max <= 16 NT: workgroup (x, y) computes U of
-// tile x, then chunk y of its outputs.
+// One launch, for few tokens and r_max <= 16 NT <= 32: workgroup (x, y)
+// computes U of tile x, then chunk y of its outputs.
 constexpr int kBothWaves = 8;
 template <typename YT, int NT>
 __global__ __launch_bounds__(kBothWaves* kWave, 2) void adapter_kernel(AdapterLaunch a, int chunk,
                                                                        int vec) {
   constexpr int W = kBothWaves;
-  __shared__ BothShared<W> sh;
+  __shared__ BothShared<NT, W> sh;
   find_tile_small(a, blockIdx.x, sh.tile);
   if (sh.tile.count == 0) return;
-  const int r = rank_of(a, sh.tile.key);
   const int j0 = blockIdx.y * chunk;
-  Expand<YT, 1, W> x(a, sh, r, j0, min(j0 + chunk, a.ad.d_out), vec);
+  Expand<YT, 1, 1, W> x(a, sh, j0, min(j0 + chunk, a.ad.d_out), vec);
   x.load_first();
-  if (r > 0) {
-    shrink<NT, W>(a, sh.tile, r, 0, 0, (a.ad.d_in + kChunk - 1) / kChunk, sh.part);
+  if (sh.tile.rank > 0) {
+    shrink<NT, 1, W>(a, sh.tile, 0, 0, (a.ad.d_in + kChunk - 1) / kChunk, sh.part);
     __syncthreads();
     for (int e = threadIdx.x; e < kTok * 16 * NT; e += W * kWave) {
       const int tok = e / (16 * NT), rank = e % (16 * NT);
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) v += sh.part[w][tok][rank];
+      for (int w = 0; w < W; ++w) v += sh.part.u[w][tok][rank];
       sh.u[tok][rank] = v;
     }
     __syncthreads();
-    halve_u<W>(r, (r + 31) / 32 * 32, sh);
+    halve_u<1, 1, W>(sh);
     __syncthreads();
   }
   x.run();
@@ -485,45 +549,51 @@ __global__ __launch_bounds__(kBothWaves* kWave, 2) void adapter_kernel(AdapterLa
 // tile into ws.tiles.  FIND: how a workgroup comes by its tile.
 constexpr int kShrinkWaves = 8;
 enum { kFindSmall, kFindMid, kFindPlanned };
-template <int FIND, int NT>
-__global__ __launch_bounds__(kShrinkWaves* kWave, 4) void shrink_kernel(AdapterLaunch a,
+template <int FIND, int NT, int NG>
+__global__ __launch_bounds__(kShrinkWaves* kWave, 2) void shrink_kernel(AdapterLaunch a,
                                                                         AdapterWs ws) {
   constexpr int W = kShrinkWaves;
-  __shared__ ShrinkShared<W> sh;
+  __shared__ ShrinkShared<NT, NG, W> sh;
   const int x = blockIdx.x;
+  if (threadIdx.x == 0) sh.tile.count = 0;
   if constexpr (FIND == kFindSmall) {
     find_tile_small(a, x, sh.tile);
   } else if constexpr (FIND == kFindMid) {
-    find_tile_mid<W>(a, x, sh.tile, sh.find);
+    find_tile_mid<NG, W>(a, x, sh.tile, sh.find);
   } else {
     const bool have = x < *ws.n_tiles;
     const int count = have ? ws.plan[3 * x + 1] : 0;
     if ((int)threadIdx.x < count) sh.tile.tok[threadIdx.x] = ws.perm[ws.plan[3 * x] + threadIdx.x];
     if (threadIdx.x == 0) {
-      sh.tile.key = have ? ws.plan[3 * x + 2] : -1;
+      const int key = have ? ws.plan[3 * x + 2] : -1;
+      sh.tile.key = key;
       sh.tile.count = count;
+      sh.tile.rank = rank_of(a, key);
+      sh.tile.scale = key >= 0 ? a.ad.scale[key] : 0.0f;
     }
-    __syncthreads();
   }
-  if (blockIdx.y == 0 && threadIdx.x < sizeof(Tile) / 4)
-    ((int32_t*)(ws.tiles + x))[threadIdx.x] = ((const int32_t*)&sh.tile)[threadIdx.x];
+  __syncthreads();
+  Tile<NG>* out = (Tile<NG>*)ws.tiles + x;
+  if (blockIdx.y == 0 && threadIdx.x < sizeof(Tile<NG>) / 4)
+    ((int32_t*)out)[threadIdx.x] = ((const int32_t*)&sh.tile)[threadIdx.x];
   if (sh.tile.count == 0) return;
-  const int r = rank_of(a, sh.tile.key);
+  const int r = sh.tile.rank;
   const int chunks = (a.ad.d_in + kChunk - 1) / kChunk;
   const int c0 = (int)((int64_t)chunks * blockIdx.y / ws.slices);
   const int c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / ws.slices);
 #pragma unroll 1
   for (int g0 = 0; g0 < r; g0 += 16 * NT) {
-    shrink<NT, W>(a, sh.tile, r, g0, c0, c1, sh.part);
+    shrink<NT, NG, W>(a, sh.tile, g0, c0, c1, sh.part);
     __syncthreads();
-    const int n = min(r - g0, 16 * NT);
-    for (int e = threadIdx.x; e < sh.tile.count * 16 * NT; e += W * kWave) {
-      const int tok = e / (16 * NT), rank = e % (16 * NT);
-      float v = 0.0f;
+    // four ranks at a time; rows of ws.u have room for whole fours
+    for (int e = threadIdx.x; e < sh.tile.count * 4 * NT; e += W * kWave) {
+      const int tok = e / (4 * NT), rank = e % (4 * NT) * 4;
+      f4 v = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < W; ++w) v += sh.part[w][tok][rank];
-      if (rank < n)
-        *gptr_w(ws.u + ((int64_t)blockIdx.y * a.T + sh.tile.tok[tok]) * ws.rank_ld + g0 + rank) = v;
+      for (int w = 0; w < W; ++w) v += *(const f4*)&sh.part.u[w][tok][rank];
+      if (g0 + rank < r)
+        *gptr_w((f4*)(ws.u + ((int64_t)blockIdx.y * a.T + sh.tile.tok[tok]) * ws.rank_ld + g0 +
+                      rank)) = v;
     }
     __syncthreads();
   }
@@ -531,31 +601,34 @@ __global__ __launch_bounds__(kShrinkWaves* kWave, 4) void shrink_kernel(AdapterL
 
 // Second: chunk blockIdx.y of the outputs of a tile.
 constexpr int kExpandWaves = 4;
-template <typename YT, int KS>
+template <typename YT, int KS, int NG>
 __global__ __launch_bounds__(kExpandWaves* kWave, 3) void expand_kernel(AdapterLaunch a,
                                                                         AdapterWs ws, int chunk,
                                                                         int vec) {
   constexpr int W = kExpandWaves;
-  __shared__ ExpandShared<W> sh;
-  if (threadIdx.x < sizeof(Tile) / 4)
-    ((int32_t*)&sh.tile)[threadIdx.x] = ((const int32_t*)(ws.tiles + blockIdx.x))[threadIdx.x];
+  __shared__ ExpandShared<NG, W> sh;
+  const Tile<NG>* in = (const Tile<NG>*)ws.tiles + blockIdx.x;
+  if (threadIdx.x < sizeof(Tile<NG>) / 4)
+    ((int32_t*)&sh.tile)[threadIdx.x] = ((const int32_t*)in)[threadIdx.x];
   __syncthreads();
   if (sh.tile.count == 0) return;
-  const int r = rank_of(a, sh.tile.key);
+  const int r = sh.tile.rank;
   const int j0 = blockIdx.y * chunk;
-  Expand<YT, KS, W> x(a, sh, r, j0, min(j0 + chunk, a.ad.d_out), vec);
+  Expand<YT, KS, NG, W> x(a, sh, j0, min(j0 + chunk, a.ad.d_out), vec);
   x.load_first();
   if (r > 0) {
-    for (int e = threadIdx.x; e < sh.tile.count * r; e += W * kWave) {
-      const int tok = e / r, rank = e % r;
+    const int fours = (r + 3) / 4;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < sh.tile.count * fours; e += W * kWave) {
+      const int tok = e / fours, rank = e % fours * 4;
       const float* p = ws.u + (int64_t)sh.tile.tok[tok] * ws.rank_ld + rank;
-      float v = 0.0f;
+      f4 v = {0, 0, 0, 0};
 #pragma unroll 4
-      for (int s = 0; s < ws.slices; ++s) v += *gptr(p + (int64_t)s * a.T * ws.rank_ld);
-      sh.u[tok][rank] = v;
+      for (int s = 0; s < ws.slices; ++s) v += *gptr((const f4*)(p + (int64_t)s * a.T * ws.rank_ld));
+      *(f4*)&sh.u[tok][rank] = v;
     }
     __syncthreads();
-    halve_u<W>(r, (r + 31) / 32 * 32, sh);
+    halve_u<KS, NG, W>(sh);
     __syncthreads();
   }
   x.run();
@@ -565,7 +638,8 @@ __global__ __launch_bounds__(kExpandWaves* kWave, 3) void expand_kernel(AdapterL
 // order of tokens within an adapter is free (a token's result does not depend
 // on its tile), so places are handed out by atomics.
 constexpr int kPlanWaves = 16;
-__global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a, AdapterWs ws) {
+__global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a, AdapterWs ws,
+                                                                 int size) {
   extern __shared__ int32_t place[];  // per adapter, and for no adapter: its count, then its place
   __shared__ int32_t tmp[kPlanWaves];
   const int n = a.ad.n + 1;
@@ -586,7 +660,7 @@ __global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a
     int tok0 = 0, tile0 = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanWaves * kWave) {
       const int i = i0 + (int)threadIdx.x;
-      const int c = i < n ? place[i] : 0, tiles = (c + kTok - 1) / kTok;
+      const int c = i < n ? place[i] : 0, tiles = (c + size - 1) / size;
       int st, sy;
       const int at_tok = tok0 + block_sum<kPlanWaves>(c, tmp, &st), at_tile = tile0 + block_sum<kPlanWaves>(tiles, tmp, &sy);
       tok0 += st;
@@ -594,8 +668,8 @@ __global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a
       if (i < n) {
         place[i] = at_tok;
         for (int k = 0; k < tiles; ++k) {
-          ws.plan[3 * (at_tile + k)] = at_tok + k * kTok;
-          ws.plan[3 * (at_tile + k) + 1] = min(c - k * kTok, kTok);
+          ws.plan[3 * (at_tile + k)] = at_tok + k * size;
+          ws.plan[3 * (at_tile + k) + 1] = min(c - k * size, size);
           ws.plan[3 * (at_tile + k) + 2] = i - 1;
         }
       }
@@ -607,32 +681,34 @@ __global__ __launch_bounds__(kPlanWaves* kWave) void plan_kernel(AdapterLaunch a
 
 // How a call is cut.
 struct Cut {
-  int tiles;   // workgroups of the tile axis
-  int chunk;   // outputs per workgroup
-  int slices;  // of K in a launch of its own; 0: one launch
+  int groups;    // of 16 tokens in a tile: 1 or kMany
+  int tiles;     // workgroups of the tile axis
+  int chunk;     // outputs per workgroup
+  int slices;    // of K in a launch of its own; 0: one launch
+  bool planned;  // whether a launch before finds the tiles
 };
 Cut get_cut(int32_t T, const dfs_adapters& ad) {
   Cut c;
+  // Tiles of 64 tokens read A and B a quarter as often, if adapters have that many.
+  c.groups = T > kSmallT && ad.r_max <= 64 && T >= 2 * kTok * (ad.n + 1) ? kMany : 1;
+  const int size = c.groups * kTok;
   // tiles that have work, at most
-  const int busy = (int)std::min<int64_t>(T, T / kTok + std::min<int64_t>(ad.n + 1, T));
+  const int busy = (int)std::min<int64_t>(T, T / size + std::min<int64_t>(ad.n + 1, T));
   c.tiles = T <= kSmallT ? (T + 7) / 8 * 8 : busy;
   const bool both =
       T <= kSmallT && ad.r_max <= 32 && (int64_t)ad.r_max * ad.d_in <= 256 * 1024;
   const int per = (both ? kBothWaves : kExpandWaves) * kChunk;  // outputs of one step
   const int most = (ad.d_out + per - 1) / per;
 #ifndef EC
-#define EC 2048
-#define SC 768
+#define EC 1024
+#define SC 384
 #endif
   const int chunks = std::max(1, std::min(most, (both ? 512 : EC) / busy));
   c.chunk = ((ad.d_out + chunks - 1) / chunks + kChunk - 1) / kChunk * kChunk;
-  const int k_most = (ad.d_in + kShrinkWaves * kChunk - 1) / (kShrinkWaves * kChunk);
+  const int k_most = (ad.d_in + 2 * kShrinkWaves * kChunk - 1) / (2 * kShrinkWaves * kChunk);
   c.slices = both ? 0 : std::max(1, std::min(k_most, SC / busy));
+  c.planned = T > kMidT || (T > kSmallT && ad.n > kMidN);
   return c;
-}
-
-bool planned(int32_t T, const dfs_adapters& ad) {
-  return T > kMidT || (T > kSmallT && ad.n > kMidN);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -642,22 +718,23 @@ struct Layout {
 };
 Layout get_layout(int32_t T, const dfs_adapters& ad, const Cut& c) {
   Layout l;
-  const bool plan = planned(T, ad);
-  l.plan = plan ? up((size_t)T * 4) : 0;
-  l.n = l.plan + (plan ? up((size_t)c.tiles * 12) : 0);
-  l.tiles = l.n + (plan ? 256 : 0);
-  l.u = l.tiles + (c.slices > 0 ? up((size_t)c.tiles * sizeof(Tile)) : 0);
+  l.plan = c.planned ? up((size_t)T * 4) : 0;
+  l.n = l.plan + (c.planned ? up((size_t)c.tiles * 12) : 0);
+  l.tiles = l.n + (c.planned ? 256 : 0);
+  const size_t tile = c.groups == 1 ? sizeof(Tile<1>) : sizeof(Tile<kMany>);
+  l.u = l.tiles + (c.slices > 0 ? up(c.tiles * tile) : 0);
   l.rank_ld = (ad.r_max + 3) / 4 * 4;
   l.total = l.u + (size_t)c.slices * T * l.rank_ld * 4;
   return l;
 }
 
-template <int FIND>
+template <int FIND, int NG>
 void go_shrink(const AdapterLaunch& a, const AdapterWs& w, const Cut& c, hipStream_t s) {
   const dim3 grid(c.tiles, c.slices), block(kShrinkWaves * kWave);
-  if (a.ad.r_max <= 16) hipLaunchKernelGGL((shrink_kernel<FIND, 1>), grid, block, 0, s, a, w);
-  else if (a.ad.r_max <= 32) hipLaunchKernelGGL((shrink_kernel<FIND, 2>), grid, block, 0, s, a, w);
-  else hipLaunchKernelGGL((shrink_kernel<FIND, 4>), grid, block, 0, s, a, w);
+  if (a.ad.r_max <= 16) hipLaunchKernelGGL((shrink_kernel<FIND, 1, NG>), grid, block, 0, s, a, w);
+  else if (a.ad.r_max <= 32)
+    hipLaunchKernelGGL((shrink_kernel<FIND, 2, NG>), grid, block, 0, s, a, w);
+  else hipLaunchKernelGGL((shrink_kernel<FIND, 4, NG>), grid, block, 0, s, a, w);
 }
 
 template <typename YT>
@@ -673,17 +750,25 @@ void go(const AdapterLaunch& a, const AdapterWs& w, const Cut& c, hipStream_t s)
       hipLaunchKernelGGL((adapter_kernel<YT, 2>), grid, block, 0, s, a, c.chunk, vec);
     return;
   }
-  if (w.planned)
+  if (c.planned)
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanWaves * kWave), (size_t)(a.ad.n + 1) * 4, s,
-                       a, w);
-  if (a.T <= kSmallT) go_shrink<kFindSmall>(a, w, c, s);
-  else if (!w.planned) go_shrink<kFindMid>(a, w, c, s);
-  else go_shrink<kFindPlanned>(a, w, c, s);
+                       a, w, c.groups * kTok);
+  if (a.T <= kSmallT) go_shrink<kFindSmall, 1>(a, w, c, s);
+  else if (!c.planned && c.groups == 1) go_shrink<kFindMid, 1>(a, w, c, s);
+  else if (!c.planned) go_shrink<kFindMid, kMany>(a, w, c, s);
+  else if (c.groups == 1) go_shrink<kFindPlanned, 1>(a, w, c, s);
+  else go_shrink<kFindPlanned, kMany>(a, w, c, s);
   const dim3 block(kExpandWaves * kWave);
-  if (a.ad.r_max <= 32)
-    hipLaunchKernelGGL((expand_kernel<YT, 1>), grid, block, 0, s, a, w, c.chunk, vec);
-  else
-    hipLaunchKernelGGL((expand_kernel<YT, 2>), grid, block, 0, s, a, w, c.chunk, vec);
+  auto second = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, w, c.chunk, vec);
+  };
+  if (c.groups == 1) {
+    if (a.ad.r_max <= 32) second(expand_kernel<YT, 1, 1>);
+    else second(expand_kernel<YT, 2, 1>);
+  } else {
+    if (a.ad.r_max <= 32) second(expand_kernel<YT, 1, kMany>);
+    else second(expand_kernel<YT, 2, kMany>);
+  }
 }
 
 }  // namespace
@@ -696,9 +781,9 @@ hipError_t launch_adapter(const AdapterLaunch& a, void* ws, hipStream_t s) {
   const Cut c = get_cut(a.T, a.ad);
   const Layout l = get_layout(a.T, a.ad, c);
   char* p = (char*)ws;
-  const AdapterWs w = {(int32_t*)p,          (int32_t*)(p + l.plan), (int32_t*)(p + l.n),
-                       (Tile*)(p + l.tiles), (float*)(p + l.u),      c.slices,
-                       planned(a.T, a.ad),   l.rank_ld};
+  const AdapterWs w = {(int32_t*)p, (int32_t*)(p + l.plan), (int32_t*)(p + l.n),
+                       p + l.tiles, (float*)(p + l.u),      c.slices,
+                       l.rank_ld};
   if (a.ydt == DFS_F16) go<_Float16>(a, w, c, s);
   else go<float>(a, w, c, s);
   return hipGetLastError();

@@ -119,6 +119,18 @@ def test_adapter_large_and_small_products():
         within(y, ref_y, bound, f"products of size {size}")
 
 
+def test_adapter_small_ranks_beside_large_ones():
+    """Ranks far below r_max, after a call that leaves NaN in the LDS of every CU."""
+    rng = np.random.default_rng(6)
+    ids = rng.integers(0, 3, 700)
+    ad, _ = make_adapters(rng, 3, 64, 256, 512, [64, 64, 64])
+    for T in (40, 700):
+        X = torch.full((T, 256), float("nan"), dtype=torch.float16, device=DEV)
+        B.dict_adapter_forward(X, ad, ints(ids[:T]))
+        check_adapter(T, 3, 64, 96, 512, "f16", [1, 3, 40], ids[:T])
+        check_adapter(T, 3, 256, 96, 128, "f32", [1, 17, 255], ids[:T])
+
+
 def test_adapter_no_tokens():
     rng = np.random.default_rng(1)
     ad, _ = make_adapters(rng, 1, 8, 64, 32, [8])
