@@ -57,6 +57,7 @@ struct AdapterWs {
 template <int W>
 struct FindShared {
   int32_t hist[kMidN + 1];  // tokens of no adapter, and of each
+  int16_t key[kMidT];       // 0: no adapter, -1: no token; a wave's tokens stand together
   int32_t scan[W];
   int32_t first;
 };
@@ -143,21 +144,22 @@ template <int NG, int W>
 __device__ void find_tile_mid(const AdapterLaunch& a, int x, Tile<NG>& tile, FindShared<W>& sh) {
   constexpr int kThreads = W * kWave, kKeys = kMidT / kThreads, kSize = kTok * NG;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int n = a.ad.n + 1;  // key 0: no adapter
+  const int n = a.ad.n + 1;
   const int keys = (a.T + kThreads - 1) / kThreads;  // of a lane
   const int t0 = wave * keys * kWave + lane;
-  int key[kKeys];
+  int16_t* mykey = sh.key + t0;
+  int id[kKeys];  // all loads at once, no branch between them
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
-    const int t = t0 + i * kWave;
-    key[i] = i < keys && t < a.T ? key_of(a, t) + 1 : -1;
-  }
+  for (int i = 0; i < kKeys; ++i) id[i] = *gptr(a.ids + min(t0 + i * kWave, a.T - 1));
   for (int i = threadIdx.x; i < n; i += kThreads) sh.hist[i] = 0;
-  if (threadIdx.x == 0) tile.count = 0;
-  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kKeys; ++i)
-    if (i < keys) count_keys(sh.hist, key[i]);
+    if (i < keys)
+      mykey[i * kWave] = (int16_t)(t0 + i * kWave >= a.T ? -1 : id[i] >= 0 && id[i] < a.ad.n ? id[i] + 1 : 0);
+  __syncthreads();
+  // (loops that are not unrolled: code that runs once costs its own fetch)
+#pragma unroll 1
+  for (int i = 0; i < keys; ++i) count_keys(sh.hist, mykey[i * kWave]);
   __syncthreads();
   // every wave looks for the tile, 64 adapters at a time
   int tile0 = 0, mine = -1, first = 0, count = 0;
@@ -185,23 +187,22 @@ __device__ void find_tile_mid(const AdapterLaunch& a, int x, Tile<NG>& tile, Fin
   const int r = rank_of(a, mine - 1);
   const float scale = mine > 0 ? *gptr(a.ad.scale + mine - 1) : 0.0f;
   int had = 0;  // this wave's tokens of the adapter
-#pragma unroll
-  for (int i = 0; i < kKeys; ++i)
-    if (i < keys) had += __popcll(__ballot(key[i] == mine));
+#pragma unroll 1
+  for (int i = 0; i < keys; ++i) had += __popcll(__ballot(mykey[i * kWave] == mine));
   if (lane == 0) sh.scan[wave] = had;
   __syncthreads();
   int at = -first;
 #pragma unroll
   for (int w = 0; w < W; ++w)
     if (w < wave) at += sh.scan[w];
-#pragma unroll
-  for (int i = 0; i < kKeys; ++i)
-    if (i < keys) {
-      const uint64_t match = __ballot(key[i] == mine);
-      const int place = at + __popcll(match & ((1ull << lane) - 1));
-      if (key[i] == mine && place >= 0 && place < kSize) tile.tok[place] = t0 + i * kWave;
-      at += __popcll(match);
-    }
+#pragma unroll 1
+  for (int i = 0; i < keys; ++i) {
+    const bool hit = mykey[i * kWave] == mine;
+    const uint64_t match = __ballot(hit);
+    const int place = at + __popcll(match & ((1ull << lane) - 1));
+    if (hit && place >= 0 && place < kSize) tile.tok[place] = t0 + i * kWave;
+    at += __popcll(match);
+  }
   if (threadIdx.x == 0) {
     tile.key = mine - 1;
     tile.count = count;
@@ -218,10 +219,11 @@ __device__ __forceinline__ void find_tile_small(const AdapterLaunch& a, int x, T
     const int lane = threadIdx.x;
     int key[kSmallT / kWave];
 #pragma unroll
-    for (int c = 0; c < kSmallT / kWave; ++c) {
-      const int t = c * kWave + lane;
-      key[c] = t < a.T ? key_of(a, t) : -2;
-    }
+    for (int c = 0; c < kSmallT / kWave; ++c)
+      key[c] = *gptr(a.ids + min(c * kWave + lane, a.T - 1));
+#pragma unroll
+    for (int c = 0; c < kSmallT / kWave; ++c)
+      key[c] = c * kWave + lane >= a.T ? -2 : key[c] >= 0 && key[c] < a.ad.n ? key[c] : -1;
     int mine = -2, place = 0, before = 0;
 #pragma unroll
     for (int c = 0; c < kSmallT / kWave; ++c)
@@ -699,14 +701,10 @@ Cut get_cut(int32_t T, const dfs_adapters& ad) {
       T <= kSmallT && ad.r_max <= 32 && (int64_t)ad.r_max * ad.d_in <= 256 * 1024;
   const int per = (both ? kBothWaves : kExpandWaves) * kChunk;  // outputs of one step
   const int most = (ad.d_out + per - 1) / per;
-#ifndef EC
-#define EC 1024
-#define SC 384
-#endif
-  const int chunks = std::max(1, std::min(most, (both ? 512 : EC) / busy));
+  const int chunks = std::max(1, std::min(most, (both ? 512 : 1024) / busy));
   c.chunk = ((ad.d_out + chunks - 1) / chunks + kChunk - 1) / kChunk * kChunk;
   const int k_most = (ad.d_in + 2 * kShrinkWaves * kChunk - 1) / (2 * kShrinkWaves * kChunk);
-  c.slices = both ? 0 : std::max(1, std::min(k_most, SC / busy));
+  c.slices = both ? 0 : std::max(1, std::min(k_most, 384 / busy));
   c.planned = T > kMidT || (T > kSmallT && ad.n > kMidN);
   return c;
 }
