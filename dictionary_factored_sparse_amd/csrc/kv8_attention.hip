@@ -24,9 +24,10 @@
 // w' = w * vscale / 2^E <= 2^15, E the running maximum of the exponents of
 // vscale, an exact power of two in which the sums are kept.
 //
-// Rounding.  w' is rounded to f16 for the second product: relative 2^-12,
-// below the f16 output's own rounding; for fp32 output it enters as the sum of
-// two f16 values.  Weights are kept at 2^13 times their value so that f16's
+// Rounding.  For prompts with f16 output w' is rounded to f16 for the second
+// product: errors of the size of the output's own rounding.  Otherwise (fp32
+// output, and few rows, where the matrix cores wait for memory anyway) it
+// enters as the sum of two f16 values.  Weights are kept at 2^13 times their value so that f16's
 // normal range reaches 2^-27 of the largest, and m is raised only when a score
 // passes it by more than 2 (weights stay below 2^15), which spares most
 // rescales of the sums.
@@ -121,16 +122,21 @@ __device__ __forceinline__ T block_scan(T v, T* tmp, T* total, int threads) {
 // Entries (request, block of qb query rows) in order and the first tile of
 // each, by one workgroup; first[entries] is the total.  Returns the entries:
 // at most `most`, which a tok_start that is not ascending could pass.
+// `extra` tiles stand for what an item costs besides its tiles.  facts: of the
+// requests, if there is room for them.
 template <typename T>  // of the entry counts: 256 requests of at most 256 entries fit int
-__device__ int make_plan(const KvAttnLaunch& a, int qb, int most, int64_t* first, int32_t* req,
-                         int32_t* qblk, int64_t* tmp, int threads) {
+__device__ int make_plan(const KvAttnLaunch& a, int qb, int extra, int most, int64_t* first,
+                         int32_t* req, int32_t* qblk, Req* facts, int64_t* tmp, int threads) {
   const int g = a.q_heads / a.kv.heads;
   int n_entries = 0;
   for (int r0 = 0; r0 < a.b.n_req; r0 += threads) {
     const int r = r0 + (int)threadIdx.x;
     int nb = 0;
-    if (r < a.b.n_req)
-      nb = (int)min<int64_t>(((int64_t)get_req(a.b, a.kv.page, r).n * g + qb - 1) / qb, most);
+    if (r < a.b.n_req) {
+      const Req q = get_req(a.b, a.kv.page, r);
+      if (facts) facts[r] = q;
+      nb = (int)min<int64_t>(((int64_t)q.n * g + qb - 1) / qb, most);
+    }
     T total;
     const T at = n_entries + block_scan<T>(nb, (T*)tmp, &total, threads);
     for (int i = 0; i < nb && at + i < most; ++i) {
@@ -145,10 +151,10 @@ __device__ int make_plan(const KvAttnLaunch& a, int qb, int most, int64_t* first
     const int e = e0 + (int)threadIdx.x;
     int64_t t = 0;
     if (e < n_entries) {
-      const Req q = get_req(a.b, a.kv.page, req[e]);
+      const Req q = facts ? facts[req[e]] : get_req(a.b, a.kv.page, req[e]);
       const int i0 = (int)((int64_t)qblk[e] * qb / g);
       const int i1 = (int)min<int64_t>(((int64_t)(qblk[e] + 1) * qb - 1) / g, q.n - 1);
-      t = (int64_t)get_span(q, q.len - q.n + i0, q.len - q.n + i1, a.window, a.sinks).n *
+      t = ((int64_t)get_span(q, q.len - q.n + i0, q.len - q.n + i1, a.window, a.sinks).n + extra) *
           a.kv.heads;
     }
     int64_t total;
@@ -162,9 +168,11 @@ __device__ int make_plan(const KvAttnLaunch& a, int qb, int most, int64_t* first
 }
 
 constexpr int kPlanThreads = 1024;
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvAttnLaunch a, AttnWs w, int qb) {
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvAttnLaunch a, AttnWs w, int qb,
+                                                            int extra) {
   __shared__ int64_t tmp[kPlanThreads / kWave];
-  const int n = make_plan<int64_t>(a, qb, w.max_entries, w.first, w.req, w.qblk, tmp, kPlanThreads);
+  const int n = make_plan<int64_t>(a, qb, extra, w.max_entries, w.first, w.req, w.qblk, nullptr, tmp,
+                                   kPlanThreads);
   if (threadIdx.x == 0) *w.n_entries = n;
 }
 
@@ -207,8 +215,9 @@ __device__ __forceinline__ f2 get2(const f2* p) {
                                                   __HIP_MEMORY_SCOPE_AGENT));
 }
 __device__ __forceinline__ void put4(float* p, f4 v) {
-  put2((f2*)p, f2{v.x, v.y});
-  put2((f2*)p + 1, f2{v.z, v.w});
+  // one store of device scope (there is no builtin of 16 bytes); the wait state
+  // keeps the next instruction off its operands
+  asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" ::"v"(p), "v"(v) : "memory");
 }
 __device__ __forceinline__ f4 get4(const float* p) {
   const f2 a = get2((const f2*)p), b = get2((const f2*)p + 1);
@@ -232,38 +241,71 @@ __device__ __forceinline__ bool arrive(uint32_t* count, int n, int* last) {
   return *last != 0;
 }
 
-// Sums v of four dims of a row over n parts, and the reference of their
-// weights with the sum of these; several parts' loads are in flight at once.
+// Joins n parts of an item: every thread calls put(row, dim, four sums,
+// reference of the weights and their sum) for its share of the rows.  ml and o
+// are indexed by slot(part) * stride + row.  E places of P parts each are in
+// flight at once: the loads go past the L2, so that their latency is what a
+// join costs.
 constexpr int kJoin = 8;
-template <int D, typename F>
-__device__ __forceinline__ f2 join(const f2* ml, const float* o, int rows, int row, int d, int n,
-                                   F slot, f4& v) {
-  float mm = -INFINITY, l = 0.0f;
-  v = f4{0, 0, 0, 0};
-  for (int b = 0; b < n; b += kJoin) {
-    f2 pm[kJoin];
-    f4 po[kJoin];
+template <int D, int E, typename F, typename G>
+__device__ __forceinline__ void join_by(const f2* ml, const float* o, int stride, int rows, int n,
+                                        F slot, G put) {
+  constexpr int P = kJoin / E;
+  const int places = rows * (D / 4);
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < places; i0 += E * kThreads) {
+    float mm[E], l[E];
+    f4 v[E];
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) {
-      const int64_t pr = slot(min(b + i, n - 1)) * rows + row;
-      pm[i] = get2(ml + pr);
-      po[i] = get4(o + pr * D + d);
+    for (int e = 0; e < E; ++e) {
+      mm[e] = -INFINITY;
+      l[e] = 0.0f;
+      v[e] = f4{0, 0, 0, 0};
     }
-    float mb = mm;
+#pragma unroll 1
+    for (int b = 0; b < n; b += P) {
+      f2 pm[E][P];
+      f4 po[E][P];
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) mb = fmaxf(mb, pm[i].x);
-    const float old = __builtin_amdgcn_exp2f(mm - mb);
-    l *= old;
-    v *= old;
-    mm = mb;
+      for (int e = 0; e < E; ++e) {
+        const int at = min(i0 + e * kThreads, places - 1);
+        const int row = at / (D / 4), d = at % (D / 4) * 4;
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) {
-      const float f = b + i < n ? __builtin_amdgcn_exp2f(pm[i].x - mb) : 0.0f;
-      l += pm[i].y * f;
-      v += po[i] * f;
+        for (int i = 0; i < P; ++i) {
+          const int64_t pr = slot(min(b + i, n - 1)) * stride + row;
+          pm[e][i] = get2(ml + pr);
+          po[e][i] = get4(o + pr * D + d);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float mb = mm[e];
+#pragma unroll
+        for (int i = 0; i < P; ++i) mb = fmaxf(mb, pm[e][i].x);
+        const float old = __builtin_amdgcn_exp2f(mm[e] - mb);
+        l[e] *= old;
+        v[e] *= old;
+        mm[e] = mb;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float f = b + i < n ? __builtin_amdgcn_exp2f(pm[e][i].x - mb) : 0.0f;
+          l[e] += pm[e][i].y * f;
+          v[e] += po[e][i] * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int at = i0 + e * kThreads;
+      if (at < places) put(at / (D / 4), at % (D / 4) * 4, v[e], f2{mm[e], l[e]});
     }
   }
-  return f2{mm, l};
+}
+template <int D, typename F, typename G>
+__device__ __forceinline__ void join(const f2* ml, const float* o, int stride, int rows, int n,
+                                     F slot, G put) {
+  if (n <= 2 && rows * (D / 4) > kThreads) join_by<D, 4>(ml, o, stride, rows, n, slot, put);
+  else join_by<D, 1>(ml, o, stride, rows, n, slot, put);
 }
 
 // Maximum and sum over the four lanes that hold one query row (lane % 16).
@@ -289,9 +331,13 @@ __device__ __forceinline__ int max4i(int v) {
 // SPLIT: the waves of a workgroup take the tiles of an item in turn, all for
 // the same NQ * 16 query rows (few rows, long caches).  Otherwise each wave
 // has NQ * 16 rows of its own and all take every tile (prompts).
-// HILO: the weights enter the second product as two f16 values.
-template <int KIND, int D, int NQ, bool SPLIT, bool HILO>
+template <int KIND, int D, int NQ, bool SPLIT, bool F32>
 struct Attn {
+  // the weights enter the second product as two f16 values
+  static constexpr bool HILO = SPLIT || F32;
+  // what an item costs besides its tiles, in tiles (see make_plan): its first
+  // reads and its results
+  static constexpr int kExtra = SPLIT ? 4 : 3;
   static constexpr int kRows = 16 * NQ;                      // per wave
   static constexpr int kQb = SPLIT ? kRows : kRows * kWaves;  // per item
   static constexpr int kSteps = D / 32;                      // first product, per key group
@@ -308,6 +354,7 @@ struct Attn {
     int last;
     int64_t first[kInlinePlan + 1];
     int32_t req[kInlinePlan], qblk[kInlinePlan];
+    Req facts[kInlinePlan];
   };
 
   // one wave's state
@@ -324,6 +371,7 @@ struct Attn {
 
   const KvAttnLaunch& a;
   const int lane, wave, r16, q4;
+  const bool wide;  // whether O takes four elements at once
   Req rq;
   Span sp;
   int kh, row0, nrows;      // this wave's first row of the request, its rows (may be <= 0)
@@ -332,7 +380,8 @@ struct Attn {
 
   __device__ __forceinline__ Attn(const KvAttnLaunch& a_)
       : a(a_), lane(threadIdx.x % kWave), wave(threadIdx.x / kWave), r16(lane & 15),
-        q4(lane >> 4) {}
+        q4(lane >> 4),
+        wide((uintptr_t)a_.O % (F32 ? 16 : 8) == 0 && a_.ldo % 4 == 0) {}
 
   __device__ __forceinline__ Pages load_pages(int u) const {
     const int kb = sp.tile(u) * kTile;
@@ -376,10 +425,10 @@ struct Attn {
     vs = *gptr(a.kv.vscale + ph);
   }
 
-  __device__ __forceinline__ void begin(int req, int qblk, int kh_) {
+  __device__ __forceinline__ void begin(const Req& facts, int req, int qblk, int kh_) {
     const int g = a.q_heads / a.kv.heads;
     kh = kh_;
-    rq = get_req(a.b, a.kv.page, req);
+    rq = facts;
     tab = a.b.table + (int64_t)req * a.b.ldt;
     const int rows = rq.n * g;  // < 2^31: n_tok rows of q_heads * head_dim elements exist
     const int item0 = qblk * kQb, item1 = min(item0 + kQb, rows);
@@ -457,7 +506,7 @@ struct Attn {
     pg1 = load_pages(after);
     const bool plain = kb + kTile - 1 <= pmin && kb + kTile <= rq.keys &&
                        (a.window <= 0 || pmax - kb < a.window || kb + kTile <= a.sinks) &&
-                       __ballot(!valid(pv)) == 0;
+                       __ballot(!valid(pv) || vscale == 0.0f) == 0;
     if (!plain) {
       const int j0 = kb + 16 * q4;
       // what some row of the wave sees
@@ -472,21 +521,28 @@ struct Attn {
           s[i][x >> 2][x & 3] = see >> x & 1u ? s[i][x >> 2][x & 3] * kscale : -INFINITY;
       }
       kscale = 1.0f;
-      if constexpr (KIND == DFS_FP8) {
-        // codes of keys that nobody sees may be NaN: make them 0
-        u4 keep;
+      // codes of keys that nobody sees may be NaN, and a scale of 0 makes 0 of
+      // any code
+      const uint32_t used = vscale == 0.0f ? 0u : any;
+      u4 keep;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          keep[w] = ((any >> (4 * w) & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
+      for (int w = 0; w < 4; ++w)
+        keep[w] = ((used >> (4 * w) & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
 #pragma unroll
-        for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
-      }
+      for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
     }
-    // value scales as (mantissa part) * 2^(ev): exact
+    // vscale = 2^(lv + ev): the exponent's maximum so far exactly, the rest as
+    // part of the weights' exponents (and out of their sums again).  Scales
+    // below 2^-64 of the largest count as that, which moves nothing and keeps
+    // their weights' sums normal.
     const int e_here = max4i(vscale > 0.0f ? __builtin_amdgcn_frexp_expf(vscale) : -126);
     const int e_new = max(ev, e_here);
-    float grow = __builtin_amdgcn_ldexpf(1.0f, max(ev - e_new, -300));
-    const float vf = __builtin_amdgcn_ldexpf(vscale, -e_new);
+    const float grow = __builtin_amdgcn_ldexpf(1.0f, max(ev - e_new, -300));
+    const float lv =
+        vscale > 0.0f
+            ? fmaxf(__builtin_amdgcn_logf(__builtin_amdgcn_ldexpf(vscale, -e_new)), -64.0f)
+            : 0.0f;
+    const float back = __builtin_amdgcn_exp2f(-lv);
     bool rescale = e_new != ev;
     ev = e_new;
     h8 w[NQ][2], wl[NQ][2];
@@ -498,23 +554,17 @@ struct Attn {
       for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[i][x >> 2][x & 3]);
       mx = max4(mx * kscale);
       const bool up = mx > m[i] + kSlack;
-      alpha[i] = grow;
-      if (up) {
-        const float f = __builtin_amdgcn_exp2f(m[i] - mx);
-        l[i] *= f;
-        alpha[i] *= f;
-        m[i] = mx;
-      }
+      const float f = up ? __builtin_amdgcn_exp2f(m[i] - mx) : 1.0f;
+      l[i] *= f;
+      alpha[i] = grow * f;
+      m[i] = up ? mx : m[i];
       rescale = rescale || up;
-      const float ref = m[i] - kWeightBits;
+      const float add = kWeightBits + lv - m[i];
       float sum = 0.0f;
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x >> 2][x & 3], kscale, -ref));
-        sum += p;
-        s[i][x >> 2][x & 3] = p * vf;
-      }
-      l[i] += sum;
+      for (int x = 0; x < 16; ++x)
+        s[i][x >> 2][x & 3] =
+            __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x >> 2][x & 3], kscale, add));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -529,8 +579,10 @@ struct Attn {
             wl[i][h][x] = lo.x;
             wl[i][h][x + 1] = lo.y;
           }
+          sum += p.x + p.y;
         }
       }
+      l[i] = __builtin_fmaf(sum, back, l[i]);
     }
     if (__ballot(rescale) != 0) {
 #pragma unroll
@@ -572,23 +624,29 @@ struct Attn {
     return (int64_t)(rq.t0 + tok) * a.ldo + (int64_t)h * D;
   }
   __device__ __forceinline__ void store(int64_t at, const f4& v, float l) const {
-    using T = typename std::conditional<HILO, float, _Float16>::type;
+    using T = typename std::conditional<F32, float, _Float16>::type;
     // rows that see nothing are 0; a sum that is NaN stays so
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    const T4 w = {(T)(v[0] * inv), (T)(v[1] * inv), (T)(v[2] * inv), (T)(v[3] * inv)};
+    if (wide) {
+      *gptr_w((T4*)((T*)a.O + at)) = w;
+    } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) *gptr_w((T*)a.O + at + c) = (T)(v[c] * inv);
+      for (int c = 0; c < 4; ++c) *gptr_w((T*)a.O + at + c) = w[c];
+    }
   }
 };
 
-template <int KIND, int D, int NQ, bool SPLIT, bool HILO>
+template <int KIND, int D, int NQ, bool SPLIT, bool F32>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_plan) {
-  using A = Attn<KIND, D, NQ, SPLIT, HILO>;
+  using A = Attn<KIND, D, NQ, SPLIT, F32>;
   __shared__ typename A::Shared sh;
   A t(a);
   const int n_entries =
-      inline_plan ? make_plan<int>(a, A::kQb, ws.max_entries, sh.first, sh.req, sh.qblk, sh.tmp,
-                                   kThreads)
+      inline_plan ? make_plan<int>(a, A::kQb, A::kExtra, ws.max_entries, sh.first, sh.req, sh.qblk,
+                                   sh.facts, sh.tmp, kThreads)
                   : *gptr(ws.n_entries);
   auto first = [&](int e) { return inline_plan ? sh.first[e] : *gptr(ws.first + e); };
   if (n_entries == 0) return;
@@ -608,14 +666,19 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
   for (int64_t x = xs; x < xe;) {
     while (first(e + 1) <= x) ++e;
     const int64_t fe = first(e);
-    const int n_tiles = (int)((first(e + 1) - fe) / a.kv.heads);
-    const int kh = (int)((x - fe) / n_tiles);
-    const int64_t item0 = fe + (int64_t)kh * n_tiles, item1 = item0 + n_tiles;
+    // an item is its tiles, and then the extra ones
+    const int n_line = (int)((first(e + 1) - fe) / a.kv.heads), n_tiles = n_line - A::kExtra;
+    const int kh = (int)((x - fe) / n_line);
+    const int64_t item0 = fe + (int64_t)kh * n_line, item1 = item0 + n_tiles;
+    if (x >= item1) {  // only extra ones are left of it
+      x = item0 + n_line;
+      continue;
+    }
     const int req = inline_plan ? sh.req[e] : *gptr(ws.req + e);
     const int qblk = inline_plan ? sh.qblk[e] : *gptr(ws.qblk + e);
     const int u0 = (int)(x - item0), u1 = (int)(min(item1, xe) - item0);
-    x = item0 + u1;
-    t.begin(req, qblk, kh);
+    x = u1 == n_tiles ? item0 + n_line : item0 + u1;
+    t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
     if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
     else if (t.nrows > 0) t.tiles(u0, u1, 1);
 #pragma unroll
@@ -692,28 +755,22 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
       // the first one of the others
       auto slot_of = [&](int w) { return 2 * (int64_t)w + (w == w0); };
       if (arrive(&ws.count[slot_of(g0)], g1 - g0 + 1, &sh.last)) {
-        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
-          const int row = idx / (D / 4), d = idx % (D / 4) * 4;
-          f4 v;
-          const f2 ml = join<D>(ws.part_ml, ws.part_o, A::kQb, row, d, g1 - g0 + 1,
-                                [&](int i) { return slot_of(g0 + i); }, v);
-          if (groups == 1) {
-            t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
-          } else {
-            const int64_t pr = slot_of(g0) * A::kQb + row;
-            put4(ws.part_o + pr * D + d, v);
-            if (d == 0) put2(ws.group_ml + pr, ml);
-          }
-        }
-        if (groups > 1 && arrive(&ws.count[2 * gridDim.x + w0], groups, &sh.last)) {
-          for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
-            const int row = idx / (D / 4), d = idx % (D / 4) * 4;
-            f4 v;
-            const f2 ml = join<D>(ws.group_ml, ws.part_o, A::kQb, row, d, groups,
-                                  [&](int i) { return slot_of(w0 + i * kJoin); }, v);
-            t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
-          }
-        }
+        join<D>(ws.part_ml, ws.part_o, A::kQb, rows, g1 - g0 + 1,
+                [&](int i) { return slot_of(g0 + i); }, [&](int row, int d, const f4& v, f2 ml) {
+                  if (groups == 1) {
+                    t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
+                  } else {
+                    const int64_t pr = slot_of(g0) * A::kQb + row;
+                    put4(ws.part_o + pr * D + d, v);
+                    if (d == 0) put2(ws.group_ml + pr, ml);
+                  }
+                });
+        if (groups > 1 && arrive(&ws.count[2 * gridDim.x + w0], groups, &sh.last))
+          join<D>(ws.group_ml, ws.part_o, A::kQb, rows, groups,
+                  [&](int i) { return slot_of(w0 + i * kJoin); },
+                  [&](int row, int d, const f4& v, f2 ml) {
+                    t.store(t.out_at(qblk * A::kQb + row) + d, v, ml.y);
+                  });
       }
     }
     __syncthreads();
@@ -762,7 +819,8 @@ Layout get_layout(const Cut& c, int D) {
 template <int KIND, int D, int NQ, bool SPLIT>
 void go(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
   const int in = c.entries <= kInlinePlan && a.b.n_req <= kInlinePlan;
-  if (!in) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w, c.qb);
+  if (!in) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w, c.qb,
+                              Attn<KIND, D, NQ, SPLIT, false>::kExtra);
   using A = Attn<KIND, D, NQ, SPLIT, false>;
   static_assert(A::kQb == (SPLIT ? 16 * NQ : 64 * NQ), "get_cut");
   const int least = SPLIT ? kWaves : 1;

@@ -491,8 +491,10 @@ dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_
  *   to no request are not written.  length below 0 counts as 0, and positions
  *   from table_pages * page on hold no key.
  * Scores, softmax statistics and sums are fp32.  The softmax weights enter
- * the second product as f16 for F16 output (their rounding is below that of
- * the output) and as the sum of two f16 values for F32 output.  Non-finite
+ * the second product as the sum of two f16 values, but for prompts (more than
+ * 32 rows of a request to a kv head on average) with F16 output as one, which
+ * errs by as much as the output's own rounding.  Scales are not negative.
+ * Non-finite
  * cache contents outside the visible positions do not reach the output.
  * The workspace's first 64 KiB must be zero before its first use; every call
  * leaves them zero again.  Calls sharing a workspace must not run
