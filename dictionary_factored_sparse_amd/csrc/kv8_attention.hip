@@ -80,6 +80,10 @@ __device__ __forceinline__ Req get_req(const KvBatch& b, int page, int r) {
   return q;
 }
 
+// A value that is the same in all lanes, as the compiler is to know: addresses
+// and bounds made of it then cost scalar instructions.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // Tiles that some row of an entry sees: the first `ns` tiles hold first
 // tokens, the others run from tile `ta`.
 struct Span {
@@ -331,7 +335,9 @@ __device__ __forceinline__ int max4i(int v) {
 // SPLIT: the waves of a workgroup take the tiles of an item in turn, all for
 // the same NQ * 16 query rows (few rows, long caches).  Otherwise each wave
 // has NQ * 16 rows of its own and all take every tile (prompts).
-template <int KIND, int D, int NQ, bool SPLIT, bool F32>
+// BIG: a tile lies in one page (pages of 64 or 128 tokens), whose address and
+// scales are then the same for all lanes.
+template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
 struct Attn {
   // the weights enter the second product as two f16 values
   static constexpr bool HILO = SPLIT || F32;
@@ -379,7 +385,7 @@ struct Attn {
   const int32_t* tab;
 
   __device__ __forceinline__ Attn(const KvAttnLaunch& a_)
-      : a(a_), lane(threadIdx.x % kWave), wave(threadIdx.x / kWave), r16(lane & 15),
+      : a(a_), lane(threadIdx.x % kWave), wave(uni(threadIdx.x / kWave)), r16(lane & 15),
         q4(lane >> 4),
         wide((uintptr_t)a_.O % (F32 ? 16 : 8) == 0 && a_.ldo % 4 == 0) {}
 
@@ -387,8 +393,16 @@ struct Attn {
     const int kb = sp.tile(u) * kTile;
     const int sh = __builtin_ctz(a.kv.page);
     const int last = a.b.table_pages - 1;
+    if constexpr (BIG) {
+      const int pg = *gptr(tab + min(kb >> sh, last));
+      return {pg, pg};
+    }
     return {*gptr(tab + min((kb + 16 * (r16 >> 2)) >> sh, last)),
             *gptr(tab + min((kb + 16 * q4) >> sh, last))};
+  }
+  // Pages that have arrived.
+  static __device__ __forceinline__ Pages settle(Pages p) {
+    return BIG ? Pages{uni(p.k), uni(p.v)} : p;
   }
   // A page that is none is read as page 0 and masked.
   __device__ __forceinline__ bool valid(int pg) const { return pg >= 0 && pg < a.kv.n_pages; }
@@ -399,23 +413,30 @@ struct Attn {
     const int kb = sp.tile(u) * kTile;
     const int P = a.kv.page;
     const int pg = valid(pg0.k) ? pg0.k : 0;
-    const int64_t at = (((int64_t)pg * a.kv.heads + kh) * P + ((kb + 16 * (r16 >> 2)) & (P - 1)) +
-                        (r16 & 3)) * D + q4 * 16;
-    const uint8_t* base = a.kv.k + (real ? at : 0);
+    const uint8_t* base = a.kv.k;
+    uint32_t off = 0;  // of this lane
+    if constexpr (BIG) {
+      base += (((int64_t)pg * a.kv.heads + kh) * P + (kb & (P - 1))) * D;
+      off = real ? (16 * (r16 >> 2) + (r16 & 3)) * D + q4 * 16 : 0;
+    } else {
+      const int64_t at = (((int64_t)pg * a.kv.heads + kh) * P + ((kb + 16 * (r16 >> 2)) & (P - 1)) +
+                          (r16 & 3)) * D + q4 * 16;
+      base += real ? at : 0;
+    }
     const int q8 = real ? 8 * q4 : 0;
 #pragma unroll
     for (int mm = 0; mm < 4; ++mm) {
       const uint8_t* p = base + 4 * mm * D;
 #pragma unroll
       for (int c = 0; c < kWide; ++c) {
-        const u4 w = ld16<u4>(p + 64 * c);
+        const u4 w = ld16<u4>(p + off + 64 * c);
         kraw[mm][4 * c] = w.x;
         kraw[mm][4 * c + 1] = w.y;
         kraw[mm][4 * c + 2] = w.z;
         kraw[mm][4 * c + 3] = w.w;
       }
       if constexpr (D % 64 != 0) {
-        const u2 w = *gptr((const u2*)(p + 64 * kWide - q8));
+        const u2 w = *gptr((const u2*)(p + off + 64 * kWide - q8));
         kraw[mm][4 * kWide] = w.x;
         kraw[mm][4 * kWide + 1] = w.y;
       }
@@ -428,7 +449,7 @@ struct Attn {
   __device__ __forceinline__ void begin(const Req& facts, int req, int qblk, int kh_) {
     const int g = a.q_heads / a.kv.heads;
     kh = kh_;
-    rq = facts;
+    rq = {uni(facts.t0), uni(facts.n), uni(facts.len), uni(facts.keys)};
     tab = a.b.table + (int64_t)req * a.b.ldt;
     const int rows = rq.n * g;  // < 2^31: n_tok rows of q_heads * head_dim elements exist
     const int item0 = qblk * kQb, item1 = min(item0 + kQb, rows);
@@ -481,11 +502,17 @@ struct Attn {
     const int P = a.kv.page, pv = pg0.v;
     u4 vraw[kDims];
     {
-      const uint8_t* base =
-          a.kv.v + (((int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh) * D + r16) * P +
-          ((kb + 16 * q4) & (P - 1));
+      const int64_t ph = (int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh;
+      const uint8_t* base = a.kv.v + ph * D * P;
+      uint32_t off = r16 * P + 16 * q4;
+      if constexpr (BIG) {
+        base += kb & (P - 1);
+      } else {
+        base += off + (((kb + 16 * q4) & (P - 1)) - 16 * q4);
+        off = 0;
+      }
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) vraw[d] = ld16<u4>(base + d * 16 * P);
+      for (int d = 0; d < kDims; ++d) vraw[d] = ld16<u4>(base + d * 16 * P + off);
     }
     f4 s[NQ][4];
 #pragma unroll
@@ -501,7 +528,7 @@ struct Attn {
       }
     }
     float kscale = ks * (a.sm_scale * kLog2e), vscale = vs;
-    pg0 = pg1;
+    pg0 = settle(pg1);
     load_k(next, more);
     pg1 = load_pages(after);
     const bool plain = kb + kTile - 1 <= pmin && kb + kTile <= rq.keys &&
@@ -610,7 +637,7 @@ struct Attn {
   __device__ __forceinline__ void tiles(int u0, int u1, int step) {
     if (u0 >= u1) return;
     const int last = u0 + (u1 - 1 - u0) / step * step;
-    pg0 = load_pages(u0);
+    pg0 = settle(load_pages(u0));
     pg1 = load_pages(min(u0 + step, last));
     load_k(u0, true);
     for (int u = u0; u <= last; u += step)
@@ -638,10 +665,10 @@ struct Attn {
   }
 };
 
-template <int KIND, int D, int NQ, bool SPLIT, bool F32>
+template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_plan) {
-  using A = Attn<KIND, D, NQ, SPLIT, F32>;
+  using A = Attn<KIND, D, NQ, SPLIT, F32, BIG>;
   __shared__ typename A::Shared sh;
   A t(a);
   const int n_entries =
@@ -667,16 +694,16 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
     while (first(e + 1) <= x) ++e;
     const int64_t fe = first(e);
     // an item is its tiles, and then the extra ones
-    const int n_line = (int)((first(e + 1) - fe) / a.kv.heads), n_tiles = n_line - A::kExtra;
-    const int kh = (int)((x - fe) / n_line);
+    const int n_line = uni((int)((first(e + 1) - fe) / a.kv.heads)), n_tiles = n_line - A::kExtra;
+    const int kh = uni((int)((x - fe) / n_line));
     const int64_t item0 = fe + (int64_t)kh * n_line, item1 = item0 + n_tiles;
     if (x >= item1) {  // only extra ones are left of it
       x = item0 + n_line;
       continue;
     }
-    const int req = inline_plan ? sh.req[e] : *gptr(ws.req + e);
-    const int qblk = inline_plan ? sh.qblk[e] : *gptr(ws.qblk + e);
-    const int u0 = (int)(x - item0), u1 = (int)(min(item1, xe) - item0);
+    const int req = uni(inline_plan ? sh.req[e] : *gptr(ws.req + e));
+    const int qblk = uni(inline_plan ? sh.qblk[e] : *gptr(ws.qblk + e));
+    const int u0 = uni((int)(x - item0)), u1 = uni((int)(min(item1, xe) - item0));
     x = u1 == n_tiles ? item0 + n_line : item0 + u1;
     t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
     if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
@@ -819,17 +846,22 @@ Layout get_layout(const Cut& c, int D) {
 template <int KIND, int D, int NQ, bool SPLIT>
 void go(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
   const int in = c.entries <= kInlinePlan && a.b.n_req <= kInlinePlan;
+  using A = Attn<KIND, D, NQ, SPLIT, false, false>;
   if (!in) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w, c.qb,
-                              Attn<KIND, D, NQ, SPLIT, false>::kExtra);
-  using A = Attn<KIND, D, NQ, SPLIT, false>;
+                              A::kExtra);
   static_assert(A::kQb == (SPLIT ? 16 * NQ : 64 * NQ), "get_cut");
   const int least = SPLIT ? kWaves : 1;
-  if (a.odt == DFS_F32)
-    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, true>), dim3(c.slices), dim3(kThreads),
-                       0, s, a, w, least, c.slices, in);
-  else
-    hipLaunchKernelGGL((attn_kernel<KIND, D, NQ, SPLIT, false>), dim3(c.slices), dim3(kThreads),
-                       0, s, a, w, least, c.slices, in);
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(c.slices), dim3(kThreads), 0, s, a, w, least, c.slices, in);
+  };
+  const bool big = a.kv.page >= kTile;
+  if (a.odt == DFS_F32) {
+    if (big) run(attn_kernel<KIND, D, NQ, SPLIT, true, true>);
+    else run(attn_kernel<KIND, D, NQ, SPLIT, true, false>);
+  } else {
+    if (big) run(attn_kernel<KIND, D, NQ, SPLIT, false, true>);
+    else run(attn_kernel<KIND, D, NQ, SPLIT, false, false>);
+  }
 }
 template <int KIND, int D>
 void go_d(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s) {
