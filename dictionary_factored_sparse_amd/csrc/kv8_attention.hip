@@ -51,6 +51,7 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 64;                // keys per tile
 constexpr int kInlinePlan = 256;         // entries up to which every workgroup plans for itself
 constexpr int kCounterBytes = 65536;     // per-slice counters at the start of the workspace
+constexpr int kWhole = 8;                // tiles up to which an item of a prompt is not split
 constexpr float kWeightBits = 13.0f;     // weights are held at 2^13 times their value
 constexpr float kSlack = 2.0f;           // the running maximum may lag by this (log2)
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -60,7 +61,7 @@ struct AttnWs {
   int64_t* first;    // plan: first tile of each entry, then the total
   int32_t* req;      // plan: request of each entry
   int32_t* qblk;     // plan: its block of query rows
-  int32_t* n_entries;
+  int32_t* n_entries;  // plan: entries, and the most tiles of an item
   int32_t max_entries;
   float* part_o;     // [2 * slices][rows][D]
   f2* part_ml;       // [2 * slices][rows]: reference of the weights, their sum
@@ -124,13 +125,14 @@ __device__ __forceinline__ T block_scan(T v, T* tmp, T* total, int threads) {
 }
 
 // Entries (request, block of qb query rows) in order and the first tile of
-// each, by one workgroup; first[entries] is the total.  Returns the entries:
+// each, by one workgroup; first[entries] is the total, *longest the most tiles
+// that an item has.  Returns the entries:
 // at most `most`, which a tok_start that is not ascending could pass.
 // `extra` tiles stand for what an item costs besides its tiles.  facts: of the
 // requests, if there is room for them.
 template <typename T>  // of the entry counts: 256 requests of at most 256 entries fit int
 __device__ int make_plan(const KvAttnLaunch& a, int qb, int extra, int most, int64_t* first,
-                         int32_t* req, int32_t* qblk, Req* facts, int64_t* tmp, int threads) {
+                         int32_t* req, int32_t* qblk, Req* facts, int32_t* longest, int64_t* tmp, int threads) {
   const int g = a.q_heads / a.kv.heads;
   int n_entries = 0;
   for (int r0 = 0; r0 < a.b.n_req; r0 += threads) {
@@ -151,6 +153,8 @@ __device__ int make_plan(const KvAttnLaunch& a, int qb, int extra, int most, int
   }
   __syncthreads();
   int64_t base = 0;
+  int most_tiles = 0;
+  if (threadIdx.x == 0) *longest = 0;
   for (int e0 = 0; e0 < n_entries; e0 += threads) {
     const int e = e0 + (int)threadIdx.x;
     int64_t t = 0;
@@ -158,8 +162,9 @@ __device__ int make_plan(const KvAttnLaunch& a, int qb, int extra, int most, int
       const Req q = facts ? facts[req[e]] : get_req(a.b, a.kv.page, req[e]);
       const int i0 = (int)((int64_t)qblk[e] * qb / g);
       const int i1 = (int)min<int64_t>(((int64_t)(qblk[e] + 1) * qb - 1) / g, q.n - 1);
-      t = ((int64_t)get_span(q, q.len - q.n + i0, q.len - q.n + i1, a.window, a.sinks).n + extra) *
-          a.kv.heads;
+      const int tiles = get_span(q, q.len - q.n + i0, q.len - q.n + i1, a.window, a.sinks).n;
+      most_tiles = max(most_tiles, tiles);
+      t = ((int64_t)tiles + extra) * a.kv.heads;
     }
     int64_t total;
     const int64_t at = base + block_scan<int64_t>(t, tmp, &total, threads);
@@ -167,6 +172,7 @@ __device__ int make_plan(const KvAttnLaunch& a, int qb, int extra, int most, int
     base += total;
   }
   if (threadIdx.x == 0) first[n_entries] = base;
+  if (most_tiles > 0) atomicMax(longest, most_tiles);
   __syncthreads();
   return n_entries;
 }
@@ -175,9 +181,13 @@ constexpr int kPlanThreads = 1024;
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvAttnLaunch a, AttnWs w, int qb,
                                                             int extra) {
   __shared__ int64_t tmp[kPlanThreads / kWave];
-  const int n = make_plan<int64_t>(a, qb, extra, w.max_entries, w.first, w.req, w.qblk, nullptr, tmp,
-                                   kPlanThreads);
-  if (threadIdx.x == 0) *w.n_entries = n;
+  __shared__ int32_t longest;
+  const int n = make_plan<int64_t>(a, qb, extra, w.max_entries, w.first, w.req, w.qblk, nullptr, &longest,
+                                   tmp, kPlanThreads);
+  if (threadIdx.x == 0) {
+    w.n_entries[0] = n;
+    w.n_entries[1] = longest;
+  }
 }
 
 // Eight codes to f16, exactly.
@@ -358,6 +368,7 @@ struct Attn {
     float m[kWaves][kRows], l[kWaves][kRows];
     int e[kWaves];
     int last;
+    int32_t longest;
     int64_t first[kInlinePlan + 1];
     int32_t req[kInlinePlan], qblk[kInlinePlan];
     Req facts[kInlinePlan];
@@ -673,7 +684,7 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
   A t(a);
   const int n_entries =
       inline_plan ? make_plan<int>(a, A::kQb, A::kExtra, ws.max_entries, sh.first, sh.req, sh.qblk,
-                                   sh.facts, sh.tmp, kThreads)
+                                   sh.facts, &sh.longest, sh.tmp, kThreads)
                   : *gptr(ws.n_entries);
   auto first = [&](int e) { return inline_plan ? sh.first[e] : *gptr(ws.first + e); };
   if (n_entries == 0) return;
@@ -690,6 +701,12 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
     e += (below - 1) * stride;
     n = min(stride, n_entries - e);
   }
+  // Items of few tiles are not split: a slice then takes those that start in it,
+  // whole.  A part and its join cost as much as some tiles (four prompts of 500
+  // tokens, 8 tiles at most: 46 us split, 38 us whole; windows of 512 tokens, 11
+  // tiles: 70 us split, 82 us whole).
+  const bool keep =
+      !SPLIT && uni(inline_plan ? sh.longest : *gptr(ws.n_entries + 1)) <= kWhole;
   for (int64_t x = xs; x < xe;) {
     while (first(e + 1) <= x) ++e;
     const int64_t fe = first(e);
@@ -697,13 +714,13 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
     const int n_line = uni((int)((first(e + 1) - fe) / a.kv.heads)), n_tiles = n_line - A::kExtra;
     const int kh = uni((int)((x - fe) / n_line));
     const int64_t item0 = fe + (int64_t)kh * n_line, item1 = item0 + n_tiles;
-    if (x >= item1) {  // only extra ones are left of it
+    if (keep ? x > item0 : x >= item1) {  // another slice's, or only extra ones are left of it
       x = item0 + n_line;
       continue;
     }
     const int req = uni(inline_plan ? sh.req[e] : *gptr(ws.req + e));
     const int qblk = uni(inline_plan ? sh.qblk[e] : *gptr(ws.qblk + e));
-    const int u0 = uni((int)(x - item0)), u1 = uni((int)(min(item1, xe) - item0));
+    const int u0 = uni((int)(x - item0)), u1 = uni(keep ? n_tiles : (int)(min(item1, xe) - item0));
     x = u1 == n_tiles ? item0 + n_line : item0 + u1;
     t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
     if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
