@@ -13,6 +13,7 @@
 // What bounds it: prompts, the bytes (source read, codes written); single
 // tokens, the chain of dependent reads (requests, page table, scale).
 #include <algorithm>
+#include <type_traits>
 
 #include "dfs_internal.hpp"
 
@@ -76,6 +77,25 @@ __device__ __forceinline__ float tamed(float v) {
   return v != v ? 0.0f : __builtin_amdgcn_fmed3f(v, -65504.0f, 65504.0f);
 }
 
+typedef uint16_t us8 __attribute__((ext_vector_type(8)));
+// Running maxima of sizes as bits (their order is the values'), f16 in pairs.
+template <typename T>
+struct Tops {
+  typename std::conditional<sizeof(T) == 2, us8, u4>::type m = 0;
+  // fp32 bits; NaN and infinities come out above kTop
+  __device__ __forceinline__ uint32_t bits() const {
+    if constexpr (sizeof(T) == 2) {
+      uint16_t h = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h = max(h, m[i]);
+      return h >= 0x7C00 ? 0x7F800000u
+                         : __float_as_uint((float)__builtin_bit_cast(_Float16, h));
+    } else {
+      return m[0];
+    }
+  }
+};
+
 // 16 bytes of source elements.
 template <typename T>
 struct Piece {
@@ -90,12 +110,16 @@ struct Piece {
       for (int i = 0; i < kN; ++i) v[i] = *gptr(p + i);
     }
   }
-  // the largest size's bits; NaN and infinities come out above kTop
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0;
+  // Folds the sizes' bits into m; Tops turns them into fp32 bits.
+  __device__ __forceinline__ void fold(Tops<T>& t) const {
+    if constexpr (sizeof(T) == 2) {
+      const us8 b = __builtin_bit_cast(us8, v) & (uint16_t)0x7FFF;
+      t.m = __builtin_elementwise_max(t.m, b);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) m = max(m, __float_as_uint((float)v[i]) & 0x7FFFFFFFu);
-    return m;
+      for (int i = 0; i < kN; ++i)
+        t.m[0] = max(t.m[0], __float_as_uint((float)v[i]) & 0x7FFFFFFFu);
+    }
   }
   __device__ __forceinline__ float at(int i, bool tame) const {
     return tame ? tamed((float)v[i]) : (float)v[i];
@@ -171,8 +195,9 @@ struct Item {
       if (s0 + i >= lo && s0 + i < hi) x[i].load(src + (s0 + i) * ld, vec);
     }
   }
-  __device__ __forceinline__ uint32_t top() const {
-    return max(max(x[0].top(), x[1].top()), max(x[2].top(), x[3].top()));
+  __device__ __forceinline__ void fold(Tops<T>& t) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i].fold(t);
   }
 };
 
@@ -207,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b,
   auto slot_of = [&](int e) { return 4 * (w0 + e / per_row); };
   auto dim_of = [&](int e) { return e % per_row * kN; };
   Item<T> k0, v0;
-  uint32_t ktop = 0, vtop = 0;
+  Tops<T> kt, vt;
   if ((int)threadIdx.x < items) {
     const int s0 = slot_of(threadIdx.x), d = dim_of(threadIdx.x);
     k0.load(ksrc + d, ldk, s0, lo, hi, vec);
@@ -225,8 +250,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b,
       was0 = *gptr((uint32_t*)(kv.v + (ph * D + (int)threadIdx.x / (w1 - w0)) * P) + w);
   }
   if ((int)threadIdx.x < items) {
-    ktop = k0.top();
-    vtop = v0.top();
+    k0.fold(kt);
+    v0.fold(vt);
   }
 #pragma unroll 1
   for (int e = threadIdx.x + kThreads; e < items; e += kThreads) {
@@ -234,9 +259,10 @@ __global__ __launch_bounds__(kThreads) void append_kernel(dfs_kv8 kv, KvBatch b,
     Item<T> x, y;
     x.load(ksrc + d, ldk, s0, lo, hi, vec);
     y.load(vsrc + d, ldv, s0, lo, hi, vec);
-    ktop = max(ktop, x.top());
-    vtop = max(vtop, y.top());
+    x.fold(kt);
+    y.fold(vt);
   }
+  uint32_t ktop = kt.bits(), vtop = vt.bits();
   block_max(ktop, vtop, red);
   const bool tame = max(ktop, vtop) > kTop;
   if (tame) {  // something is not finite or too large: once more, with what it counts as
