@@ -27,10 +27,10 @@
 // Rounding.  For prompts with f16 output w' is rounded to f16 for the second
 // product: errors of the size of the output's own rounding.  Otherwise (fp32
 // output, and few rows, where the matrix cores wait for memory anyway) it
-// enters as the sum of two f16 values.  Weights are kept at 2^13 times their value so that f16's
-// normal range reaches 2^-27 of the largest, and m is raised only when a score
-// passes it by more than 2 (weights stay below 2^15), which spares most
-// rescales of the sums.
+// enters as the sum of two f16 values.  Weights are kept at 2^13 times their
+// value so that f16's normal range reaches 2^-27 of the largest, and m is
+// raised only when a score passes it by more than 2 (weights stay below 2^15),
+// which spares most rescales of the sums.
 //
 // Work split.  The tiles of 64 keys of all items (request, block of query
 // rows, kv head) form one line, cut into equal slices, one per workgroup: the
@@ -38,6 +38,18 @@
 // long request loads every CU alike.  An item that lies in several slices is
 // joined by the workgroup that finishes last, in slice order, so results do
 // not depend on which that is.
+//
+// What bounds it, as measured (head_dim 128 unless stated).  Decode: the codes,
+// read once.  32 requests of 80 to 8192 tokens, 32 heads: 190 us for 1.05 GB,
+// 5.5 TB/s (a plain read of 1 GiB: 5.84); 4 tokens over 131071, 8 kv heads for
+// 32: 64 us, 4.2 TB/s; 24 int8 requests under a window of 4096, pages of 16: 47
+// us, 4.2 TB/s; these two end with a join.  One request of 777 tokens: 10.4 us,
+// chain of plan, pages, codes, join.  Prompts: vector instructions (conversions,
+// exponentials, masks), which the matrix instructions hide behind: VALU busy 60%
+// of the time, matrix cores 23%.  3 chunks of 2048 tokens over 1021 to 3069
+// cached ones: 254 us, 0.57 PFLOP/s (0.78 over long caches).  Sharing the
+// converted codes of a tile between the waves through LDS costs a barrier per
+// tile: 303 us where each wave converting for itself took 281.
 #include <algorithm>
 #include <type_traits>
 
@@ -217,8 +229,10 @@ __device__ __forceinline__ h8 codes_h8(uint32_t lo, uint32_t hi) {
 // Parts of an item pass between workgroups of different XCDs, whose L2s are
 // not coherent for plain accesses: they are written and read by accesses of
 // device scope, which do not stay in an L2, so no cache has to be written back
-// or invalidated (a fence of device scope does both: measured below).  A part
-// counts as done when its stores have completed (stores_done, then the
+// or invalidated.  A fence of device scope does both, for the whole L2: with
+// fences, 4 drafted tokens over 131071 took 107 us (65 without), a windowed
+// decode batch of 24 requests 106 (49), one request of 777 tokens 24 (14.7).
+// A part counts as done when its stores have completed (stores_done, then the
 // barrier, then the counter).
 __device__ __forceinline__ void put2(f2* p, f2 v) {
   __hip_atomic_store((uint64_t*)p, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
@@ -349,10 +363,14 @@ __device__ __forceinline__ int max4i(int v) {
 // scales are then the same for all lanes.
 template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
 struct Attn {
-  // the weights enter the second product as two f16 values
+  // the weights enter the second product as two f16 values; for few rows this
+  // costs at most 2% (24 windowed requests: 48.0 us with one, 49.0 with two;
+  // 32 long ones 190.0, 190.7), and halves the error of f16 output
   static constexpr bool HILO = SPLIT || F32;
   // what an item costs besides its tiles, in tiles (see make_plan): its first
-  // reads and its results
+  // reads and its results (32 requests to 8192 tokens: 202 us where items
+  // counted by tiles alone, 191 so; one of 777 tokens: 14.1, 10.5; prompts
+  // under a window of 512: 74, 64)
   static constexpr int kExtra = SPLIT ? 4 : 3;
   static constexpr int kRows = 16 * NQ;                      // per wave
   static constexpr int kQb = SPLIT ? kRows : kRows * kWaves;  // per item
@@ -831,13 +849,19 @@ struct Cut {
 Cut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
   Cut c;
   const int64_t g = q_heads / kv.heads;
-  const double rows = (double)n_tok * g / std::max(n_req, 1);  // rows of a request, on average
+  // By the rows of a request, on average.  Up to 16 one group of rows: 10.5 us
+  // at one request, 191 at 32 long ones, against 11.6 and 196 with two groups.
+  // Up to 32 the waves share the rows: 40.8 us at 20 rows of 8 requests to 16000
+  // tokens, 42.0 where each wave has its own; 191, 209 at one row of 32; at 48
+  // rows both take 60 to 63 us, and prompts 403 us shared, 254 with rows of their own.
+  const double rows = (double)n_tok * g / std::max(n_req, 1);
   c.split = rows <= 32;
   c.nq = c.split && rows <= 16 ? 1 : 2;
   c.qb = c.split ? 16 * c.nq : 16 * c.nq * 4;
   c.entries = std::min<int64_t>(n_req, n_tok) + (int64_t)n_tok * g / c.qb;
   // as many workgroups as the device holds at once: two per CU, one where a
-  // wave needs more than half of a SIMD's registers
+  // wave needs more than half of a SIMD's registers (half as many: 269 against
+  // 254 us for prompts, 71 against 64 with a window, 197 against 191 at decode)
   c.slices = kv.head_dim == 256 ? 256 : 512;
   return c;
 }
