@@ -8,12 +8,17 @@
 //
 // What bounds it.  At decode the adapters' own bytes, once per adapter
 // (2 r (d_in + d_out)), and a chain of dependent reads: ids, X and A, then B.
-// For prompts X, base and Y, each read or written once.  Hence one launch
-// that keeps U in LDS: a workgroup computes its tile's U with K split over its
-// waves and then a chunk of the outputs.  With few tiles several workgroups
-// take chunks of one tile and each computes U anew: A is then read from L2 by
-// all of them, which costs less than a second launch as long as A is small
-// (see split_ranks).  Otherwise a first launch splits K over workgroups.
+// For prompts X, base and Y, each read or written once.  For small A one launch
+// keeps U in LDS: a workgroup computes its tile's U with K split over its waves
+// and then a chunk of the outputs; several workgroups take chunks of one tile
+// and each computes U anew.  Otherwise a first launch splits K over workgroups
+// and a second one does the outputs (get_cut holds both sides' times).
+//
+// Measured: 4 tokens of 4 adapters of rank 16, 4096 -> 4096: 9.2 us.  61 tokens
+// of 24 adapters of ranks to 64, 11008 -> 4096 (37 MB): 15.4 and 10.6 us; the
+// first reads 16 rows of A, 64 bytes each, per instruction, and takes 10.7 if A
+// lies in the order of those reads.  4099 tokens of 7 prompts, ranks to 32, 4096 -> 4096
+// (102 MB): 19.4 and 22.0 us, 2.5 TB/s in all; finding the tiles takes 3 of it.
 //
 // Rounding.  X, A and B are f16 and products of them exact in fp32; sums are
 // fp32.  U enters the second product as the sum of two f16 values, 22 bits,
@@ -691,20 +696,28 @@ struct Cut {
 };
 Cut get_cut(int32_t T, const dfs_adapters& ad) {
   Cut c;
-  // Tiles of 64 tokens read A and B a quarter as often, if adapters have that many.
-  c.groups = T > kSmallT && ad.r_max <= 64 && T >= 2 * kTok * (ad.n + 1) ? kMany : 1;
+  // Tiles of 64 tokens read A and B a quarter as often, if adapters have that
+  // many: rank 32, 4096 -> 4096, 41.4 us against 44.7 in tiles of 16 at 455
+  // tokens per adapter, 48.8 and 52.6 at 129, 32.4 and 34.1 at 65, 28.4 and 25.1 at 32.
+  c.groups = T > kSmallT && ad.r_max <= 64 && T >= (int64_t)kMany * kTok * (ad.n + 1) ? kMany : 1;
   const int size = c.groups * kTok;
   // tiles that have work, at most
   const int busy = (int)std::min<int64_t>(T, T / size + std::min<int64_t>(ad.n + 1, T));
   c.tiles = T <= kSmallT ? (T + 7) / 8 * 8 : busy;
+  // One launch while the A that every workgroup reads is small.  4 tokens, the
+  // kernels' own time without what lies between two: rank 8 over 4096, 7.9 us
+  // against 8.8 in two launches; 16 over 4096, 9.2 and 9.1; 32 over 2048, 9.0 and
+  // 9.4; 32 over 4096, 12.7 and 9.9; 32 over 8192, 20.5 and 9.9.
   const bool both =
-      T <= kSmallT && ad.r_max <= 32 && (int64_t)ad.r_max * ad.d_in <= 256 * 1024;
+      T <= kSmallT && ad.r_max <= 32 && (int64_t)ad.r_max * ad.d_in <= 64 * 1024;
   const int per = (both ? kBothWaves : kExpandWaves) * kChunk;  // outputs of one step
   const int most = (ad.d_out + per - 1) / per;
   const int chunks = std::max(1, std::min(most, (both ? 512 : 1024) / busy));
   c.chunk = ((ad.d_out + chunks - 1) / chunks + kChunk - 1) / kChunk * kChunk;
   const int k_most = (ad.d_in + 2 * kShrinkWaves * kChunk - 1) / (2 * kShrinkWaves * kChunk);
   c.slices = both ? 0 : std::max(1, std::min(k_most, 384 / busy));
+  // A launch that plans costs 5.1 us at 1100 tokens and 9.9 at 4099, what the
+  // workgroups do instead about 2 and 3; it is for what their LDS cannot hold.
   c.planned = T > kMidT || (T > kSmallT && ad.n > kMidN);
   return c;
 }

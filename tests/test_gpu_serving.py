@@ -103,6 +103,21 @@ def test_adapter_very_many_tokens(n):
         check_adapter(len(ids), n, 8, 40, 24, "f32", ranks, ids)
 
 
+@pytest.mark.parametrize("r_max", [12, 27, 64, 70])
+@pytest.mark.parametrize("T,n", [(300, 1), (1000, 3), (1000, 12), (9000, 5)])
+def test_adapter_many_tokens_of_few_adapters(T, n, r_max):
+    rng = np.random.default_rng(T + n + r_max)
+    ranks = [max(1, r_max - 5 * i) for i in range(n)]
+    ids = np.repeat(rng.integers(-1, n, T // 50 + 1), 50)[:T]
+    check_adapter(T, n, r_max, 136, 200, "f16", ranks, ids)
+
+
+@pytest.mark.parametrize("d_in", [2048, 2056, 4096, 4104])
+@pytest.mark.parametrize("r_max", [16, 32])
+def test_adapter_few_tokens_over_longer_rows(d_in, r_max):
+    check_adapter(7, 3, r_max, d_in, 320, "f32", [r_max, 5, r_max - 1], [2, 0, -1, 1, 2, 2, 0])
+
+
 def test_adapter_large_and_small_products():
     """X A^T far outside f16's range, and far below it."""
     rng = np.random.default_rng(4)
