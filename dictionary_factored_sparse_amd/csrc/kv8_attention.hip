@@ -24,10 +24,11 @@
 // w' = w * vscale / 2^E <= 2^15, E the running maximum of the exponents of
 // vscale, an exact power of two in which the sums are kept.
 //
-// Rounding.  For prompts with f16 output w' is rounded to f16 for the second
-// product: errors of the size of the output's own rounding.  Otherwise (fp32
-// output, and few rows, where the matrix cores wait for memory anyway) it
-// enters as the sum of two f16 values.  Weights are kept at 2^13 times their
+// Rounding.  w' enters the second product as the sum of two f16 values: f16
+// output is then as near to exact as its own rounding allows (2.1e-4 of the
+// norm).  One f16 value gave 3.2e-4 at 238 us for the prompts below, which take
+// 256 with two; for few rows two cost at most 2% (24 windowed requests 48.0 us
+// with one, 49.0; 32 long ones 190.0, 190.7).  Weights are kept at 2^13 times their
 // value so that f16's normal range reaches 2^-27 of the largest, and m is
 // raised only when a score passes it by more than 2 (weights stay below 2^15),
 // which spares most rescales of the sums.
@@ -47,7 +48,7 @@
 // chain of plan, pages, codes, join.  Prompts: vector instructions (conversions,
 // exponentials, masks), which the matrix instructions hide behind: VALU busy 60%
 // of the time, matrix cores 23%.  3 chunks of 2048 tokens over 1021 to 3069
-// cached ones: 254 us, 0.57 PFLOP/s (0.78 over long caches).  Sharing the
+// cached ones: 256 us, 0.56 PFLOP/s.  Sharing the
 // converted codes of a tile between the waves through LDS costs a barrier per
 // tile: 303 us where each wave converting for itself took 281.
 #include <algorithm>
@@ -363,10 +364,6 @@ __device__ __forceinline__ int max4i(int v) {
 // scales are then the same for all lanes.
 template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
 struct Attn {
-  // the weights enter the second product as two f16 values; for few rows this
-  // costs at most 2% (24 windowed requests: 48.0 us with one, 49.0 with two;
-  // 32 long ones 190.0, 190.7), and halves the error of f16 output
-  static constexpr bool HILO = SPLIT || F32;
   // what an item costs besides its tiles, in tiles (see make_plan): its first
   // reads and its results (32 requests to 8192 tokens: 202 us where items
   // counted by tiles alone, 191 so; one of 777 tokens: 14.1, 10.5; prompts
@@ -629,12 +626,10 @@ struct Attn {
           const h2 hi = __builtin_convertvector(p, h2);
           w[i][h][x] = hi.x;
           w[i][h][x + 1] = hi.y;
-          if constexpr (HILO) {
-            const f2 rest = {p.x - (float)hi.x, p.y - (float)hi.y};
-            const h2 lo = __builtin_convertvector(rest, h2);
-            wl[i][h][x] = lo.x;
-            wl[i][h][x + 1] = lo.y;
-          }
+          const f2 rest = {p.x - (float)hi.x, p.y - (float)hi.y};
+          const h2 lo = __builtin_convertvector(rest, h2);
+          wl[i][h][x] = lo.x;
+          wl[i][h][x + 1] = lo.y;
           sum += p.x + p.y;
         }
       }
@@ -654,10 +649,8 @@ struct Attn {
       for (int i = 0; i < NQ; ++i) {
         o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[i][0], o[i][d], 0, 0, 0);
         o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[i][1], o[i][d], 0, 0, 0);
-        if constexpr (HILO) {
-          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[i][0], o[i][d], 0, 0, 0);
-          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[i][1], o[i][d], 0, 0, 0);
-        }
+        o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[i][0], o[i][d], 0, 0, 0);
+        o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[i][1], o[i][d], 0, 0, 0);
       }
     }
   }
