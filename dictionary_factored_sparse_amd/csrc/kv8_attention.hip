@@ -21,17 +21,23 @@
 //     16 q .. are contiguous in a page (dfs_kv8 stores values so).
 // Codes become f16 exactly (every E4M3 and int8 value is an f16 value); the
 // page scales multiply the fp32 scores, and for values they enter the weights:
-// w' = w * vscale / 2^E <= 2^15, E the running maximum of the exponents of
-// vscale, an exact power of two in which the sums are kept.
+// w'_j = 2^(t_j + log2(vscale_j) - c), c the running maximum over the row's own
+// keys of t_j + log2(vscale_j), so that a row's sums keep their bits whatever
+// the scales of pages that it does not see or hardly weighs (with one exponent
+// of vscale per wave, rows beside a page of 2^24 times their values lost 1e-4 of
+// theirs, of 2^40 times all).  The sums are in units of 2^c, those of the
+// weights themselves in units of 2^m.
 //
 // Rounding.  w' enters the second product as the sum of two f16 values: f16
 // output is then as near to exact as its own rounding allows (2.1e-4 of the
 // norm).  One f16 value gave 3.2e-4 at 238 us for the prompts below, which take
 // 256 with two; for few rows two cost at most 2% (24 windowed requests 48.0 us
 // with one, 49.0; 32 long ones 190.0, 190.7).  Weights are kept at 2^13 times their
-// value so that f16's normal range reaches 2^-27 of the largest, and m is
-// raised only when a score passes it by more than 2 (weights stay below 2^15),
-// which spares most rescales of the sums.
+// value so that f16's normal range reaches 2^-27 of the largest, and c is
+// raised only when a key passes it by more than 2 (weights stay below 2^15),
+// which spares most rescales of the sums.  m may lag by 32: nothing is held in
+// few bits there, and finding its maximum over the lanes for every tile took the
+// prompts below from 259 to 283 us.
 //
 // Work split.  The tiles of 64 keys of all items (request, block of query
 // rows, kv head) form one line, cut into equal slices, one per workgroup: the
@@ -66,7 +72,10 @@ constexpr int kInlinePlan = 256;         // entries up to which every workgroup 
 constexpr int kCounterBytes = 65536;     // per-slice counters at the start of the workspace
 constexpr int kWhole = 8;                // tiles up to which an item of a prompt is not split
 constexpr float kWeightBits = 13.0f;     // weights are held at 2^13 times their value
-constexpr float kSlack = 2.0f;           // the running maximum may lag by this (log2)
+constexpr float kSlack = 2.0f;           // the reference of the sums may lag by this (log2),
+constexpr float kFar = 32.0f;            // that of the weights' own sum by this
+constexpr float kLeast = 72.0f;          // 2^(13 + kFar - kLeast) is 0 in f16, 2^(13 - kLeast) far
+                                         // above the least normal fp32
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttnWs {
@@ -350,12 +359,6 @@ __device__ __forceinline__ float sum4(float v) {
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
-__device__ __forceinline__ int max4i(int v) {
-  auto a = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = max((int)a[0], (int)a[1]);
-  auto b = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-  return max((int)b[0], (int)b[1]);
-}
 
 // SPLIT: the waves of a workgroup take the tiles of an item in turn, all for
 // the same NQ * 16 query rows (few rows, long caches).  Otherwise each wave
@@ -381,7 +384,6 @@ struct Attn {
       int64_t tmp[kWaves];
     };
     float m[kWaves][kRows], l[kWaves][kRows];
-    int e[kWaves];
     int last;
     int32_t longest;
     int64_t first[kInlinePlan + 1];
@@ -393,7 +395,7 @@ struct Attn {
   h8 qf[NQ][kSteps];
   f4 o[NQ][kDims];
   float m[NQ], l[NQ];
-  int ev;  // sums are in units of 2^ev (and 2^13)
+  float c[NQ];  // o is in units of 2^(c - 13), l of 2^(m - 13)
   uint32_t kraw[4][D / 16];  // K codes of the tile to come
   float ks, vs;              // and the scales of this lane's key block in it
   // pages of a tile: of this lane's K rows, and of its key block
@@ -497,12 +499,11 @@ struct Attn {
         const int d = s < 2 * kWide ? (s >> 1) * 64 + q4 * 16 + (s & 1) * 8 : 64 * kWide + q4 * 8;
         qf[i][s] = ld16<h8>(qp + d);
       }
-      m[i] = -1e30f;
+      m[i] = c[i] = -1e30f;
       l[i] = 0.0f;
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[i][d] = f4{0, 0, 0, 0};
     }
-    ev = -126;
   }
 
   // Bits of this lane's 16 keys, from j0 on, that lie below key `end`.
@@ -584,35 +585,44 @@ struct Attn {
 #pragma unroll
       for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
     }
-    // vscale = 2^(lv + ev): the exponent's maximum so far exactly, the rest as
-    // part of the weights' exponents (and out of their sums again).  Scales
-    // below 2^-64 of the largest count as that, which moves nothing and keeps
-    // their weights' sums normal.
-    const int e_here = max4i(vscale > 0.0f ? __builtin_amdgcn_frexp_expf(vscale) : -126);
-    const int e_new = max(ev, e_here);
-    const float grow = __builtin_amdgcn_ldexpf(1.0f, max(ev - e_new, -300));
-    const float lv =
-        vscale > 0.0f
-            ? fmaxf(__builtin_amdgcn_logf(__builtin_amdgcn_ldexpf(vscale, -e_new)), -64.0f)
-            : 0.0f;
-    const float back = __builtin_amdgcn_exp2f(-lv);
-    bool rescale = e_new != ev;
-    ev = e_new;
+    // vscale = 2^(ve + lf), lf = -inf for a scale of 0.  A lane's keys lie in one
+    // page, so that what its scale adds to the weights' exponents goes out of
+    // their sum again by one factor.
+    const float ve = __builtin_amdgcn_frexp_expf(vscale);
+    const float lf =
+        __builtin_amdgcn_logf(__builtin_amdgcn_ldexpf(vscale, -__builtin_amdgcn_frexp_expf(vscale)));
+    float mx[NQ];
+    bool far = false, rescale = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      mx[i] = s[i][0][0];
+#pragma unroll
+      for (int x = 1; x < 16; ++x) mx[i] = fmaxf(mx[i], s[i][x >> 2][x & 3]);
+      mx[i] *= kscale;
+      far = far || mx[i] > m[i] + kFar;
+    }
+    if (__ballot(far) != 0) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const float top = fmaxf(max4(mx[i]), m[i]);
+        l[i] *= __builtin_amdgcn_exp2f(m[i] - top);
+        m[i] = top;
+      }
+    }
     h8 w[NQ][2], wl[NQ][2];
     float alpha[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      float mx = s[i][0][0];
-#pragma unroll
-      for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[i][x >> 2][x & 3]);
-      mx = max4(mx * kscale);
-      const bool up = mx > m[i] + kSlack;
-      const float f = up ? __builtin_amdgcn_exp2f(m[i] - mx) : 1.0f;
-      l[i] *= f;
-      alpha[i] = grow * f;
-      m[i] = up ? mx : m[i];
+      const float mo = max4(mx[i] + (ve + lf));
+      const bool up = mo > c[i] + kSlack;
+      alpha[i] = up ? __builtin_amdgcn_exp2f(c[i] - mo) : 1.0f;
+      c[i] = up ? mo : c[i];
       rescale = rescale || up;
-      const float add = kWeightBits + lv - m[i];
+      // Contributions below 2^(kFar - kLeast) of the largest may count as that: as
+      // f16 they are 0, and the sum of the weights keeps its part of them.
+      const float rel = fmaxf((ve - c[i]) + lf, -kLeast - m[i]);
+      const float back = __builtin_amdgcn_exp2f(-rel - m[i]);
+      const float add = kWeightBits + rel;
       float sum = 0.0f;
 #pragma unroll
       for (int x = 0; x < 16; ++x)
@@ -652,6 +662,25 @@ struct Attn {
         o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[i][0], o[i][d], 0, 0, 0);
         o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[i][1], o[i][d], 0, 0, 0);
       }
+    }
+  }
+
+  // The sum of a row's weights over its four lanes, in units (2^m from here on)
+  // that bring it to 1/2 .. 1, and o in the same.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      l[i] = sum4(l[i]);
+      const int e = __builtin_amdgcn_frexp_expf(l[i]);
+      l[i] = __builtin_amdgcn_ldexpf(l[i], -e);
+      const float by = fmaxf(c[i] - m[i], -1000.0f), whole = floorf(by);
+      const float f = __builtin_amdgcn_exp2f(by - whole);
+      m[i] += (float)e - kWeightBits;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          o[i][d][x] = __builtin_amdgcn_ldexpf(o[i][d][x] * f, (int)whole - e);
     }
   }
 
@@ -736,8 +765,7 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
     t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
     if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
     else if (t.nrows > 0) t.tiles(u0, u1, 1);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) t.l[i] = sum4(t.l[i]);
+    t.finish();
     const bool whole = u0 == 0 && u1 == n_tiles;
     // a slice has at most two items that are not whole: its first and its last
     const int64_t slot = 2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0);
@@ -757,7 +785,6 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
             *(f4*)&sh.o[(t.wave * A::kRows + row) * D + d * 16 + t.q4 * 4] = t.o[i][d];
         }
       }
-      if (t.lane == 0) sh.e[t.wave] = t.ev;
       __syncthreads();
       for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
         const int row = idx / (D / 4), d = idx % (D / 4) * 4;
@@ -770,7 +797,7 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
         for (int w = 0; w < kWaves; ++w) {
           const float f = __builtin_amdgcn_exp2f(sh.m[w][row] - mm);
           l += sh.l[w][row] * f;
-          v += *(f4*)&sh.o[(w * A::kRows + row) * D + d] * __builtin_amdgcn_ldexpf(f, sh.e[w]);
+          v += *(f4*)&sh.o[(w * A::kRows + row) * D + d] * f;
         }
         if (whole) {
           t.store(t.out_at(t.row0 + row) + d, v, l);
@@ -788,11 +815,8 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
           const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
 #pragma unroll
           for (int d = 0; d < A::kDims; ++d) {
-            f4 v = t.o[i][d];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = __builtin_amdgcn_ldexpf(v[c], t.ev);
-            if (whole) t.store(at + d * 16 + t.q4 * 4, v, t.l[i]);
-            else put4(&ws.part_o[pr * D + d * 16 + t.q4 * 4], v);
+            if (whole) t.store(at + d * 16 + t.q4 * 4, t.o[i][d], t.l[i]);
+            else put4(&ws.part_o[pr * D + d * 16 + t.q4 * 4], t.o[i][d]);
           }
           if (!whole && t.q4 == 0) put2(&ws.part_ml[pr], f2{t.m[i], t.l[i]});
         }
