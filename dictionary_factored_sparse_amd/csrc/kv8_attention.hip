@@ -236,6 +236,11 @@ __device__ __forceinline__ h8 codes_h8(uint32_t lo, uint32_t hi) {
   return v;
 }
 
+// The top bit of each byte that is an E4M3 NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
+  return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
 // Parts of an item pass between workgroups of different XCDs, whose L2s are
 // not coherent for plain accesses: they are written and read by accesses of
 // device scope, which do not stay in an L2, so no cache has to be written back
@@ -520,26 +525,40 @@ struct Attn {
     return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
   }
 
+  // What some row of the wave sees of this lane's 16 keys from j0 on, in page pv.
+  __device__ __forceinline__ uint32_t seen_by_any(int pv, int j0) const {
+    return valid(pv) ? seen(window_low(pmin), min(pmax + 1, rq.keys), j0) : 0u;
+  }
+  // This lane's V codes of the tile that starts at key kb: its row of the first
+  // 16 dims, and the others 16 P bytes apart.
+  __device__ __forceinline__ const uint8_t* v_codes(int kb, int pv, uint32_t& off) const {
+    const int P = a.kv.page;
+    const int64_t ph = (int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh;
+    const uint8_t* base = a.kv.v + ph * D * P;
+    off = r16 * P + 16 * q4;
+    if constexpr (BIG) {
+      base += kb & (P - 1);
+    } else {
+      base += off + (((kb + 16 * q4) & (P - 1)) - 16 * q4);
+      off = 0;
+    }
+    return base;
+  }
+
   // Tile u, whose K codes are in kraw.  The tile `next` is loaded meanwhile,
   // and the pages of the tile `after`.  The loads are in the order in which
   // they are waited for, with no branch around them: a wait then leaves the
   // later ones in flight.
+  template <bool CAREFUL>
   __device__ __forceinline__ void tile(int u, int next, int after, bool more) {
     const int kb = sp.tile(u) * kTile;
-    const int P = a.kv.page, pv = pg0.v;
+    const int pv = pg0.v;
     u4 vraw[kDims];
     {
-      const int64_t ph = (int64_t)(valid(pv) ? pv : 0) * a.kv.heads + kh;
-      const uint8_t* base = a.kv.v + ph * D * P;
-      uint32_t off = r16 * P + 16 * q4;
-      if constexpr (BIG) {
-        base += kb & (P - 1);
-      } else {
-        base += off + (((kb + 16 * q4) & (P - 1)) - 16 * q4);
-        off = 0;
-      }
+      uint32_t off;
+      const uint8_t* base = v_codes(kb, pv, off);
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) vraw[d] = ld16<u4>(base + d * 16 * P + off);
+      for (int d = 0; d < kDims; ++d) vraw[d] = ld16<u4>(base + d * 16 * a.kv.page + off);
     }
     f4 s[NQ][4];
 #pragma unroll
@@ -564,8 +583,7 @@ struct Attn {
     if (!plain) {
       const int j0 = kb + 16 * q4;
       // what some row of the wave sees
-      const uint32_t any =
-          valid(pv) ? seen(window_low(pmin), min(pmax + 1, rq.keys), j0) : 0u;
+      const uint32_t any = seen_by_any(pv, j0);
       if (any == 0) vscale = 0.0f;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -584,6 +602,15 @@ struct Attn {
         keep[w] = ((used >> (4 * w) & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
 #pragma unroll
       for (int d = 0; d < kDims; ++d) vraw[d] &= keep;
+      if constexpr (CAREFUL) {
+#pragma unroll
+        for (int d = 0; d < kDims; ++d)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t n = nan_codes(vraw[d][x]);
+            vraw[d][x] &= ~(n - (n >> 7));
+          }
+      }
     }
     // vscale = 2^(ve + lf), lf = -inf for a scale of 0.  A lane's keys lie in one
     // page, so that what its scale adds to the weights' exponents goes out of
@@ -685,6 +712,7 @@ struct Attn {
   }
 
   // tiles u0, u0 + step, ... below u1
+  template <bool CAREFUL>
   __device__ __forceinline__ void tiles(int u0, int u1, int step) {
     if (u0 >= u1) return;
     const int last = u0 + (u1 - 1 - u0) / step * step;
@@ -692,7 +720,62 @@ struct Attn {
     pg1 = load_pages(min(u0 + step, last));
     load_k(u0, true);
     for (int u = u0; u <= last; u += step)
-      tile(u, min(u + step, last), min(u + 2 * step, last), u < last);
+      tile<CAREFUL>(u, min(u + step, last), min(u + 2 * step, last), u < last);
+  }
+
+  // NaN codes of V in a tile that some rows see only in part: a weight of 0 does
+  // not keep them out of the rows that do not see their keys.  The sums tell, and
+  // cost nothing on the way; where some are NaN, the tiles are taken once more in
+  // a careful form, with such codes as 0, and spread_nan makes NaN of the sums
+  // that they belong to.  (Looked for in the tiles themselves, they took 3% of
+  // the time for prompts and for one short request; so, 0 to 1%.)
+  __device__ __forceinline__ bool any_nan() const {
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int d = 0; d < kDims; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z = __builtin_fmaf(o[i][d][x], 0.0f, z);
+    return __ballot(z != z) != 0;
+  }
+  // A product of ones counts, for each row and dim, the NaN codes that the row
+  // sees; put(i, d) is called where there are some, i the group of rows.  u0, u1
+  // and step as for tiles().
+  template <typename F>
+  __device__ __forceinline__ void spread_nan(int u0, int u1, int step, F put) const {
+    stores_done();
+#pragma unroll 1
+    for (int u = u0; u < u1; u += step) {
+      const int kb = sp.tile(u) * kTile, j0 = kb + 16 * q4, pv = settle(load_pages(u)).v;
+      const uint32_t any = seen_by_any(pv, j0);
+      uint32_t off;
+      const uint8_t* base = v_codes(kb, pv, off);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // eight of the lane's keys at a time
+        const uint32_t some = any >> (8 * h) & 0xFFu;
+        h8 w[NQ];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const uint32_t see = some & seen(window_low(pos[i]), pos[i] + 1, j0) >> (8 * h);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[i][x] = see >> x & 1u ? (_Float16)1.0f : (_Float16)0.0f;
+        }
+#pragma unroll 1
+        for (int d = 0; d < kDims; ++d) {
+          const u2 c = *gptr((const u2*)(base + d * 16 * a.kv.page + off + 8 * h));
+          // 0x08 where there is one: 2^-6
+          const h8 v = codes_h8<KIND>(nan_codes(c.x) >> 4, nan_codes(c.y) >> 4);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            const f4 n = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[i], f4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (n[x] > 0.0f) put(i, d * 16 + q4 * 4 + x);
+          }
+        }
+      }
+    }
   }
 
   // One row's destination.
@@ -701,8 +784,11 @@ struct Attn {
     const int tok = row / g, h = kh * g + row - tok * g;
     return (int64_t)(rq.t0 + tok) * a.ldo + (int64_t)h * D;
   }
+  using T = typename std::conditional<F32, float, _Float16>::type;
+  __device__ __forceinline__ void store_nan(int64_t at) const {
+    *gptr_w((T*)a.O + at) = (T)__builtin_nanf("");
+  }
   __device__ __forceinline__ void store(int64_t at, const f4& v, float l) const {
-    using T = typename std::conditional<F32, float, _Float16>::type;
     // rows that see nothing are 0; a sum that is NaN stays so
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     typedef T T4 __attribute__((ext_vector_type(4)));
@@ -763,8 +849,14 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
     const int u0 = uni((int)(x - item0)), u1 = uni(keep ? n_tiles : (int)(min(item1, xe) - item0));
     x = u1 == n_tiles ? item0 + n_line : item0 + u1;
     t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
-    if constexpr (SPLIT) t.tiles(u0 + t.wave, u1, kWaves);
-    else if (t.nrows > 0) t.tiles(u0, u1, 1);
+    const int v0 = SPLIT ? u0 + t.wave : u0, step = SPLIT ? kWaves : 1;
+    const int v1 = SPLIT || t.nrows > 0 ? u1 : u0;  // this wave's tiles: v0, v0 + step, ... below v1
+    t.template tiles<false>(v0, v1, step);
+    const bool nans = KIND == DFS_FP8 && t.any_nan();
+    if (KIND == DFS_FP8 && nans) {
+      t.begin(inline_plan ? sh.facts[req] : get_req(a.b, a.kv.page, req), req, qblk, kh);
+      t.template tiles<true>(v0, v1, step);
+    }
     t.finish();
     const bool whole = u0 == 0 && u1 == n_tiles;
     // a slice has at most two items that are not whole: its first and its last
@@ -785,6 +877,9 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
             *(f4*)&sh.o[(t.wave * A::kRows + row) * D + d * 16 + t.q4 * 4] = t.o[i][d];
         }
       }
+      if (KIND == DFS_FP8 && nans) t.spread_nan(v0, v1, step, [&](int i, int d) {
+        sh.o[(t.wave * A::kRows + 16 * i + t.r16) * D + d] = __builtin_nanf("");
+      });
       __syncthreads();
       for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
         const int row = idx / (D / 4), d = idx % (D / 4) * 4;
@@ -821,6 +916,18 @@ void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_pl
           if (!whole && t.q4 == 0) put2(&ws.part_ml[pr], f2{t.m[i], t.l[i]});
         }
       }
+      if (KIND == DFS_FP8 && nans)
+        t.spread_nan(v0, v1, step, [&](int i, int d) {
+          const int row = 16 * i + t.r16;
+          if (row >= t.nrows) return;
+          if (whole) {
+            t.store_nan(t.out_at(t.row0 + row) + d);
+          } else {
+            const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
+            __hip_atomic_store(&ws.part_o[pr * D + d], __builtin_nanf(""), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+          }
+        });
     }
     if (!whole) {
       // The parts of an item are joined in groups of kJoin slices, each by the

@@ -1,5 +1,5 @@
 """A row of the attention depends on nothing but the keys that it sees: pages of much larger value
-scales that other rows of the same wave see must not change it.
+scales and NaN codes that other rows of the same wave see must not change it.
 
 Bound of a row, in its own terms (a_j = w_j vscale_j, the size of key j's contribution): each score
 errs as its fp32 sum does, which its weight follows; the exponent's argument and value add
@@ -143,3 +143,23 @@ def test_scales_at_the_ends_of_fp32():
         c = Cache(np.random.default_rng(8), "fp8", 2, 64, 16, lengths)
         steps(c, lengths, [-110, -20, 110, -110])
         check(c, new, lengths, group, "f32")
+
+
+# ------------------------------------------------------------------------------- NaN
+
+def places(lengths):
+    """Positions near the end of the first request, in pages that only some of its rows see."""
+    n = lengths[0]
+    return sorted({n - 1, n - 2, n - 4, max(n - 20, 0), 3})
+
+
+@pytest.mark.parametrize("new,lengths,group", SHAPES)
+@pytest.mark.parametrize("page", [16, 64])
+def test_nan_value_codes(new, lengths, group, page):
+    """A NaN code of V makes NaN of its dim for the rows that see its key, and of nothing else."""
+    for window, sinks in ((0, 0), (7, 2)):
+        c = Cache(np.random.default_rng(1), "fp8", 2, 96, page, lengths)
+        for i, j in enumerate(places(lengths)):
+            c.v[c.table[0, j // page], i % 2, 5 + 17 * i, j % page] = 0x7F if i % 3 else 0xFF
+        got = check(c, new, lengths, group, "f32", window=window, sinks=sinks)
+        assert np.isnan(got).any() and not np.isnan(got).all(-1).any()
