@@ -579,18 +579,22 @@ struct Attn {
     pg1 = load_pages(after);
     const bool plain = kb + kTile - 1 <= pmin && kb + kTile <= rq.keys &&
                        (a.window <= 0 || pmax - kb < a.window || kb + kTile <= a.sinks) &&
-                       __ballot(!valid(pv) || vscale == 0.0f) == 0;
+                       __ballot(!valid(pv) || !(vscale > 0.0f && vscale < INFINITY)) == 0;
     if (!plain) {
       const int j0 = kb + 16 * q4;
       // what some row of the wave sees
       const uint32_t any = seen_by_any(pv, j0);
       if (any == 0) vscale = 0.0f;
+      // A scale that is not finite makes NaN of the rows that see a key of its
+      // page, by their scores, and of no other.
+      const float odd = vscale - vscale;
+      if (odd != 0.0f) vscale = 0.0f;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         const uint32_t see = any & seen(window_low(pos[i]), pos[i] + 1, j0);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          s[i][x >> 2][x & 3] = see >> x & 1u ? s[i][x >> 2][x & 3] * kscale : -INFINITY;
+          s[i][x >> 2][x & 3] = see >> x & 1u ? s[i][x >> 2][x & 3] * kscale + odd : -INFINITY;
       }
       kscale = 1.0f;
       // codes of keys that nobody sees may be NaN, and a scale of 0 makes 0 of

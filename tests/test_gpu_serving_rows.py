@@ -1,5 +1,5 @@
 """A row of the attention depends on nothing but the keys that it sees: pages of much larger value
-scales and NaN codes that other rows of the same wave see must not change it.
+scales, NaN codes and NaN scales that other rows of the same wave see must not change it.
 
 Bound of a row, in its own terms (a_j = w_j vscale_j, the size of key j's contribution): each score
 errs as its fp32 sum does, which its weight follows; the exponent's argument and value add
@@ -163,3 +163,16 @@ def test_nan_value_codes(new, lengths, group, page):
             c.v[c.table[0, j // page], i % 2, 5 + 17 * i, j % page] = 0x7F if i % 3 else 0xFF
         got = check(c, new, lengths, group, "f32", window=window, sinks=sinks)
         assert np.isnan(got).any() and not np.isnan(got).all(-1).any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,lengths,group", SHAPES)
+@pytest.mark.parametrize("page", [16, 64])
+def test_nan_scales(kind, new, lengths, group, page):
+    """A page's NaN scale, of K or V, makes NaN of the rows that see a key of it, and of no other."""
+    for which in ("ks", "vs"):
+        for window in (0, 5):
+            for at in (0, (lengths[0] - 1) // page):
+                c = Cache(np.random.default_rng(2), kind, 2, 64, page, lengths)
+                getattr(c, which)[c.table[0, at], 1] = np.nan
+                check(c, new, lengths, group, "f32", window=window)
