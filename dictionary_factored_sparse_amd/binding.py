@@ -654,12 +654,23 @@ def _ints(t: torch.Tensor, what: str, n: int) -> None:
         raise ValueError(f"{what}: contiguous int32 of {n} values required")
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
-    """The stream to launch on: the given one, or the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
+def _stream_of(t: torch.Tensor) -> int:
+    """The stream to launch on: the current one of t's device."""
     return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
 
+
+def _on(stream, fn, *args):
+    """fn(*args) with ``stream`` as the current stream: workspaces and outputs that it makes are
+    allocated and cleared in the order of that stream's work, and a workspace is not handed out
+    again while that work still uses it.  The output may be used on the caller's stream."""
+    before = torch.cuda.current_stream(stream.device)
+    if before == stream:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if out is not None:
+        out.record_stream(before)
+    return out
 
 
 def adapter_workspace(T: int, ad: DeviceAdapters, device) -> torch.Tensor:
@@ -675,6 +686,8 @@ def dict_adapter_forward(X, ad: DeviceAdapters, ids, base=None, Y=None, ydtype=t
     """Y[t] = base[t] + scale[a] (X[t] A_a^T) B_a^T with a = ids[t], and base[t]
     where ids[t] names no adapter.  ``base`` None stands for zeros; ``Y`` may be
     ``base`` (the adapters are added in place)."""
+    if stream is not None:
+        return _on(stream, dict_adapter_forward, X, ad, ids, base, Y, ydtype, ws)
     T = X.shape[0]
     ldx = _matrix(X, "X", None, ad.d_in)
     if ad.d_in % 8 and T and (X.storage_offset() + (T - 1) * ldx + -(-ad.d_in // 8) * 8
@@ -694,7 +707,7 @@ def dict_adapter_forward(X, ad: DeviceAdapters, ids, base=None, Y=None, ydtype=t
         ws = adapter_workspace(T, ad, X.device)
     st = lib().dict_adapter_forward(X.data_ptr(), _dt(X), T, ldx, ad._ref, ids.data_ptr(), ptr, ldb,
                                     Y.data_ptr(), _dt(Y), ldy, ws.data_ptr(), ws.numel(),
-                                    _stream_of(X, stream))
+                                    _stream_of(X))
     if st:
         raise DfsError("dict_adapter_forward", st)
     return Y
@@ -716,6 +729,8 @@ def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> No
     """Append the rows of K and V (heads * head_dim columns) to the cache, in
     place: request r's rows are tok_start[r] .. tok_start[r+1]-1 and go to the
     positions from cached[r] on, in the pages of table[r]."""
+    if stream is not None:
+        return _on(stream, kv8_append, kv, K, V, tok_start, cached, table)
     n_req, ldt, pages = _kv_batch(kv, tok_start, cached, table)
     ldk = _matrix(K, "K", None, kv.heads * kv.head_dim)
     n_tok = K.shape[0]
@@ -725,7 +740,7 @@ def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> No
     _same_device((kv.k, K, V, tok_start, cached, table), "cache")
     st = lib().kv8_append(kv._ref, n_req, n_tok, tok_start.data_ptr(), cached.data_ptr(),
                           table.data_ptr(), ldt, pages, K.data_ptr(), ldk, V.data_ptr(), ldv,
-                          _dt(K), _stream_of(K, stream))
+                          _dt(K), _stream_of(K))
     if st:
         raise DfsError("kv8_append", st)
 
@@ -747,6 +762,9 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
     """Causal attention of the rows of Q (q_heads * head_dim columns) over the
     cache: request r's rows are the last of its length[r] tokens.  ``sm_scale``
     None is 1/sqrt(head_dim); ``window`` 0 is no window.  Returns O."""
+    if stream is not None:
+        return _on(stream, kv8_attention, kv, Q, tok_start, length, table, q_heads, sm_scale,
+                   window, sinks, O, odtype, ws)
     n_req, ldt, pages = _kv_batch(kv, tok_start, length, table)
     n_tok, cols = Q.shape[0], q_heads * kv.head_dim
     ldq = _matrix(Q, "Q", None, cols)
@@ -762,7 +780,7 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
                              table.data_ptr(), ldt, pages, Q.data_ptr(), ldq, q_heads,
                              kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window, sinks,
                              O.data_ptr(), _dt(O), ldo, ws.data_ptr(), ws.numel(),
-                             _stream_of(Q, stream))
+                             _stream_of(Q))
     if st:
         raise DfsError("kv8_attention", st)
     return O

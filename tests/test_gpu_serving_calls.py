@@ -1,0 +1,45 @@
+"""How the serving calls are made: on a stream given by argument, with one workspace kept for
+calls of many sizes."""
+import numpy as np
+import pytest
+import torch
+
+from dictionary_factored_sparse_amd import binding as B
+from tests.gpu_helpers import DEV, say
+from tests.test_gpu_serving import Cache, ints, make_adapters
+
+pytestmark = pytest.mark.gpu
+
+
+def halves(rng, *shape):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float16)).to(DEV)
+
+
+def test_calls_on_a_stream_given_by_argument():
+    """Workspaces and outputs that the calls make are in the order of that stream, whatever the
+    current one is busy with."""
+    rng = np.random.default_rng(1)
+    lengths = [700, 33, 2000]
+    c = Cache(rng, "fp8", 2, 128, 64, lengths)
+    ad, _ = make_adapters(rng, 5, 64, 512, 256, [64, 8, 33, 5, 64])
+    X, ids, Q = halves(rng, 300, 512), ints(rng.integers(-1, 5, 300)), halves(rng, 3, 512)
+    K, V = halves(rng, 3, 256), halves(rng, 3, 256)
+    start, cached, length = ints([0, 1, 2, 3]), ints(np.array(lengths) - 1), ints(lengths)
+    Y = B.dict_adapter_forward(X, ad, ids)
+    B.kv8_append(c.kv, K, V, start, cached, c.tab)
+    O = B.kv8_attention(c.kv, Q, start, length, c.tab, 4)
+    big = torch.randn(4096, 4096, device=DEV).half()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for i in range(4):
+        say(f"case: stream given by argument, round {i}")
+        junk = [torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk                       # what the current stream's allocator gives next is not zero
+        for _ in range(10):
+            big @ big
+        y = B.dict_adapter_forward(X, ad, ids, stream=side)
+        B.kv8_append(c.kv, K, V, start, cached, c.tab, stream=side)
+        o = B.kv8_attention(c.kv, Q, start, length, c.tab, 4, stream=side)
+        side.synchronize()
+        assert torch.equal(y, Y) and torch.equal(o, O)

@@ -1,0 +1,73 @@
+"""The Python binding of the serving calls, on the CPU: what it allocates and where, and what it
+refuses before the library sees a pointer."""
+import contextlib
+
+import pytest
+import torch
+
+from dictionary_factored_sparse_amd import binding as B
+
+z = lambda dt, *s: torch.zeros(*s, dtype=dt)  # noqa: E731
+h, f, i = torch.float16, torch.float32, torch.int32
+
+
+class Streams:
+    """Stands for torch.cuda's streams: which one is current, and on which tensors were made."""
+
+    class Stream:
+        device = torch.device("cpu")
+
+        def __init__(self, n):
+            self.cuda_stream = n
+
+    def __init__(self, patch):
+        self.side, self.now, self.made, self.launched = self.Stream(7), self.Stream(1), [], []
+        patch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
+        patch.setattr(torch.cuda, "stream", self.use)
+        patch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+        patch.setattr(B, "_on_device", lambda *a: None, raising=False)
+        patch.setattr(B, "_stream_of", lambda t, *given: (
+            given[0] if given and given[0] is not None else self.now).cuda_stream)
+        for name in ("empty", "zeros"):
+            make = getattr(torch, name)
+            patch.setattr(torch, name, lambda *a, make=make, **k: (
+                self.made.append(self.now.cuda_stream), make(*a, **k))[1])
+        patch.setattr(B, "lib", lambda: self)
+
+    @contextlib.contextmanager
+    def use(self, s):
+        was, self.now = self.now, s
+        yield
+        self.now = was
+
+    def __getattr__(self, name):      # the library
+        def call(*args):
+            if name.endswith("workspace_size"):
+                args[-1]._obj.value = 70000
+            else:
+                self.launched.append(args[-1])
+            return 0
+        return call
+
+
+def serving_calls():
+    ad = B.DeviceAdapters(z(h, 3, 8, 64), z(h, 3, 40, 8), z(i, 3), z(f, 3))
+    kv = B.DeviceKV8.empty(4, 2, 64, 16, "int8", "cpu")
+    K, start, have, table = z(h, 3, 128), z(i, 3), z(i, 2), z(i, 2, 4)
+    return [(B.dict_adapter_forward, (K[:, :64], ad, z(i, 3))),
+            (B.kv8_append, (kv, K, K, start, have, table)),
+            (B.kv8_attention, (kv, z(h, 3, 256), start, have, table, 4))]
+
+
+def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
+    calls = serving_calls()
+    s = Streams(monkeypatch)
+    for fn, args in calls:
+        for stream in (None, s.side, s.now):
+            s.made.clear()
+            s.launched.clear()
+            fn(*args, stream=stream)
+            want = (stream or s.now).cuda_stream
+            assert s.launched == [want] and set(s.made) <= {want}, (fn.__name__, stream)
+            assert s.made or fn is B.kv8_append
+            assert s.now.cuda_stream == 1
