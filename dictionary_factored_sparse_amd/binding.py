@@ -639,6 +639,20 @@ def _same_device(ts, what: str) -> None:
             raise ValueError(f"{what}: every tensor on one device required")
 
 
+def _on_device(ts, what: str) -> None:
+    """The tensors of a call, whose addresses the GPU gets: all on one."""
+    if not ts[0].is_cuda:
+        raise ValueError(f"{what}: tensors on a GPU required")
+    _same_device(ts, what)
+
+
+def _ws_bytes(ws: torch.Tensor, like: torch.Tensor) -> int:
+    """Bytes of a workspace that the caller gives."""
+    if ws.device != like.device or not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the inputs' device required")
+    return ws.numel() * ws.element_size()
+
+
 def _matrix(t: torch.Tensor, what: str, rows: int | None, cols: int) -> int:
     """Checks a row-major tensor; its row stride."""
     shape, stride = t.shape, t.stride()
@@ -656,7 +670,7 @@ def _ints(t: torch.Tensor, what: str, n: int) -> None:
 
 def _stream_of(t: torch.Tensor) -> int:
     """The stream to launch on: the current one of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _on(stream, fn, *args):
@@ -702,11 +716,12 @@ def dict_adapter_forward(X, ad: DeviceAdapters, ids, base=None, Y=None, ydtype=t
         ptr, ldb = base.data_ptr(), _matrix(base, "base", T, ad.d_out)
         if base.dtype != Y.dtype:
             raise TypeError("base and Y must have the same type")
-    _same_device((X, ad.A, ids, Y) if base is None else (X, ad.A, ids, Y, base), "adapters")
+    xdt, ydt = _dt(X), _dt(Y)
+    _on_device((X, ad.A, ids, Y) if base is None else (X, ad.A, ids, Y, base), "adapters")
     if ws is None:
         ws = adapter_workspace(T, ad, X.device)
-    st = lib().dict_adapter_forward(X.data_ptr(), _dt(X), T, ldx, ad._ref, ids.data_ptr(), ptr, ldb,
-                                    Y.data_ptr(), _dt(Y), ldy, ws.data_ptr(), ws.numel(),
+    st = lib().dict_adapter_forward(X.data_ptr(), xdt, T, ldx, ad._ref, ids.data_ptr(), ptr, ldb,
+                                    Y.data_ptr(), ydt, ldy, ws.data_ptr(), _ws_bytes(ws, X),
                                     _stream_of(X))
     if st:
         raise DfsError("dict_adapter_forward", st)
@@ -737,10 +752,11 @@ def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> No
     ldv = _matrix(V, "V", n_tok, kv.heads * kv.head_dim)
     if K.dtype != V.dtype:
         raise TypeError("K and V must have the same type")
-    _same_device((kv.k, K, V, tok_start, cached, table), "cache")
+    dt = _dt(K)
+    _on_device((kv.k, K, V, tok_start, cached, table), "cache")
     st = lib().kv8_append(kv._ref, n_req, n_tok, tok_start.data_ptr(), cached.data_ptr(),
                           table.data_ptr(), ldt, pages, K.data_ptr(), ldk, V.data_ptr(), ldv,
-                          _dt(K), _stream_of(K))
+                          dt, _stream_of(K))
     if st:
         raise DfsError("kv8_append", st)
 
@@ -773,13 +789,14 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
     if O is None:
         O = torch.empty(n_tok, cols, dtype=odtype, device=Q.device)
     ldo = _matrix(O, "O", n_tok, cols)
-    _same_device((kv.k, Q, O, tok_start, length, table), "cache")
+    odt = _dt(O)
+    _on_device((kv.k, Q, O, tok_start, length, table), "cache")
     if ws is None:
         ws = kv8_attention_workspace(kv, n_req, n_tok, q_heads, Q.device)
     st = lib().kv8_attention(kv._ref, n_req, n_tok, tok_start.data_ptr(), length.data_ptr(),
                              table.data_ptr(), ldt, pages, Q.data_ptr(), ldq, q_heads,
                              kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window, sinks,
-                             O.data_ptr(), _dt(O), ldo, ws.data_ptr(), ws.numel(),
+                             O.data_ptr(), odt, ldo, ws.data_ptr(), _ws_bytes(ws, Q),
                              _stream_of(Q))
     if st:
         raise DfsError("kv8_attention", st)

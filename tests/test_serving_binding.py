@@ -71,3 +71,35 @@ def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
             assert s.launched == [want] and set(s.made) <= {want}, (fn.__name__, stream)
             assert s.made or fn is B.kv8_append
             assert s.now.cuda_stream == 1
+
+
+class Refusing:
+    """A library that must not be reached: the addresses would be the host's."""
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return lambda *args: 0
+        raise AssertionError(f"{name} was called")
+
+
+def test_tensors_of_the_host_are_refused(monkeypatch):
+    calls = serving_calls()
+    monkeypatch.setattr(B, "lib", lambda: Refusing())
+    for fn, args in calls:
+        with pytest.raises(ValueError, match="GPU"):
+            fn(*args)
+
+
+def test_a_workspace_is_on_the_inputs_device_and_counted_in_bytes(monkeypatch):
+    calls = serving_calls()
+    s = Streams(monkeypatch)
+    got = []
+    monkeypatch.setattr(Streams, "__getattr__",
+                        lambda self, name: lambda *args: got.append(args[-2]) or 0)
+    for fn, args in (calls[0], calls[2]):
+        fn(*args, ws=z(i, 1000))
+        fn(*args, ws=z(torch.uint8, 1000))
+        for bad in (torch.empty(1000, dtype=torch.uint8, device="meta"), z(torch.uint8, 2000)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                fn(*args, ws=bad)
+    assert got == [4000, 1000] * 2
