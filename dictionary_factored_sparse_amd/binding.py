@@ -11,8 +11,10 @@ The functions carry the C names.  Small holder classes (``DeviceDict``,
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, is_dataclass
 
 import torch
 
@@ -156,6 +158,44 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _used_on(out, stream) -> None:
+    """Tells the allocator that a call's results are used on ``stream`` too."""
+    if isinstance(out, torch.Tensor):
+        out.record_stream(stream)
+    elif isinstance(out, (list, tuple)):
+        for t in out:
+            _used_on(t, stream)
+    elif is_dataclass(out):
+        _used_on(list(vars(out).values()), stream)
+
+
+def _on(stream, fn, *args, **kw):
+    """fn(*args) with ``stream`` as the current stream: workspaces and outputs that it makes are
+    allocated and cleared in the order of that stream's work, and a workspace is not handed out
+    again while that work still uses it.  The output may be used on the caller's stream."""
+    before = torch.cuda.current_stream(stream.device)
+    if before == stream:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        out = fn(*args, **kw)
+    _used_on(out, before)
+    return out
+
+
+def _streamed(fn):
+    """A call with a parameter ``stream``: None is the current stream, another one is made the
+    current one for the call (see _on)."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.pop("stream", None)
+        if stream is None:
+            return fn(*args[:at], **kw)
+        return _on(stream, fn, *args[:at], **kw)
+    return call
+
+
 def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.float16:
         return DFS_F16
@@ -282,6 +322,7 @@ def dict_csc_capacity(nnz: int) -> int:
 
 # ----------------------------------------------------------------- packing
 
+@_streamed
 def dict_pack_csc(Cd: torch.Tensor, stream=None) -> DeviceCSC:
     """Dense (k, d_out) f16/f32 device tensor -> DeviceCSC (two calls: count,
     then fill into buffers sized from the count)."""
@@ -309,6 +350,7 @@ def dict_pack_csc(Cd: torch.Tensor, stream=None) -> DeviceCSC:
     return DeviceCSC(k, d_out, n, colptr, rowidx, vals=vals)
 
 
+@_streamed
 def dict_pack_bcsc(Cd: torch.Tensor, stream=None) -> DeviceCSC:
     """Dense (k, d_out) f16/f32 device tensor -> block-structured DeviceCSC
     (blocks of 8 consecutive atoms per column; count call, then fill)."""
@@ -336,6 +378,7 @@ def dict_pack_bcsc(Cd: torch.Tensor, stream=None) -> DeviceCSC:
     return DeviceCSC(k, d_out, n, colptr, bidx, vals=vals, block_rows=8)
 
 
+@_streamed
 def nvfp4_pack(x: torch.Tensor, stream=None) -> DeviceNVFP4:
     """fp32 device tensor (any shape, contiguous) -> DeviceNVFP4 of x.numel()."""
     assert x.dtype == torch.float32 and x.is_contiguous()
@@ -349,18 +392,21 @@ def nvfp4_pack(x: torch.Tensor, stream=None) -> DeviceNVFP4:
     return q
 
 
+@_streamed
 def nvfp4_unpack(q: DeviceNVFP4, stream=None) -> torch.Tensor:
     y = torch.empty(q.n, dtype=torch.float32, device=q.codes.device)
     _check("nvfp4_unpack", lib().nvfp4_unpack(q.nv(), q.n, y.data_ptr(), _stream(stream)))
     return y
 
 
+@_streamed
 def csc_to_nvfp4(c: DeviceCSC, stream=None) -> DeviceCSC:
     """Quantise a DeviceCSC's values (CSC order) to NVFP4, support unchanged."""
     v = c.vals[:c.nnz].float().contiguous()
     return DeviceCSC(c.k, c.d_out, c.nnz, c.colptr, c.rowidx, nv=nvfp4_pack(v, stream))
 
 
+@_streamed
 def csc_quantize8(c: DeviceCSC, kind: str, stream=None) -> DeviceCSC:
     """Quantise a DeviceCSC's f16/f32 values to 8-bit codes (``kind`` "fp8"
     or "int8", one scale per column); support shared with ``c``."""
@@ -405,6 +451,7 @@ def workspace_error_word(ws: torch.Tensor) -> int:
     return int(ws[128:132].view(torch.int32).item())
 
 
+@_streamed
 def dict_group_forward(Xs, D: DeviceDict, Cs, Ys=None, ydtype=torch.float16, ws=None,
                        stream=None):
     """Y_l = (X_l D) C_l for every layer of a group sharing D."""
@@ -431,6 +478,7 @@ def dict_group_forward(Xs, D: DeviceDict, Cs, Ys=None, ydtype=torch.float16, ws=
     return Ys
 
 
+@_streamed
 def dict_group_forward_noalloc(Xs, D: DeviceDict, Cs, Ys, stream=None):
     """dict_group_forward on the library's own workspace (no allocation in
     the call; Ys must be given)."""
@@ -462,6 +510,7 @@ def multi_workspace(n_dicts: int, n_layers: int, T: int, D: DeviceDict, Cs: Devi
     return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
+@_streamed
 def dict_multi_forward(Xs, Ds, Cs, Ys=None, ydtype=torch.float16, ws=None, stream=None):
     """Y[d * n + l] = (X_l D_d) C[d * n + l] for n = len(Xs) layers and the
     dictionaries Ds (q, k, v-like groups over the same activations); Cs is
@@ -489,6 +538,7 @@ def dict_multi_forward(Xs, Ds, Cs, Ys=None, ydtype=torch.float16, ws=None, strea
     return Ys
 
 
+@_streamed
 def dict_proj_forward(X, D: DeviceDict, Cs: DeviceCSC, Y=None, ydtype=torch.float16, ws=None,
                       stream=None):
     T = X.shape[0]
@@ -508,6 +558,7 @@ def dict_proj_forward(X, D: DeviceDict, Cs: DeviceCSC, Y=None, ydtype=torch.floa
     return Y
 
 
+@_streamed
 def dict_xd_forward(Xs, D: DeviceDict, zdtype=torch.float32, Z=None, ws=None, stream=None):
     n = len(Xs)
     T = Xs[0].shape[0]
@@ -530,6 +581,7 @@ def dict_xd_forward(Xs, D: DeviceDict, zdtype=torch.float32, Z=None, ws=None, st
     return Z
 
 
+@_streamed
 def dict_zc_forward(Z, T: int, Cs, Ys=None, ydtype=torch.float16, stream=None):
     n = len(Cs)
     d_out = Cs[0].d_out
@@ -673,20 +725,6 @@ def _stream_of(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _on(stream, fn, *args):
-    """fn(*args) with ``stream`` as the current stream: workspaces and outputs that it makes are
-    allocated and cleared in the order of that stream's work, and a workspace is not handed out
-    again while that work still uses it.  The output may be used on the caller's stream."""
-    before = torch.cuda.current_stream(stream.device)
-    if before == stream:
-        return fn(*args)
-    with torch.cuda.stream(stream):
-        out = fn(*args)
-    if out is not None:
-        out.record_stream(before)
-    return out
-
-
 def adapter_workspace(T: int, ad: DeviceAdapters, device) -> torch.Tensor:
     """Workspace of dict_adapter_forward for up to T tokens."""
     n = C.c_size_t(0)
@@ -805,6 +843,7 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
 
 # ----------------------------------------------------------------- producer steps
 
+@_streamed
 def dict_gram_inverse(D: DeviceDict, S: torch.Tensor, lam: float, stream=None):
     """P = (D^T S D + lam I)^-1 (k x k fp32).  Returns (P, error word): the
     error word is non-zero if the matrix was not positive definite."""
@@ -822,6 +861,7 @@ def dict_gram_inverse(D: DeviceDict, S: torch.Tensor, lam: float, stream=None):
     return P, ws[:4].view(torch.int32)
 
 
+@_streamed
 def dict_obs_prune(Cm: torch.Tensor, P: torch.Tensor, n_prune: int, stream=None):
     """Fixed-inverse pruning of every column of Cm (k x d_out fp32); returns
     (pruned coefficients fp32, keep mask uint8)."""
@@ -837,6 +877,7 @@ def dict_obs_prune(Cm: torch.Tensor, P: torch.Tensor, n_prune: int, stream=None)
     return out, keep
 
 
+@_streamed
 def dict_refit(W: torch.Tensor, Cm: torch.Tensor, lam: float, stream=None):
     """Refit D (C C^T + lam I) = W C^T.  W: d_in x N, Cm: k x N (fp32).
     Returns (Dt: k x d_in fp32 atom-major, error word)."""
@@ -886,6 +927,7 @@ def to_device_csc(dense_np, device, nvfp4: bool = False, fmt: str | None = None)
 
 # ----------------------------------------------------------------- measurement support
 
+@_streamed
 def probe_mfma(blocks: int, iters: int, device="cuda:0", out=None, stream=None):
     """Matrix-core probe: blocks x 256 threads, each wave `iters` rounds of 8
     independent 32x32x16 f16 MFMAs on registers (blocks * 4 * iters * 8 *
@@ -900,6 +942,7 @@ def probe_mfma_flop(blocks: int, iters: int) -> float:
     return float(blocks) * 4 * iters * 8 * 32768
 
 
+@_streamed
 def probe_read(buf, blocks: int, out=None, stream=None):
     """HBM read probe: reads every byte of the device tensor `buf` once
     (blocks x 256 threads, grid-strided 16-byte words).  Returns the

@@ -44,6 +44,8 @@ class Streams:
         def call(*args):
             if name.endswith("workspace_size"):
                 args[-1]._obj.value = 70000
+            elif name == "dict_csc_capacity":
+                return 16
             else:
                 self.launched.append(args[-1])
             return 0
@@ -71,6 +73,33 @@ def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
             assert s.launched == [want] and set(s.made) <= {want}, (fn.__name__, stream)
             assert s.made or fn is B.kv8_append
             assert s.now.cuda_stream == 1
+
+
+def test_the_projections_calls_too(monkeypatch):
+    """The same of the calls that pack, multiply and prune."""
+    D = B.DeviceDict.from_atoms(z(h, 16, 64))
+    c = B.DeviceCSC(16, 40, 8, z(i, 41), z(torch.int16, 16), vals=z(h, 16))
+    q = B.DeviceNVFP4.empty(32, "cpu")
+    X, Z, W, S = z(h, 3, 64), z(f, 3, 16), z(f, 16, 40), z(f, 64, 64)
+    calls = [(B.dict_group_forward, ([X], D, [c])), (B.dict_multi_forward, ([X], [D], [c])),
+             (B.dict_proj_forward, (X, D, c)), (B.dict_xd_forward, ([X], D)),
+             (B.dict_zc_forward, (Z, 3, [c])), (B.nvfp4_pack, (W,)), (B.nvfp4_unpack, (q,)),
+             (B.dict_pack_csc, (z(h, 16, 40),)), (B.dict_pack_bcsc, (z(h, 16, 40),)),
+             (B.csc_quantize8, (c, "fp8")), (B.csc_to_nvfp4, (c,)),
+             (B.dict_gram_inverse, (D, S, 0.1)), (B.dict_obs_prune, (W, z(f, 16, 16), 4)),
+             (B.dict_refit, (z(f, 64, 40), W, 0.1))]
+    s = Streams(monkeypatch)
+    for fn, args in calls:
+        for stream in (None, s.side, s.now):
+            s.made.clear()
+            s.launched.clear()
+            fn(*args, stream=stream)
+            want = (stream or s.now).cuda_stream
+            assert set(s.launched) == {want} and set(s.made) == {want}, (fn.__name__, stream)
+            assert s.now.cuda_stream == 1
+    s.launched.clear()
+    B.nvfp4_pack(W, s.side)                                  # by position
+    assert s.launched == [7]
 
 
 class Refusing:
