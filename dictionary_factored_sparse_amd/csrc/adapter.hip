@@ -694,6 +694,10 @@ struct Cut {
   int slices;    // of K in a launch of its own; 0: one launch
   bool planned;  // whether a launch before finds the tiles
 };
+constexpr int kSlots = 384;  // workgroups of the first launch, while there are fewer tiles
+int most_slices(const dfs_adapters& ad) {
+  return (ad.d_in + 2 * kShrinkWaves * kChunk - 1) / (2 * kShrinkWaves * kChunk);
+}
 Cut get_cut(int32_t T, const dfs_adapters& ad) {
   Cut c;
   // Tiles of 64 tokens read A and B a quarter as often, if adapters have that
@@ -714,8 +718,7 @@ Cut get_cut(int32_t T, const dfs_adapters& ad) {
   const int most = (ad.d_out + per - 1) / per;
   const int chunks = std::max(1, std::min(most, (both ? 512 : 1024) / busy));
   c.chunk = ((ad.d_out + chunks - 1) / chunks + kChunk - 1) / kChunk * kChunk;
-  const int k_most = (ad.d_in + 2 * kShrinkWaves * kChunk - 1) / (2 * kShrinkWaves * kChunk);
-  c.slices = both ? 0 : std::max(1, std::min(k_most, 384 / busy));
+  c.slices = both ? 0 : std::max(1, std::min(most_slices(ad), kSlots / busy));
   // A launch that plans costs 5.1 us at 1100 tokens and 9.9 at 4099, what the
   // workgroups do instead about 2 and 3; it is for what their LDS cannot hold.
   c.planned = T > kMidT || (T > kSmallT && ad.n > kMidN);
@@ -784,8 +787,35 @@ void go(const AdapterLaunch& a, const AdapterWs& w, const Cut& c, hipStream_t s)
 
 }  // namespace
 
-size_t adapter_ws_bytes(int32_t T, const dfs_adapters& ad) {
+size_t adapter_ws_need(int32_t T, const dfs_adapters& ad) {
   return T > 0 ? get_layout(T, ad, get_cut(T, ad)).total : 0;
+}
+
+// Enough for every call of up to T tokens.  A call's own need does not rise with
+// its tokens throughout: slices fall in whole steps, and tiles of 64 tokens are
+// fewer.  So each part is taken at the most that it can be.
+size_t adapter_ws_bytes(int32_t T, const dfs_adapters& ad) {
+  if (T <= 0) return 0;
+  const Cut c = get_cut(T, ad);
+  if (T <= kSmallT && c.slices == 0) return 0;  // so is every smaller batch
+  const bool planned = T > kMidT || (T > kSmallT && ad.n > kMidN);
+  const bool many = c.groups == kMany;
+  // tiles of 16 tokens end where those of 64 begin
+  const int64_t t16 = many ? std::min<int64_t>(T, std::max<int64_t>(kSmallT, (int64_t)kMany * kTok * (ad.n + 1)))
+                           : T;
+  auto busy = [&](int64_t t, int size) {
+    return std::min<int64_t>(t, t / size + std::min<int64_t>(ad.n + 1, t));
+  };
+  const int64_t tiles16 = std::max<int64_t>((std::min<int64_t>(T, kSmallT) + 7) / 8 * 8, busy(t16, kTok));
+  const int64_t tiles64 = many ? busy(T, kTok * kMany) : 0;
+  size_t bytes = 0;
+  if (planned) bytes += up((size_t)T * 4) + up((size_t)std::max(tiles16, tiles64) * 12) + 256;
+  bytes += std::max(up(tiles16 * sizeof(Tile<1>)), up(tiles64 * sizeof(Tile<kMany>)));
+  // slices * tokens: slices are at most kSlots / busy (or 1), busy is at least
+  // tokens / size
+  const int64_t rows = std::max<int64_t>(
+      T, std::min<int64_t>((int64_t)most_slices(ad) * T, (int64_t)kSlots * (many ? kTok * kMany : kTok)));
+  return bytes + (size_t)rows * get_layout(T, ad, c).rank_ld * 4;
 }
 
 hipError_t launch_adapter(const AdapterLaunch& a, void* ws, hipStream_t s) {

@@ -843,7 +843,7 @@ dfs_status dict_adapter_forward(const void* X, int32_t xdt, int32_t T, int64_t l
   if (T == 0) return DFS_OK;
   if (!ids) return DFS_E_INVALID;
   if ((uintptr_t)ids % 4 != 0) return DFS_E_ALIGN;
-  const size_t need = adapter_ws_bytes(T, *ad);
+  const size_t need = adapter_ws_need(T, *ad);
   if (need > 0) {
     if (!ws || ws_bytes < need) return DFS_E_WORKSPACE;
     if (!aligned16(ws)) return DFS_E_ALIGN;

@@ -248,7 +248,8 @@ struct AdapterLaunch {
   int32_t ydt;
   int64_t ldy;
 };
-size_t adapter_ws_bytes(int32_t T, const dfs_adapters& ad);
+size_t adapter_ws_need(int32_t T, const dfs_adapters& ad);   // of a call of T tokens
+size_t adapter_ws_bytes(int32_t T, const dfs_adapters& ad);  // of every call of up to T
 hipError_t launch_adapter(const AdapterLaunch& a, void* ws, hipStream_t s);
 
 constexpr int kMaxKvRequests = 65535;

@@ -392,7 +392,8 @@ typedef struct {
   const float* scale;
 } dfs_adapters;
 
-/* Workspace bytes of dict_adapter_forward for T tokens.  Need not be zeroed. */
+/* Workspace bytes of dict_adapter_forward for any call of up to T tokens with
+ * this pool.  Need not be zeroed. */
 dfs_status dict_adapter_workspace_size(int32_t T, const dfs_adapters* ad, size_t* bytes);
 
 /* Low-rank adapters of many requests beside a shared projection: for every

@@ -43,3 +43,18 @@ def test_calls_on_a_stream_given_by_argument():
         o = B.kv8_attention(c.kv, Q, start, length, c.tab, 4, stream=side)
         side.synchronize()
         assert torch.equal(y, Y) and torch.equal(o, O)
+
+
+def test_one_adapter_workspace_for_every_smaller_batch():
+    """A workspace for 9000 tokens, full of NaN, serves smaller batches in any order."""
+    rng = np.random.default_rng(2)
+    for n, r_max in ((3, 32), (24, 64), (300, 8)):
+        ad, _ = make_adapters(rng, n, r_max, 1096, 72, rng.integers(1, r_max + 1, n))
+        X, ids = halves(rng, 9000, 1096), ints(rng.integers(-1, n, 9000))
+        ws = B.adapter_workspace(9000, ad, DEV)
+        for T in (9000, 5, 300, 1, 8192, 64, 191, 192, 256, 257, 1024, 8193):
+            say(f"case: adapters, one workspace, n={n} T={T}")
+            ws.fill_(0xFF)
+            y = B.dict_adapter_forward(X[:T], ad, ids[:T], ws=ws)
+            assert torch.equal(y, B.dict_adapter_forward(X[:T], ad, ids[:T]))
+            assert torch.isfinite(y).all()

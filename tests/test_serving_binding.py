@@ -132,3 +132,30 @@ def test_a_workspace_is_on_the_inputs_device_and_counted_in_bytes(monkeypatch):
             with pytest.raises(ValueError, match="workspace"):
                 fn(*args, ws=bad)
     assert got == [4000, 1000] * 2
+
+
+def test_adapter_workspace_holds_every_smaller_batch():
+    """The size rises with T, and no call of up to T tokens asks for more: the library is given
+    the size for T and reaches its next check (a workspace that is not aligned) at every T'."""
+    import ctypes as C
+    P, n = 0x10000, C.c_size_t(0)
+    lib = B.lib()
+    steps = sorted({*range(1, 600), *range(600, 9000, 7), 1151, 1152, 4099, 7679, 7680, 8191, 8192,
+                    8193, 8194, 12000, 16384, 40000, 100000, 1000003})
+    for pool, r, d_in, d_out in ((24, 64, 11008, 4096), (8, 32, 4096, 4096), (1, 8, 64, 64),
+                                 (1, 256, 5120, 96), (512, 16, 2048, 2048), (5000, 64, 8192, 256),
+                                 (16000, 33, 1000, 500), (3, 200, 30000, 64)):
+        ad = B.Adapters(pool, r, d_in, d_out, P, -(-d_in // 8) * 8, 0, P, -(-r // 8) * 8, 0, P, P)
+
+        def forward(T, size):
+            return lib.dict_adapter_forward(P, B.DFS_F16, T, -(-d_in // 8) * 8, C.byref(ad), P,
+                                            None, 0, P, B.DFS_F16, d_out, P + 8, size, None)
+
+        sizes = []
+        for T in steps:
+            assert lib.dict_adapter_workspace_size(T, C.byref(ad), C.byref(n)) == 0
+            sizes.append(n.value)
+        assert sizes == sorted(sizes), (pool, r, d_in)
+        for T, size in zip(steps, sizes):
+            if size:                # 4: past the check of the size; none needed reaches no launch
+                assert forward(T, size) == 4, (pool, r, d_in, T)
