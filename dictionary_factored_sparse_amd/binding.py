@@ -801,13 +801,15 @@ def kv8_append(kv: DeviceKV8, K, V, tok_start, cached, table, stream=None) -> No
 
 def kv8_attention_workspace(kv: DeviceKV8, n_req: int, n_tok: int, q_heads: int,
                             device) -> torch.Tensor:
-    """Workspace of kv8_attention, zeroed (its first part must be zero before
-    its first use)."""
+    """Workspace of kv8_attention for any call of up to n_req requests and n_tok tokens, its
+    first 64 KiB zeroed (as they must be before its first use)."""
     n = C.c_size_t(0)
     _check("kv8_attention_workspace_size",
            lib().kv8_attention_workspace_size(C.byref(kv.desc()), n_req, n_tok, q_heads,
                                               C.byref(n)))
-    return torch.zeros(n.value, dtype=torch.uint8, device=device)
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
 
 
 def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_scale=None,

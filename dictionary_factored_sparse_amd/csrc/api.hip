@@ -902,7 +902,7 @@ dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const 
   if (n_req == 0 || n_tok == 0) return DFS_OK;
   if (!Q || !O) return DFS_E_INVALID;
   if (!aligned16(Q) || !elem_aligned(O, odt)) return DFS_E_ALIGN;
-  const size_t need = kv8_attention_ws_bytes(*kv, n_req, n_tok, q_heads);
+  const size_t need = kv8_attention_ws_need(*kv, n_req, n_tok, q_heads);
   if (need > 0) {
     if (!ws || ws_bytes < need) return DFS_E_WORKSPACE;
     if (!aligned16(ws)) return DFS_E_ALIGN;

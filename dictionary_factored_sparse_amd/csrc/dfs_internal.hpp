@@ -278,6 +278,8 @@ struct KvAttnLaunch {
   int32_t odt;
   int64_t ldo;
 };
+// Workspace of a call, and of every call of up to n_req requests and n_tok tokens.
+size_t kv8_attention_ws_need(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
 size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
 hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s);
 

@@ -1048,8 +1048,19 @@ void go_kind(const KvAttnLaunch& a, const AttnWs& w, const Cut& c, hipStream_t s
 
 }  // namespace
 
-size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
+size_t kv8_attention_ws_need(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
   return get_layout(get_cut(kv, n_req, n_tok, q_heads), kv.head_dim).total;
+}
+
+// Enough for every call of up to n_req requests and n_tok tokens: fewer requests
+// have more rows each, so that blocks can be larger than this call's, and the
+// smallest blocks are for at most 16 rows a request.
+size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
+  const int64_t rows = (int64_t)n_tok * (q_heads / kv.heads);
+  Cut c = get_cut(kv, 1, n_tok, q_heads);  // the largest blocks
+  c.entries = std::min(n_req, n_tok) +
+              std::max(std::min<int64_t>(rows / 16, std::max(n_req, 1)), rows / 128);
+  return get_layout(c, kv.head_dim).total;
 }
 
 hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s) {

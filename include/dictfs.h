@@ -469,8 +469,9 @@ dfs_status kv8_append(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int
                       int32_t table_pages, const void* K, int64_t ldk, const void* V, int64_t ldv,
                       int32_t dtype, void* stream);
 
-/* Workspace bytes of kv8_attention for n_req requests with n_tok query tokens
- * in all. */
+/* Workspace bytes of kv8_attention for any call of up to n_req requests with up
+ * to n_tok query tokens in all, over a cache of this form and for q_heads.  A
+ * batch of one request may need the most, so the size is that of the largest. */
 dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
                                         int32_t q_heads, size_t* bytes);
 

@@ -58,3 +58,24 @@ def test_one_adapter_workspace_for_every_smaller_batch():
             y = B.dict_adapter_forward(X[:T], ad, ids[:T], ws=ws)
             assert torch.equal(y, B.dict_adapter_forward(X[:T], ad, ids[:T]))
             assert torch.isfinite(y).all()
+
+
+def test_one_attention_workspace_for_every_smaller_batch():
+    """A workspace for 12 requests and 700 tokens serves decode batches, drafts, prompts and many
+    kinds of batches between, in any order; only its first 64 KiB are cleared, once."""
+    rng = np.random.default_rng(3)
+    lengths = [900, 700, 64, 1, 130, 333, 17, 500, 250, 80, 40, 700]
+    c = Cache(rng, "int8", 2, 64, 32, lengths)
+    H = 6
+    ws = B.kv8_attention_workspace(c.kv, 12, 700, H, DEV)
+    ws[65536:] = 0xFF
+    Q = halves(rng, 700, H * 64)
+    for r0, r1, new in ((0, 12, 1), (0, 1, 700), (0, 12, 7), (3, 4, 1), (0, 2, 300), (7, 12, 3),
+                        (0, 1, 11), (0, 6, 60), (0, 1, 5), (2, 3, 64), (0, 12, 1)):
+        n = np.minimum(new, lengths[r0:r1])
+        say(f"case: attention, one workspace, requests {r0}..{r1 - 1}, new {n.tolist()}")
+        args = (c.kv, Q[:n.sum()], ints(np.concatenate([[0], np.cumsum(n)])), ints(lengths[r0:r1]),
+                c.tab[r0:r1], H)
+        o = B.kv8_attention(*args, ws=ws)
+        assert not ws[:65536].any()
+        assert torch.equal(o, B.kv8_attention(*args)) and torch.isfinite(o).all()

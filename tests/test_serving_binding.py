@@ -159,3 +159,26 @@ def test_adapter_workspace_holds_every_smaller_batch():
         for T, size in zip(steps, sizes):
             if size:                # 4: past the check of the size; none needed reaches no launch
                 assert forward(T, size) == 4, (pool, r, d_in, T)
+
+
+def test_attention_workspace_holds_every_smaller_batch():
+    """The size rises with the requests and with the tokens, and no call of up to that many asks
+    for more (as above: the check after the size's is reached)."""
+    import ctypes as C
+    P, n = 0x10000, C.c_size_t(0)
+    lib = B.lib()
+    reqs = [1, 2, 3, 5, 15, 16, 17, 32, 33, 63, 255, 256, 257, 1000, 65535]
+    toks = [1, 2, 4, 8, 15, 16, 17, 31, 32, 33, 64, 100, 512, 1000, 4097, 8192, 70000]
+    for heads, group, dim in ((8, 1, 128), (8, 4, 128), (4, 3, 64), (2, 17, 96), (1, 32, 256)):
+        kv = B.KV8(8, heads, dim, 64, B.DFS_FP8, 0, P, P, P, P)
+        H, size = heads * group, {}
+        for r in reqs:
+            for t in toks:
+                assert lib.kv8_attention_workspace_size(C.byref(kv), r, t, H, C.byref(n)) == 0
+                size[r, t] = n.value
+                assert lib.kv8_attention(C.byref(kv), r, t, P, P, P, 4, 4, P, H * dim, H, 0.1, 0, 0,
+                                         P, B.DFS_F16, H * dim, P + 8, n.value, None) == 4
+        for a, b in zip(reqs, reqs[1:]):
+            assert all(size[a, t] <= size[b, t] for t in toks), (heads, group, dim, a)
+        for a, b in zip(toks, toks[1:]):
+            assert all(size[r, a] <= size[r, b] for r in reqs), (heads, group, dim, a)
