@@ -492,12 +492,12 @@ dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_
  *   q_heads % heads == 0.  tok_start as for kv8_append; rows of O that belong
  *   to no request are not written.  length below 0 counts as 0, and positions
  *   from table_pages * page on hold no key.
- * Scores, softmax statistics and sums are fp32.  The softmax weights enter
- * the second product as the sum of two f16 values, but for prompts (more than
- * 32 rows of a request to a kv head on average) with F16 output as one, which
- * errs by as much as the output's own rounding.  Scales are not negative.
- * Non-finite
- * cache contents outside the visible positions do not reach the output.
+ * Scores, softmax statistics and sums are fp32.  The softmax weights, each
+ * times its page's value scale, enter the second product as the sum of two f16
+ * values: to 2^-21 of themselves, or to 2^-37 of the row's largest one.  Scales
+ * are not negative.  A row depends on nothing but the keys that it sees: NaN
+ * codes and scales that are not finite reach the rows that see a key of theirs
+ * (a NaN code of V one dimension of them), and no other.
  * The workspace's first 64 KiB must be zero before its first use; every call
  * leaves them zero again.  Calls sharing a workspace must not run
  * concurrently.  Work is split over the keys by lengths read on the device,

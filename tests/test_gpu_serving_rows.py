@@ -145,6 +145,24 @@ def test_scales_at_the_ends_of_fp32():
         check(c, new, lengths, group, "f32")
 
 
+# ------------------------------------------------------------------------------- f16 output
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,lengths,group", [
+    ([1] * 90, [150 + 2 * r for r in range(90)], 2), ([3] * 20, [200 + r for r in range(20)], 4),
+    ([64], [200], 2), ([200, 90], [330, 90], 1)])
+def test_f16_output_has_only_its_own_rounding(kind, new, lengths, group):
+    """The weights keep two f16 values where the output is f16 too.  With one, a weight errs by up
+    to 2^-12 of itself, and over values of both signs the sum by as much as the output's rounding:
+    together 1.4 times that in the mean.  With two, nothing else comes near 2^-14."""
+    c = Cache(np.random.default_rng(6), kind, 2, 128, 64, lengths)
+    Q = np.random.default_rng(7).standard_normal((sum(new), 2 * group * 128)).astype(np.float16)
+    got = check(c, new, lengths, group, "f16", Q=Q)
+    ref, _ = row_reference(c, Q.astype(np.float64), new, lengths, group, 0, 0, "f16")
+    rms = lambda e: float(np.sqrt((e ** 2).mean()))  # noqa: E731
+    assert rms(got - ref) <= 1.1 * rms(ref.astype(np.float16).astype(np.float64) - ref)
+
+
 # ------------------------------------------------------------------------------- NaN
 
 def places(lengths):
