@@ -15,10 +15,12 @@
 // and a second one does the outputs (get_cut holds both sides' times).
 //
 // Measured: 4 tokens of 4 adapters of rank 16, 4096 -> 4096: 9.2 us.  61 tokens
-// of 24 adapters of ranks to 64, 11008 -> 4096 (37 MB): 15.4 and 10.6 us; the
-// first reads 16 rows of A, 64 bytes each, per instruction, and takes 10.7 if A
-// lies in the order of those reads.  4099 tokens of 7 prompts, ranks to 32, 4096 -> 4096
-// (102 MB): 19.4 and 22.0 us, 2.5 TB/s in all; finding the tiles takes 3 of it.
+// of 24 adapters of ranks to 64, 11008 -> 4096 (37 MB): 15.6 and 10.5 us, 25.8 a
+// call among others; the first reads 16 rows of A, 64 bytes each, per
+// instruction, and takes 10.7 if A lies in the order of those reads.  4099 tokens
+// of 7 prompts, ranks to 32, 4096 -> 4096 (102 MB): 19.5 and 22.1 us, 46.5 a call
+// (2.2 TB/s): 5 go between and about the two launches, and finding the tiles
+// takes 3 of the first.
 //
 // Rounding.  X, A and B are f16 and products of them exact in fp32; sums are
 // fp32.  U enters the second product as the sum of two f16 values, 22 bits,

@@ -10,13 +10,15 @@
 // stored with the page's tokens contiguous: a lane packs the codes of four
 // tokens into a word, and the words go out through LDS.
 //
-// What bounds it: prompts, the bytes (source read, codes written): 8400 tokens
-// of 32 heads of 128 from f16 take 58 us, 3.6 TB/s over 206 MB, against 83
+// What bounds it: prompts, the bytes (source read, codes written): 7191 tokens
+// of 32 heads of 128 from f16 take 58 us, 3.0 TB/s over 177 MB, against 83
 // with a workgroup for K and one for V and value codes stored without LDS.
-// Single tokens, the chain of dependent reads (requests, page table, scale) and
-// pages coded anew: 10.6 us for 32 requests of 32 heads, 7.5 for 444 tokens of
-// 8 heads on pages of 16 (with plain divisions, and FP8 codes made by bit
-// operations and stored one by one, 21.6 and 13.1; prompts 254).
+// Single tokens, the chain of dependent reads (requests, page table, scale):
+// 10.8 us for 32 requests of 32 heads, 7.7 for 346 tokens of 8 heads on pages of
+// 16 (with plain divisions, and FP8 codes made by bit operations and stored one
+// by one, 21.6 and 13.1; prompts 254).  These are calls whose pages keep their
+// scales.  Where the new tokens raise some, older codes of those pages are coded
+// anew: 15.5 and 8.4 us for the kernel alone, against 11.2 and 7.8.
 #include <algorithm>
 #include <type_traits>
 

@@ -30,8 +30,8 @@
 //
 // Rounding.  w' enters the second product as the sum of two f16 values: f16
 // output is then as near to exact as its own rounding allows (2.1e-4 of the
-// norm).  One f16 value gave 3.2e-4 at 238 us for the prompts below, which take
-// 256 with two; for few rows two cost at most 2% (24 windowed requests 48.0 us
+// norm).  One f16 value gave 3.2e-4 and took 238 us for the prompts below where
+// two took 256; for few rows two cost at most 2% (24 windowed requests 48.0 us
 // with one, 49.0; 32 long ones 190.0, 190.7).  Weights are kept at 2^13 times their
 // value so that f16's normal range reaches 2^-27 of the largest, and c is
 // raised only when a key passes it by more than 2 (weights stay below 2^15),
@@ -46,17 +46,18 @@
 // joined by the workgroup that finishes last, in slice order, so results do
 // not depend on which that is.
 //
-// What bounds it, as measured (head_dim 128 unless stated).  Decode: the codes,
-// read once.  32 requests of 80 to 8192 tokens, 32 heads: 190 us for 1.05 GB,
-// 5.5 TB/s (a plain read of 1 GiB: 5.84); 4 tokens over 131071, 8 kv heads for
-// 32: 64 us, 4.2 TB/s; 24 int8 requests under a window of 4096, pages of 16: 47
-// us, 4.2 TB/s; these two end with a join.  One request of 777 tokens: 10.4 us,
-// chain of plan, pages, codes, join.  Prompts: vector instructions (conversions,
-// exponentials, masks), which the matrix instructions hide behind: VALU busy 60%
-// of the time, matrix cores 23%.  3 chunks of 2048 tokens over 1021 to 3069
-// cached ones: 256 us, 0.56 PFLOP/s.  Sharing the
-// converted codes of a tile between the waves through LDS costs a barrier per
-// tile: 303 us where each wave converting for itself took 281.
+// What bounds it, as measured (head_dim 128 unless stated; times of a call among
+// others).  Decode: the codes, read once.  32 requests of 646 to 8192 tokens, 32
+// heads: 191 us for 1.05 GB, 5.5 TB/s (a plain read of 1 GiB: 5.84); 4 tokens over
+// 131071, 8 kv heads for 32: 65 us, 4.1 TB/s; 24 int8 requests under a window of
+// 4096, pages of 16: 50 us, 3.9 TB/s; these two end with a join.  One request of
+// 777 tokens: 10.3 us, chain of plan, pages, codes, join.  Prompts: the vector
+// units are busy 61% of the time (conversions, exponentials, masks), the matrix
+// cores 37%, neither full.  3 chunks of 1500 to 2048 tokens over 495 to 1021
+// cached ones: 261 us, 0.55 PFLOP/s.  Sharing the converted codes of a tile
+// between the waves through LDS costs a barrier per tile: 303 us where each wave
+// converting for itself took 281.  head_dim 256: 32 requests to 8000 tokens, 8 kv
+// heads for 16, 117 us; 3 chunks to 1024 tokens over to 500, 4 for 16, 163 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -989,7 +990,8 @@ Cut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads) {
   c.entries = std::min<int64_t>(n_req, n_tok) + (int64_t)n_tok * g / c.qb;
   // as many workgroups as the device holds at once: two per CU, one where a
   // wave needs more than half of a SIMD's registers (half as many: 269 against
-  // 254 us for prompts, 71 against 64 with a window, 197 against 191 at decode)
+  // 254 us for prompts, 71 against 64 with a window, 197 against 191 at decode;
+  // head_dim 256 with 512: 230 against 163 for prompts, 124 against 117 at decode)
   c.slices = kv.head_dim == 256 ? 256 : 512;
   return c;
 }
