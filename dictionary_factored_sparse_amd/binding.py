@@ -158,27 +158,31 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
-def _used_on(out, stream) -> None:
-    """Tells the allocator that a call's results are used on ``stream`` too."""
-    if isinstance(out, torch.Tensor):
-        out.record_stream(stream)
-    elif isinstance(out, (list, tuple)):
-        for t in out:
-            _used_on(t, stream)
-    elif is_dataclass(out):
-        _used_on(list(vars(out).values()), stream)
+def _tensors(x):
+    """The tensors of an argument or result: one, lists of them, holder classes."""
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, (list, tuple)):
+        for y in x:
+            yield from _tensors(y)
+    elif is_dataclass(x):
+        yield from _tensors(list(vars(x).values()))
 
 
 def _on(stream, fn, *args, **kw):
     """fn(*args) with ``stream`` as the current stream: workspaces and outputs that it makes are
     allocated and cleared in the order of that stream's work, and a workspace is not handed out
     again while that work still uses it.  The output may be used on the caller's stream."""
+    for t in _tensors(args):
+        if t.device != stream.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
     before = torch.cuda.current_stream(stream.device)
     if before == stream:
         return fn(*args, **kw)
     with torch.cuda.stream(stream):
         out = fn(*args, **kw)
-    _used_on(out, before)
+    for t in _tensors(out):
+        t.record_stream(before)
     return out
 
 

@@ -102,6 +102,16 @@ def test_the_projections_calls_too(monkeypatch):
     assert s.launched == [7]
 
 
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    calls = serving_calls() + [(B.nvfp4_pack, (z(f, 16, 40),))]
+    s = Streams(monkeypatch)
+    s.side.device = torch.device("meta")
+    for fn, args in calls:
+        with pytest.raises(ValueError, match="stream of"):
+            fn(*args, stream=s.side)
+    assert not s.launched
+
+
 class Refusing:
     """A library that must not be reached: the addresses would be the host's."""
 
