@@ -192,11 +192,12 @@ def _streamed(fn):
     at = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
-    def call(*args, **kw):
-        stream = args[at] if len(args) > at else kw.pop("stream", None)
+    def call(*args, stream=None, **kw):
+        if len(args) > at:
+            stream, args = args[at], args[:at]
         if stream is None:
-            return fn(*args[:at], **kw)
-        return _on(stream, fn, *args[:at], **kw)
+            return fn(*args, **kw)
+        return _on(stream, fn, *args, **kw)
     return call
 
 
