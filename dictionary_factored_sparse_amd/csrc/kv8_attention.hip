@@ -401,7 +401,8 @@ struct Attn {
   h8 qf[NQ][kSteps];
   f4 o[NQ][kDims];
   float m[NQ], l[NQ];
-  float c[NQ];  // o is in units of 2^(c - 13), l of 2^(m - 13)
+  float c[NQ];  // o is in units of 2^(c - 13), l of 2^(m - 13); whole numbers, so
+                // that what they put into exponents and factors is exact
   uint32_t kraw[4][D / 16];  // K codes of the tile to come
   float ks, vs;              // and the scales of this lane's key block in it
   // pages of a tile: of this lane's K rows, and of its key block
@@ -636,7 +637,7 @@ struct Attn {
     if (__ballot(far) != 0) {
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const float top = fmaxf(max4(mx[i]), m[i]);
+        const float top = fmaxf(ceilf(max4(mx[i])), m[i]);
         l[i] *= __builtin_amdgcn_exp2f(m[i] - top);
         m[i] = top;
       }
@@ -645,16 +646,15 @@ struct Attn {
     float alpha[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const float mo = max4(mx[i] + (ve + lf));
+      const float mo = ceilf(max4(mx[i] + (ve + lf)));
       const bool up = mo > c[i] + kSlack;
       alpha[i] = up ? __builtin_amdgcn_exp2f(c[i] - mo) : 1.0f;
       c[i] = up ? mo : c[i];
       rescale = rescale || up;
       // Contributions below 2^(kFar - kLeast) of the largest may count as that: as
       // f16 they are 0, and the sum of the weights keeps its part of them.
-      const float rel = fmaxf((ve - c[i]) + lf, -kLeast - m[i]);
-      const float back = __builtin_amdgcn_exp2f(-rel - m[i]);
-      const float add = kWeightBits + rel;
+      const float add = fmaxf((ve + kWeightBits - c[i]) + lf, kWeightBits - kLeast - m[i]);
+      const float back = __builtin_amdgcn_exp2f((kWeightBits - m[i]) - add);
       float sum = 0.0f;
 #pragma unroll
       for (int x = 0; x < 16; ++x)
@@ -705,14 +705,13 @@ struct Attn {
       l[i] = sum4(l[i]);
       const int e = __builtin_amdgcn_frexp_expf(l[i]);
       l[i] = __builtin_amdgcn_ldexpf(l[i], -e);
-      const float by = fmaxf(c[i] - m[i], -1000.0f), whole = floorf(by);
-      const float f = __builtin_amdgcn_exp2f(by - whole);
+      const int by = (int)fmaxf(c[i] - m[i], -1000.0f) - e;
       m[i] += (float)e - kWeightBits;
 #pragma unroll
       for (int d = 0; d < kDims; ++d)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          o[i][d][x] = __builtin_amdgcn_ldexpf(o[i][d][x] * f, (int)whole - e);
+          o[i][d][x] = __builtin_amdgcn_ldexpf(o[i][d][x], by);
     }
   }
 
