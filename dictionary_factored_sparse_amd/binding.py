@@ -39,7 +39,10 @@ SYMBOLS = ("dict_pack_csc_workspace_size", "dict_pack_csc", "nvfp4_pack_workspac
            "dfs_probe_read",
            "dict_multi_workspace_size", "dict_multi_forward", "dict_group_forward_noalloc",
            "dict_adapter_workspace_size", "dict_adapter_forward", "kv8_append",
-           "kv8_attention_workspace_size", "kv8_attention")
+           "kv8_attention_workspace_size", "kv8_attention",
+           "kv8_prefix_attention_workspace_size", "kv8_prefix_attention", "kv8_tables",
+           "kv8_release", "kv8_reorder_workspace_size", "kv8_reorder", "kv8_copy_pages",
+           "beam_select_workspace_size", "beam_select")
 
 
 class NV(C.Structure):
@@ -133,6 +136,19 @@ def lib():
             "kv8_attention_workspace_size": [C.POINTER(KV8), i32, i32, i32, psz],
             "kv8_attention": [C.POINTER(KV8), i32, i32, vp, vp, vp, i64, i32, vp, i64, i32,
                               C.c_float, i32, i32, vp, i32, i64, vp, sz, vp],
+            "kv8_prefix_attention_workspace_size": [C.POINTER(KV8), i32, i32, i32, psz],
+            "kv8_prefix_attention": [C.POINTER(KV8), i32, i32, vp, vp, vp, i64, i32, i32, vp, vp,
+                                     vp, i64, i32, C.c_float, i32, i32, vp, i32, i64, vp, sz, vp],
+            "kv8_tables": [i32, i32, i32, vp, vp, vp, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp,
+                           vp],
+            "kv8_release": [i32, i32, vp, vp, i64, i32, vp, vp, vp],
+            "kv8_reorder_workspace_size": [i32, psz],
+            "kv8_reorder": [i32, i32, i32, i32, vp, vp, i64, vp, vp, i32, vp, i64, i32, vp, vp,
+                            vp, vp, vp, sz, vp],
+            "kv8_copy_pages": [i32, C.POINTER(KV8), i32, vp, vp, vp, vp],
+            "beam_select_workspace_size": [i32, i32, i32, psz],
+            "beam_select": [i32, i32, i32, vp, i32, i64, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz,
+                            vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -846,6 +862,261 @@ def kv8_attention(kv: DeviceKV8, Q, tok_start, length, table, q_heads: int, sm_s
     if st:
         raise DfsError("kv8_attention", st)
     return O
+
+
+def kv8_prefix_attention_workspace(kv: DeviceKV8, n_req: int, n_tok: int, q_heads: int,
+                                   device) -> torch.Tensor:
+    """Workspace of kv8_prefix_attention for any call of up to n_req requests and n_tok tokens,
+    its first 64 KiB zeroed (as they must be before its first use)."""
+    n = C.c_size_t(0)
+    _check("kv8_prefix_attention_workspace_size",
+           lib().kv8_prefix_attention_workspace_size(C.byref(kv.desc()), n_req, n_tok, q_heads,
+                                                     C.byref(n)))
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
+
+
+def kv8_prefix_attention(kv: DeviceKV8, Q, tok_start, length, table, group_start, shared,
+                         q_heads: int, sm_scale=None, window: int = 0, sinks: int = 0, O=None,
+                         odtype=torch.float16, ws=None, stream=None):
+    """kv8_attention where the requests group_start[i] .. group_start[i+1]-1 have their first
+    shared[i] tokens in the same pages: these are read once for all of them.  Returns O."""
+    if stream is not None:
+        return _on(stream, kv8_prefix_attention, kv, Q, tok_start, length, table, group_start,
+                   shared, q_heads, sm_scale, window, sinks, O, odtype, ws)
+    n_req, ldt, pages = _kv_batch(kv, tok_start, length, table)
+    n_tok, cols, n_groups = Q.shape[0], q_heads * kv.head_dim, shared.shape[0]
+    ldq = _matrix(Q, "Q", None, cols)
+    _ints(shared, "shared", n_groups)
+    _ints(group_start, "group_start", n_groups + 1)
+    if Q.dtype != torch.float16:
+        raise TypeError("Q must be float16")
+    if O is None:
+        O = torch.empty(n_tok, cols, dtype=odtype, device=Q.device)
+    ldo = _matrix(O, "O", n_tok, cols)
+    odt = _dt(O)
+    _on_device((kv.k, Q, O, tok_start, length, table, group_start, shared), "cache")
+    if ws is None:
+        ws = kv8_prefix_attention_workspace(kv, n_req, n_tok, q_heads, Q.device)
+    st = lib().kv8_prefix_attention(kv._ref, n_req, n_tok, tok_start.data_ptr(), length.data_ptr(),
+                                    table.data_ptr(), ldt, pages, n_groups, group_start.data_ptr(),
+                                    shared.data_ptr(), Q.data_ptr(), ldq, q_heads,
+                                    kv.head_dim ** -0.5 if sm_scale is None else sm_scale, window,
+                                    sinks, O.data_ptr(), odt, ldo, ws.data_ptr(), _ws_bytes(ws, Q),
+                                    _stream_of(Q))
+    if st:
+        raise DfsError("kv8_prefix_attention", st)
+    return O
+
+
+# ----------------------------------------------------------------- pages of the cache, beams
+
+@dataclass
+class DeviceBatch:
+    """What kv8_tables makes of a batch of n_req requests in n_tok rows: ``tok_start``
+    int32[n_req + 1], ``length`` int32[n_req], ``tok_req``, ``tok_pos`` int32[n_tok] and ``slot``
+    int64[n_tok] (each may be None: not wanted), ``missing`` int32[1]."""
+    tok_start: torch.Tensor
+    length: torch.Tensor
+    tok_req: torch.Tensor | None
+    tok_pos: torch.Tensor | None
+    slot: torch.Tensor | None
+    missing: torch.Tensor
+    n_tok: int
+
+    def __post_init__(self):
+        n_req = self.length.shape[0]
+        _ints(self.length, "length", n_req)
+        _ints(self.tok_start, "tok_start", n_req + 1)
+        _ints(self.missing, "missing", 1)
+        for t, what in ((self.tok_req, "tok_req"), (self.tok_pos, "tok_pos")):
+            if t is not None:
+                _ints(t, what, self.n_tok)
+        s = self.slot
+        if s is not None and (s.shape != (self.n_tok,) or s.dtype != torch.int64
+                              or not s.is_contiguous()):
+            raise ValueError(f"slot: contiguous int64 of {self.n_tok} values required")
+        _same_device([t for t in vars(self).values() if isinstance(t, torch.Tensor)], "batch")
+
+    @staticmethod
+    def empty(n_req: int, n_tok: int, device) -> "DeviceBatch":
+        e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)  # noqa: E731
+        return DeviceBatch(e(n_req + 1), e(n_req), e(n_tok), e(n_tok), e(n_tok, torch.int64), e(1),
+                           n_tok)
+
+
+def _table(t: torch.Tensor, what: str, rows: int | None = None) -> int:
+    """Checks rows of a page table; their stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != torch.int32 or (stride[1] != 1 and shape[1] > 1 and shape[0]):
+        raise ValueError(f"{what}: int32 rows with unit column stride required")
+    if rows is not None and shape[0] != rows:
+        raise ValueError(f"{what}: {shape[0]} rows, expected {rows}")
+    return max(stride[0], shape[1]) if shape[0] <= 1 else stride[0]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv8_tables(refs, page: int, cached, n_new, table, batch: DeviceBatch | None = None,
+               n_tok: int | None = None, stream=None) -> DeviceBatch:
+    """Pages for the new tokens of a batch, in ``table`` and ``refs`` (in place), and its starts,
+    lengths and slot maps in ``batch`` (made for ``n_tok`` rows if None).  Returns the batch."""
+    if stream is not None:
+        return _on(stream, kv8_tables, refs, page, cached, n_new, table, batch, n_tok)
+    n_req = cached.shape[0]
+    _ints(refs, "refs", refs.shape[0])
+    _ints(cached, "cached", n_req)
+    _ints(n_new, "n_new", n_req)
+    ldt = _table(table, "table", n_req)
+    if batch is None:
+        if n_tok is None:
+            raise ValueError("a batch, or the rows of one to make, required")
+        batch = DeviceBatch.empty(n_req, n_tok, refs.device)
+    b = batch
+    if b.length.shape[0] != n_req or (n_tok is not None and n_tok != b.n_tok):
+        raise ValueError(f"batch: made for {b.length.shape[0]} requests and {b.n_tok} rows")
+    _on_device((refs, cached, n_new, table, b.tok_start), "pages")
+    st = lib().kv8_tables(n_req, page, refs.shape[0], refs.data_ptr(), cached.data_ptr(),
+                          n_new.data_ptr(), b.n_tok, table.data_ptr(), ldt, table.shape[1],
+                          b.tok_start.data_ptr(), b.length.data_ptr(), _ptr(b.tok_req),
+                          _ptr(b.tok_pos), _ptr(b.slot), b.missing.data_ptr(), _stream_of(refs))
+    if st:
+        raise DfsError("kv8_tables", st)
+    return b
+
+
+def kv8_release(refs, table, first=None, last=None, stream=None) -> None:
+    """Give back the pages of the entries first[r] .. last[r]-1 of each row of ``table`` (None:
+    from 0, to the row's end); both tensors change in place."""
+    if stream is not None:
+        return _on(stream, kv8_release, refs, table, first, last)
+    n_req = table.shape[0]
+    _ints(refs, "refs", refs.shape[0])
+    ldt = _table(table, "table")
+    given = [refs, table]
+    for t, what in ((first, "first"), (last, "last")):
+        if t is not None:
+            _ints(t, what, n_req)
+            given.append(t)
+    _on_device(given, "pages")
+    st = lib().kv8_release(n_req, refs.shape[0], refs.data_ptr(), table.data_ptr(), ldt,
+                           table.shape[1], _ptr(first), _ptr(last), _stream_of(refs))
+    if st:
+        raise DfsError("kv8_release", st)
+
+
+def kv8_reorder_workspace(n_in: int, device) -> torch.Tensor:
+    """Workspace of kv8_reorder for up to n_in rows."""
+    n = C.c_size_t(0)
+    _check("kv8_reorder_workspace_size", lib().kv8_reorder_workspace_size(n_in, C.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def kv8_reorder(refs, page: int, table, length, parent, table_out, keep: bool = False,
+                length_out=None, src=None, dst=None, missing=None, ws=None, stream=None):
+    """Row b of ``table_out`` becomes row parent[b] of ``table``, sharing its pages; the rows of
+    ``table`` end unless ``keep``.  Returns (length_out, src, dst, missing): the rows' lengths, the
+    pages to copy (kv8_copy_pages) and how many rows got none."""
+    if stream is not None:
+        return _on(stream, kv8_reorder, refs, page, table, length, parent, table_out, keep,
+                   length_out, src, dst, missing, ws)
+    n_in, n_out = length.shape[0], parent.shape[0]
+    _ints(refs, "refs", refs.shape[0])
+    _ints(length, "length", n_in)
+    _ints(parent, "parent", n_out)
+    ldt, ldo = _table(table, "table", n_in), _table(table_out, "table_out", n_out)
+    if table.shape[1] != table_out.shape[1]:
+        raise ValueError("table and table_out: rows of the same entries required")
+    made = lambda t, n: torch.empty(n, dtype=torch.int32,  # noqa: E731
+                                    device=refs.device) if t is None else t
+    length_out, src, dst = made(length_out, n_out), made(src, n_out), made(dst, n_out)
+    missing = made(missing, 1)
+    for t, what in ((length_out, "length_out"), (src, "src"), (dst, "dst")):
+        _ints(t, what, n_out)
+    _ints(missing, "missing", 1)
+    if ws is None:
+        ws = kv8_reorder_workspace(n_in, refs.device)
+    _on_device((refs, table, length, parent, table_out, length_out, src, dst, missing), "pages")
+    st = lib().kv8_reorder(n_in, n_out, page, refs.shape[0], refs.data_ptr(), table.data_ptr(), ldt,
+                           length.data_ptr(), parent.data_ptr(), int(keep), table_out.data_ptr(),
+                           ldo, table.shape[1], length_out.data_ptr(), src.data_ptr(),
+                           dst.data_ptr(), missing.data_ptr(), ws.data_ptr(), _ws_bytes(ws, refs),
+                           _stream_of(refs))
+    if st:
+        raise DfsError("kv8_reorder", st)
+    return length_out, src, dst, missing
+
+
+def kv8_copy_pages(kvs, src, dst, length=None, stream=None) -> None:
+    """Copy page src[i] to page dst[i] in each of the caches ``kvs`` (pairs of -1 are passed over);
+    with ``length``, the first length[i] % page tokens of it."""
+    if stream is not None:
+        return _on(stream, kv8_copy_pages, kvs, src, dst, length)
+    n = src.shape[0]
+    _ints(src, "src", n)
+    _ints(dst, "dst", n)
+    given = [src, dst] + [kv.k for kv in kvs]
+    if length is not None:
+        _ints(length, "length", n)
+        given.append(length)
+    _on_device(given, "cache")
+    st = lib().kv8_copy_pages(len(kvs), (KV8 * len(kvs))(*[kv.desc() for kv in kvs]), n,
+                              src.data_ptr(), dst.data_ptr(), _ptr(length), _stream_of(src))
+    if st:
+        raise DfsError("kv8_copy_pages", st)
+
+
+def beam_workspace(n_req: int, width: int, vocab: int, device) -> torch.Tensor:
+    """Workspace of beam_select for any call of up to n_req requests, width beams and vocab tokens,
+    its first 64 KiB zeroed (as they must be before its first use)."""
+    n = C.c_size_t(0)
+    _check("beam_select_workspace_size",
+           lib().beam_select_workspace_size(n_req, width, vocab, C.byref(n)))
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
+
+
+def beam_select(logits, score, width: int, eos: int = -1, done=None, norm=None, parent=None,
+                token=None, score_out=None, done_out=None, ws=None, stream=None):
+    """The ``width`` best continuations of each request, whose beams are ``width`` rows of
+    ``logits`` (n_req * width, vocab) and ``score``.  Returns (parent, token, score, done): rows of
+    the batch, tokens, fp32 sums of log probabilities, int32."""
+    if stream is not None:
+        return _on(stream, beam_select, logits, score, width, eos, done, norm, parent, token,
+                   score_out, done_out, ws)
+    if logits.dim() != 2 or width < 1 or logits.shape[0] % width:
+        raise ValueError("logits: (requests * width, vocab) required")
+    rows, vocab = logits.shape
+    ldl = _matrix(logits, "logits", None, vocab)
+    made = lambda t, dt: torch.empty(rows, dtype=dt, device=logits.device  # noqa: E731
+                                     ) if t is None else t
+    parent, token = made(parent, torch.int32), made(token, torch.int32)
+    score_out, done_out = made(score_out, torch.float32), made(done_out, torch.int32)
+    given = [logits, score, parent, token, score_out, done_out]
+    for t, what in ((parent, "parent"), (token, "token"), (done, "done"), (done_out, "done_out")):
+        if t is not None:
+            _ints(t, what, rows)
+    for t, what in ((score, "score"), (norm, "norm"), (score_out, "score_out")):
+        if t is not None and (t.shape != (rows,) or t.dtype != torch.float32
+                              or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous float32 of {rows} values required")
+    given += [t for t in (done, norm) if t is not None]
+    dt = _dt(logits)
+    _on_device(given, "beams")
+    if ws is None:
+        ws = beam_workspace(rows // width, width, vocab, logits.device)
+    st = lib().beam_select(rows // width, width, vocab, logits.data_ptr(), dt,
+                           max(ldl, vocab) if rows <= 1 else ldl, score.data_ptr(), _ptr(done),
+                           _ptr(norm), eos, parent.data_ptr(), token.data_ptr(),
+                           score_out.data_ptr(), _ptr(done_out), ws.data_ptr(),
+                           _ws_bytes(ws, logits), _stream_of(logits))
+    if st:
+        raise DfsError("beam_select", st)
+    return parent, token, score_out, done_out
 
 
 # ----------------------------------------------------------------- producer steps

@@ -8,6 +8,7 @@
 // before anything is enqueued.
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "dfs_internal.hpp"
@@ -313,6 +314,32 @@ dfs_status check_kv_batch(const dfs_kv8* kv, const KvBatch& b) {
   if ((uintptr_t)b.tok_start % 4 != 0 || (uintptr_t)b.have % 4 != 0 || (uintptr_t)b.table % 4 != 0)
     return DFS_E_ALIGN;
   return DFS_OK;
+}
+
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((uintptr_t)p % 4 != 0) return false;
+  return true;
+}
+
+// Whether arrays of n and m elements of four bytes share any.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + 4 * m && (uintptr_t)b < (uintptr_t)a + 4 * n;
+}
+
+// The pool, and the rows of a page table over it.
+dfs_status check_pool(int32_t page, int32_t n_pages, const int32_t* refs) {
+  if (page != 16 && page != 32 && page != 64 && page != 128) return DFS_E_UNSUPPORTED;
+  if (n_pages <= 0 || !refs) return DFS_E_INVALID;
+  if (n_pages > 1 << 28) return DFS_E_RANGE;
+  return aligned4({refs}) ? DFS_OK : DFS_E_ALIGN;
+}
+dfs_status check_rows(int32_t rows, const int32_t* table, int64_t ldt, int32_t table_pages,
+                      int32_t page) {
+  if (rows < 0 || table_pages <= 0 || ldt < table_pages) return DFS_E_INVALID;
+  if (rows > kMaxKvRequests || (int64_t)table_pages * page >= (int64_t)1 << 31) return DFS_E_RANGE;
+  if (rows > 0 && !table) return DFS_E_INVALID;
+  return aligned4({table}) ? DFS_OK : DFS_E_ALIGN;
 }
 
 }  // namespace
@@ -883,6 +910,27 @@ dfs_status kv8_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_
   return DFS_OK;
 }
 
+namespace {
+dfs_status check_attention(const KvAttnLaunch& a) {
+  DFS_TRY(check_kv_batch(&a.kv, a.b));
+  if (a.q_heads <= 0 || a.q_heads % a.kv.heads != 0) return DFS_E_INVALID;
+  if (a.q_heads > kMaxKvHeads) return DFS_E_RANGE;
+  if (!(a.sm_scale > 0.0f) || !(a.sm_scale < 3.0e38f)) return DFS_E_INVALID;
+  if (a.sinks < 0) return DFS_E_INVALID;
+  if (!is_act_dtype(a.odt)) return DFS_E_UNSUPPORTED;
+  const int64_t row = (int64_t)a.q_heads * a.kv.head_dim;
+  if (a.ldq < row || a.ldo < row) return DFS_E_INVALID;
+  if (a.ldq % 8 != 0) return DFS_E_ALIGN;
+  if (a.b.n_req == 0 || a.b.n_tok == 0) return DFS_OK;
+  if (!a.Q || !a.O) return DFS_E_INVALID;
+  return aligned16(a.Q) && elem_aligned(a.O, a.odt) ? DFS_OK : DFS_E_ALIGN;
+}
+dfs_status check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return DFS_E_WORKSPACE;
+  return aligned16(ws) ? DFS_OK : DFS_E_ALIGN;
+}
+}  // namespace
+
 dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const int32_t* tok_start,
                          const int32_t* length, const int32_t* table, int64_t ldt,
                          int32_t table_pages, const void* Q, int64_t ldq, int32_t q_heads,
@@ -890,26 +938,176 @@ dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const 
                          int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
   DFS_TRY(check_kv8(kv));
   const KvBatch b = {n_req, n_tok, tok_start, length, table, ldt, table_pages};
-  DFS_TRY(check_kv_batch(kv, b));
-  if (q_heads <= 0 || q_heads % kv->heads != 0) return DFS_E_INVALID;
-  if (q_heads > kMaxKvHeads) return DFS_E_RANGE;
-  if (!(sm_scale > 0.0f) || !(sm_scale < 3.0e38f)) return DFS_E_INVALID;
-  if (sinks < 0) return DFS_E_INVALID;
-  if (!is_act_dtype(odt)) return DFS_E_UNSUPPORTED;
-  const int64_t row = (int64_t)q_heads * kv->head_dim;
-  if (ldq < row || ldo < row) return DFS_E_INVALID;
-  if (ldq % 8 != 0) return DFS_E_ALIGN;
+  const KvAttnLaunch a = {*kv, b, (const _Float16*)Q, ldq, q_heads, sm_scale, window, sinks, O,
+                          odt, ldo};
+  DFS_TRY(check_attention(a));
   if (n_req == 0 || n_tok == 0) return DFS_OK;
-  if (!Q || !O) return DFS_E_INVALID;
-  if (!aligned16(Q) || !elem_aligned(O, odt)) return DFS_E_ALIGN;
-  const size_t need = kv8_attention_ws_need(*kv, n_req, n_tok, q_heads);
+  DFS_TRY(check_ws(ws, ws_bytes, kv8_attention_ws_need(*kv, n_req, n_tok, q_heads)));
+  DFS_HIP(launch_kv8_attention(a, ws, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+dfs_status kv8_prefix_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                               int32_t q_heads, size_t* bytes) {
+  DFS_TRY(kv8_attention_workspace_size(kv, n_req, n_tok, q_heads, bytes));
+  *bytes = kv8_prefix_ws_bytes(*kv, n_req, n_tok, q_heads);
+  return DFS_OK;
+}
+
+dfs_status kv8_prefix_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                const int32_t* tok_start, const int32_t* length,
+                                const int32_t* table, int64_t ldt, int32_t table_pages,
+                                int32_t n_groups, const int32_t* group_start,
+                                const int32_t* shared, const void* Q, int64_t ldq, int32_t q_heads,
+                                float sm_scale, int32_t window, int32_t sinks, void* O, int32_t odt,
+                                int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  DFS_TRY(check_kv8(kv));
+  const KvBatch b = {n_req, n_tok, tok_start, length, table, ldt, table_pages};
+  const KvAttnLaunch a = {*kv, b, (const _Float16*)Q, ldq, q_heads, sm_scale, window, sinks, O,
+                          odt, ldo};
+  DFS_TRY(check_attention(a));
+  if (n_groups < 0 || n_groups > n_req) return DFS_E_INVALID;
+  if (n_req == 0 || n_tok == 0) return DFS_OK;
+  if (n_groups > 0 && (!group_start || !shared)) return DFS_E_INVALID;
+  if (!aligned4({group_start, shared})) return DFS_E_ALIGN;
+  DFS_TRY(check_ws(ws, ws_bytes, kv8_prefix_ws_need(*kv, n_req, n_tok, q_heads, n_groups)));
+  DFS_HIP(launch_kv8_prefix_attention(a, n_groups, group_start, shared, ws, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+// ------------------------------------------------------------------ pages of the cache
+
+dfs_status kv8_tables(int32_t n_req, int32_t page, int32_t n_pages, int32_t* refs,
+                      const int32_t* cached, const int32_t* n_new, int32_t n_tok, int32_t* table,
+                      int64_t ldt, int32_t table_pages, int32_t* tok_start, int32_t* length,
+                      int32_t* tok_req, int32_t* tok_pos, int64_t* slot, int32_t* missing,
+                      void* stream) {
+  DFS_TRY(check_pool(page, n_pages, refs));
+  DFS_TRY(check_rows(n_req, table, ldt, table_pages, page));
+  if (n_tok < 0) return DFS_E_INVALID;
+  if (!tok_start || !missing || (n_req > 0 && (!cached || !n_new || !length))) return DFS_E_INVALID;
+  if (!aligned4({cached, n_new, tok_start, length, tok_req, tok_pos, missing}) ||
+      (uintptr_t)slot % 8 != 0)
+    return DFS_E_ALIGN;
+  if (overlap(length, n_req, cached, n_req) || overlap(length, n_req, n_new, n_req))
+    return DFS_E_INVALID;
+  const KvTables a = {n_req, n_tok,       page,      n_pages, refs,    cached,  n_new, table,
+                      ldt,   table_pages, tok_start, length,  tok_req, tok_pos, slot,  missing};
+  DFS_HIP(launch_kv8_tables(a, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+dfs_status kv8_release(int32_t n_req, int32_t n_pages, int32_t* refs, int32_t* table, int64_t ldt,
+                       int32_t table_pages, const int32_t* first, const int32_t* last,
+                       void* stream) {
+  DFS_TRY(check_pool(16, n_pages, refs));
+  DFS_TRY(check_rows(n_req, table, ldt, table_pages, 1));
+  if (!aligned4({first, last})) return DFS_E_ALIGN;
+  if (n_req == 0) return DFS_OK;
+  const KvRelease a = {n_req, n_pages, refs, table, ldt, table_pages, first, last};
+  DFS_HIP(launch_kv8_release(a, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+dfs_status kv8_reorder_workspace_size(int32_t n_in, size_t* bytes) {
+  if (!bytes || n_in < 0) return DFS_E_INVALID;
+  if (n_in > kMaxKvRequests) return DFS_E_RANGE;
+  *bytes = round256((size_t)n_in * 8);
+  return DFS_OK;
+}
+
+dfs_status kv8_reorder(int32_t n_in, int32_t n_out, int32_t page, int32_t n_pages, int32_t* refs,
+                       const int32_t* table, int64_t ldt, const int32_t* length,
+                       const int32_t* parent, int32_t keep, int32_t* table_out, int64_t ldo,
+                       int32_t table_pages, int32_t* length_out, int32_t* src, int32_t* dst,
+                       int32_t* missing, void* ws, size_t ws_bytes, void* stream) {
+  DFS_TRY(check_pool(page, n_pages, refs));
+  DFS_TRY(check_rows(n_in, table, ldt, table_pages, page));
+  DFS_TRY(check_rows(n_out, table_out, ldo, table_pages, page));
+  if (!missing || (n_in > 0 && !length) ||
+      (n_out > 0 && (!parent || !length_out || !src || !dst)))
+    return DFS_E_INVALID;
+  if (!aligned4({length, parent, length_out, src, dst, missing})) return DFS_E_ALIGN;
+  if (n_in > 0 && n_out > 0 &&
+      (overlap(table, (n_in - 1) * ldt + table_pages, table_out, (n_out - 1) * ldo + table_pages) ||
+       overlap(length, n_in, length_out, n_out) || overlap(parent, n_out, length_out, n_out)))
+    return DFS_E_INVALID;
+  const size_t need = (size_t)n_in * 8;
   if (need > 0) {
     if (!ws || ws_bytes < need) return DFS_E_WORKSPACE;
     if (!aligned16(ws)) return DFS_E_ALIGN;
   }
-  const KvAttnLaunch a = {*kv, b, (const _Float16*)Q, ldq, q_heads, sm_scale, window, sinks, O,
-                          odt, ldo};
-  DFS_HIP(launch_kv8_attention(a, ws, (hipStream_t)stream));
+  const KvReorder a = {n_in, n_out, page,        n_pages, refs,       table, ldt, length, parent,
+                       table_out, ldo, table_pages, keep,    length_out, src,   dst, missing};
+  DFS_HIP(launch_kv8_reorder(a, (int32_t*)ws, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+dfs_status kv8_copy_pages(int32_t n_kv, const dfs_kv8* kv, int32_t n, const int32_t* src,
+                          const int32_t* dst, const int32_t* length, void* stream) {
+  if (n_kv < 0 || n < 0 || (n_kv > 0 && !kv)) return DFS_E_INVALID;
+  if (n_kv > kMaxLayers) return DFS_E_RANGE;
+  KvCopy a = {};
+  for (int32_t i = 0; i < n_kv; ++i) {
+    DFS_TRY(check_kv8(kv + i));
+    if (kv[i].heads != kv[0].heads || kv[i].head_dim != kv[0].head_dim ||
+        kv[i].page != kv[0].page || kv[i].n_pages != kv[0].n_pages)
+      return DFS_E_INVALID;
+    a.kv[i] = kv[i];
+  }
+  if (n_kv == 0 || n == 0) return DFS_OK;
+  if (!src || !dst) return DFS_E_INVALID;
+  if (!aligned4({src, dst, length})) return DFS_E_ALIGN;
+  a.n_kv = n_kv;
+  a.n = n;
+  a.src = src;
+  a.dst = dst;
+  a.length = length;
+  DFS_HIP(launch_kv8_copy(a, (hipStream_t)stream));
+  return DFS_OK;
+}
+
+// ------------------------------------------------------------------ beams
+
+namespace {
+dfs_status check_beams(int32_t n_req, int32_t width, int32_t vocab) {
+  if (n_req < 0 || width <= 0 || vocab <= 0) return DFS_E_INVALID;
+  if (width > kMaxBeams || n_req > kMaxBeamRequests || (int64_t)n_req * width > 65535 ||
+      vocab > 1 << 30)
+    return DFS_E_RANGE;
+  return DFS_OK;
+}
+}  // namespace
+
+dfs_status beam_select_workspace_size(int32_t n_req, int32_t width, int32_t vocab, size_t* bytes) {
+  if (!bytes) return DFS_E_INVALID;
+  DFS_TRY(check_beams(n_req, width, vocab));
+  *bytes = beam_ws_bytes(n_req, width, vocab);
+  return DFS_OK;
+}
+
+dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* logits,
+                       int32_t dtype, int64_t ldl, const float* score, const int32_t* done,
+                       const float* norm, int32_t eos, int32_t* parent, int32_t* token,
+                       float* score_out, int32_t* done_out, void* ws, size_t ws_bytes,
+                       void* stream) {
+  DFS_TRY(check_beams(n_req, width, vocab));
+  if (!is_act_dtype(dtype)) return DFS_E_UNSUPPORTED;
+  if (ldl < vocab) return DFS_E_INVALID;
+  if (done && (eos < 0 || eos >= vocab)) return DFS_E_INVALID;
+  if (n_req == 0) return DFS_OK;
+  if (!logits || !score || !parent || !token || !score_out) return DFS_E_INVALID;
+  if (!elem_aligned(logits, dtype) ||
+      !aligned4({score, done, norm, parent, token, score_out, done_out}))
+    return DFS_E_ALIGN;
+  const int64_t rows = (int64_t)n_req * width;
+  for (const void* out : {(const void*)parent, (const void*)token, (const void*)score_out, (const void*)done_out})
+    for (const void* in : {(const void*)score, (const void*)done, (const void*)norm})
+      if (overlap(out, rows, in, rows)) return DFS_E_INVALID;
+  DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab, dtype)));
+  const BeamLaunch a = {n_req, width, vocab,  logits, dtype,     ldl,     score,
+                        done,  norm,  eos,    parent, token,     score_out, done_out};
+  DFS_HIP(launch_beam_select(a, ws, (hipStream_t)stream));
   return DFS_OK;
 }
 

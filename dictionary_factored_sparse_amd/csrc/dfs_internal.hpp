@@ -49,6 +49,28 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Sum of v over the threads before this one, and over all of them; tmp: one T a wave.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* tmp, T* total, int threads) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const T y = __shfl_up(x, o, kWave);
+    if (lane >= o) x += y;
+  }
+  if (lane == kWave - 1) tmp[wave] = x;
+  __syncthreads();
+  T base = 0, sum = 0;
+  for (int w = 0; w < threads / kWave; ++w) {
+    if (w < wave) base += tmp[w];
+    sum += tmp[w];
+  }
+  __syncthreads();
+  *total = sum;
+  return base + x - v;  // exclusive
+}
+
 // ------------------------------------------------------------------ formats
 // E4M3 (bias 7, no infinities) code -> fp32, from the format definition.
 __device__ __forceinline__ float e4m3_to_f32(uint32_t c) {
@@ -282,6 +304,74 @@ struct KvAttnLaunch {
 size_t kv8_attention_ws_need(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
 size_t kv8_attention_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
 hipError_t launch_kv8_attention(const KvAttnLaunch& a, void* ws, hipStream_t s);
+
+// The same with requests that share their first tokens.
+size_t kv8_prefix_ws_need(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads,
+                          int32_t n_groups);
+size_t kv8_prefix_ws_bytes(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads);
+hipError_t launch_kv8_prefix_attention(const KvAttnLaunch& a, int32_t n_groups,
+                                       const int32_t* group_start, const int32_t* shared, void* ws,
+                                       hipStream_t s);
+
+// Page tables of the cache, and its pages' use
+struct KvTables {
+  int32_t n_req, n_tok, page, n_pages;
+  int32_t* refs;
+  const int32_t *cached, *n_new;
+  int32_t* table;
+  int64_t ldt;
+  int32_t table_pages;
+  int32_t *tok_start, *length, *tok_req, *tok_pos;  // the last two may be null
+  int64_t* slot;                                    // may be null
+  int32_t* missing;
+};
+hipError_t launch_kv8_tables(const KvTables& a, hipStream_t s);
+struct KvRelease {
+  int32_t n_req, n_pages;
+  int32_t *refs, *table;
+  int64_t ldt;
+  int32_t table_pages;
+  const int32_t *first, *last;  // may be null
+};
+hipError_t launch_kv8_release(const KvRelease& a, hipStream_t s);
+struct KvReorder {
+  int32_t n_in, n_out, page, n_pages;
+  int32_t* refs;
+  const int32_t* table;
+  int64_t ldt;
+  const int32_t *length, *parent;
+  int32_t* out;
+  int64_t ldo;
+  int32_t table_pages, keep;
+  int32_t *length_out, *src, *dst, *missing;
+};
+hipError_t launch_kv8_reorder(const KvReorder& a, int32_t* ws, hipStream_t s);  // ws: 2 n_in
+struct KvCopy {
+  dfs_kv8 kv[kMaxLayers];  // of one shape
+  int32_t n_kv, n;
+  const int32_t *src, *dst, *length;  // length may be null
+};
+hipError_t launch_kv8_copy(const KvCopy& a, hipStream_t s);
+
+// Selection of beam search
+constexpr int kMaxBeams = 32;
+constexpr int kMaxBeamRequests = 16384;  // counters in the first 64 KiB of the workspace
+struct BeamLaunch {
+  int32_t n_req, width, vocab;
+  const void* logits;
+  int32_t dtype;
+  int64_t ldl;
+  const float* score;
+  const int32_t* done;  // may be null
+  const float* norm;    // may be null
+  int32_t eos;
+  int32_t *parent, *token;
+  float* score_out;
+  int32_t* done_out;  // may be null
+};
+size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab, int32_t dtype);
+size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab);
+hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s);
 
 // NVFP4 packing
 size_t nvfp4_ws_bytes(int64_t n);

@@ -509,6 +509,145 @@ dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const 
                          float sm_scale, int32_t window, int32_t sinks, void* O, int32_t odt,
                          int64_t ldo, void* ws, size_t ws_bytes, void* stream);
 
+/* Attention of new tokens over the cache where requests share their first
+ * tokens: the samples or beams of one prompt, questions to one document, chats
+ * behind one system prompt.  The keys and values that the requests of a group
+ * share are read once for all of them.
+ * Group i is the requests group_start[i] .. group_start[i+1]-1
+ * (group_start[n_groups+1] int32, device, non-decreasing; values are clamped to
+ * 0 .. n_req); requests outside every group stand alone.  The first shared[i]
+ * tokens (shared[n_groups] int32, device; negative counts as 0) of a group's
+ * requests are the same: up to there the table rows of its requests name the
+ * same pages.  Where they do not, the first row's page may be read in place of
+ * another's.  A request shorter than shared[i] stands alone.  Everything else, the
+ * result too, is as for kv8_attention: the causal mask, window and sinks go by
+ * each request's own positions.
+ * 0 <= n_groups <= n_req; 0 is kv8_attention.  The workspace is of
+ * kv8_prefix_attention_workspace_size; its first 64 KiB must be zero before its
+ * first use, every call leaves them zero again, and calls sharing a workspace
+ * must not run concurrently.  Groups, lengths and how much is shared are read on
+ * the device, so a captured call follows later ones; results do not change from
+ * run to run. */
+dfs_status kv8_prefix_attention_workspace_size(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                               int32_t q_heads, size_t* bytes);
+dfs_status kv8_prefix_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
+                                const int32_t* tok_start, const int32_t* length,
+                                const int32_t* table, int64_t ldt, int32_t table_pages,
+                                int32_t n_groups, const int32_t* group_start,
+                                const int32_t* shared, const void* Q, int64_t ldq, int32_t q_heads,
+                                float sm_scale, int32_t window, int32_t sinks, void* O, int32_t odt,
+                                int64_t ldo, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Pages of the cache: page tables, shared prompts, beams                  */
+/* ---------------------------------------------------------------------- */
+/* The use of a pool of pages is one count per page, refs[n_pages] (int32,
+ * device): how many entries of page tables name it; 0 is free.  A pool that
+ * nobody uses is all zero.  The calls below keep the counts; the caches of all
+ * layers of a model share one table and one pool.  page is 16, 32, 64 or 128
+ * (DFS_E_UNSUPPORTED), 0 < n_pages <= 2^28; rows of tables as for dfs_kv8 (an entry
+ * outside 0 .. n_pages-1 is no page), at most 65535 (DFS_E_RANGE).  Pages are
+ * handed out lowest first, in the order of rows and entries, and nothing
+ * depends on the order in which the device works.  Calls over one pool must not
+ * run concurrently. */
+
+/* Page tables, starts, lengths and slot maps of a batch from its requests'
+ * lengths.  Request r has cached[r] tokens in the cache and n_new[r] to come
+ * (int32, device; negative counts as 0).  With n the new tokens that still fit
+ * the batch's n_tok rows, in order of requests:
+ *   tok_start[n_req+1]: the requests' first rows, and the end of the last's;
+ *   length[r] = cached[r] + n  (must not overlap cached);
+ *   table: entries cached/page (rounded up) .. length/page (rounded up) - 1, as
+ *     far as the row's table_pages go, that name no page get the lowest free
+ *     page, whose count becomes 1; entries that name one keep it, so that the
+ *     same call again changes nothing;
+ *   missing[1]: how many entries got none because no page was free (they are
+ *     -1, and kv8_append and kv8_attention pass over them); call again when
+ *     pages have been given back;
+ *   for row t of request r: tok_req[t] = r, tok_pos[t] = its position, slot[t] =
+ *     page * (its page) + (its place in it), int64, or -1 without a page; rows
+ *     from tok_start[n_req] on get -1 in each.  tok_req, tok_pos and slot (n_tok
+ *     each) may be NULL. */
+dfs_status kv8_tables(int32_t n_req, int32_t page, int32_t n_pages, int32_t* refs,
+                      const int32_t* cached, const int32_t* n_new, int32_t n_tok, int32_t* table,
+                      int64_t ldt, int32_t table_pages, int32_t* tok_start, int32_t* length,
+                      int32_t* tok_req, int32_t* tok_pos, int64_t* slot, int32_t* missing,
+                      void* stream);
+
+/* Give back the pages of entries first[r] .. last[r]-1 of each row: their
+ * counts go down by one and the entries become -1.  first NULL stands for 0,
+ * last NULL for table_pages (int32, device, in entries; clamped to the row).
+ * For requests that have ended, tokens taken back, pages that a window has
+ * left. */
+dfs_status kv8_release(int32_t n_req, int32_t n_pages, int32_t* refs, int32_t* table, int64_t ldt,
+                       int32_t table_pages, const int32_t* first, const int32_t* last,
+                       void* stream);
+
+/* Workspace bytes of kv8_reorder for up to n_in rows.  Need not be zeroed. */
+dfs_status kv8_reorder_workspace_size(int32_t n_in, size_t* bytes);
+
+/* Rows forked, reordered or dropped: row b of table_out becomes row parent[b] of
+ * table (n_in rows of length[n_in] tokens; a parent outside 0 .. n_in-1 gives an
+ * empty row), length_out[b] its length.  Pages are shared: counts go up by the
+ * entries written, and, unless keep is non-zero, down by those of the rows of
+ * table, which end with the call (table itself is not written).  Entries past a
+ * row's length are not passed on.
+ * A page that is partly filled takes the next tokens, so each row needs its own:
+ * the first row of a parent keeps it where nobody else's entries name it, every
+ * other row gets the lowest free page, and src[b], dst[b] name the pages to copy
+ * from and to (-1, -1 for rows that need no copy).  Copy them before anything is
+ * written (kv8_copy_pages with length_out, for each layer's cache).  missing[1]
+ * counts rows that got no page because none was free; their entry is -1.
+ * table_out must not overlap table; ws as for kv8_reorder_workspace_size,
+ * 16-byte aligned. */
+dfs_status kv8_reorder(int32_t n_in, int32_t n_out, int32_t page, int32_t n_pages, int32_t* refs,
+                       const int32_t* table, int64_t ldt, const int32_t* length,
+                       const int32_t* parent, int32_t keep, int32_t* table_out, int64_t ldo,
+                       int32_t table_pages, int32_t* length_out, int32_t* src, int32_t* dst,
+                       int32_t* missing, void* ws, size_t ws_bytes, void* stream);
+
+/* Copy pages inside each of up to 16 caches of one shape (the layers of a
+ * model; kv is a host array): page src[i] to page dst[i] for i < n, keys,
+ * values and scales; pairs that name no page, or one page twice, are passed
+ * over.  length (may be NULL): only the first length[i] % page tokens, rounded up
+ * to a multiple of 16, are copied, all where that is 0; the others keep what
+ * they hold.  No page may be dst twice, nor src of one pair and dst of another. */
+dfs_status kv8_copy_pages(int32_t n_kv, const dfs_kv8* kv, int32_t n, const int32_t* src,
+                          const int32_t* dst, const int32_t* length, void* stream);
+
+/* Workspace bytes of beam_select for any call of up to n_req requests, width
+ * beams and vocab tokens. */
+dfs_status beam_select_workspace_size(int32_t n_req, int32_t width, int32_t vocab, size_t* bytes);
+
+/* The next beams of beam search.  Request r has rows r*width .. r*width+width-1
+ * of logits (vocab columns, dtype F16 or F32, any leading dimension >= vocab,
+ * aligned to the element) and of score (fp32: the sum of the beam's log
+ * probabilities so far).  Token v after row w has
+ *   total = score[w] + logits[w, v] - log sum_u exp(logits[w, u]).
+ * The width continuations of the request with the largest total * norm[w] (norm:
+ * fp32 > 0 per row, a length penalty for instance; NULL stands for 1), largest
+ * first, are written to parent (their row, counted over the batch), token and
+ * score_out (their total).  Equals go to the lower row, in a row to the larger
+ * logit, then to the lower token.
+ *   done (int32 per row, may be NULL): a row with done != 0 has one continuation,
+ *     the token eos (0 .. vocab-1 then) at its own score; done_out (may be NULL)
+ *     is 1 where the parent was done or the token is eos.
+ *   Logits of -inf, and NaN, are no continuations; +inf counts as the largest
+ *   finite number.  A row whose score is not finite, or whose norm is not
+ *   positive and finite, has none (the first step gives the beams 1 .. width-1 a
+ *   score of -inf).  Where a request has fewer continuations than width, parent
+ *   is its first row, token -1, score -inf and done_out 0.
+ * Exponentials are fp32, their sums and the totals 64 bits.
+ * 1 <= width <= 32, n_req <= 16384, n_req * width <= 65535 (DFS_E_RANGE).
+ * Outputs must not overlap inputs.  The workspace's first 64 KiB must be zero
+ * before its first use; every call leaves them zero again.  Calls sharing a
+ * workspace must not run concurrently. */
+dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* logits,
+                       int32_t dtype, int64_t ldl, const float* score, const int32_t* done,
+                       const float* norm, int32_t eos, int32_t* parent, int32_t* token,
+                       float* score_out, int32_t* done_out, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* ---------------------------------------------------------------------- */
 /* Producer steps (offline, fp32)                                          */
 /* ---------------------------------------------------------------------- */
