@@ -44,13 +44,26 @@ struct Plan {
   Req facts[kInlinePlan];
 };
 
-// Complete rows go to the output.
-template <typename A>
-struct Out {
-  const A& t;
-  __device__ __forceinline__ int64_t at(int row) const { return t.out_at(row); }
-  __device__ __forceinline__ void put(int64_t at, int d, const f4& v, f2 ml) const { t.store(at + d, v, ml.y); }
-  __device__ __forceinline__ void put_nan(int64_t at, int d) const { t.store_nan(at + d); }
+// The items of a batch; complete rows go to the output.
+template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
+struct Batch : Attn<KIND, D, NQ, SPLIT, F32, BIG> {
+  using A = Attn<KIND, D, NQ, SPLIT, F32, BIG>;
+  const AttnWs& ws;
+  const Plan& plan;
+  const int inline_plan;
+  __device__ __forceinline__ Batch(const KvAttnLaunch& a, const AttnWs& w, const Plan& p, int in)
+      : A(a), ws(w), plan(p), inline_plan(in) {}
+  __device__ __forceinline__ int64_t first(int e) const { return inline_plan ? plan.first[e] : *gptr(ws.first + e); }
+  __device__ __forceinline__ int longest() const { return uni(inline_plan ? plan.longest : *gptr(ws.n_entries + 1)); }
+  __device__ __forceinline__ int ready(int e, int kh) {
+    const int req = uni(inline_plan ? plan.req[e] : *gptr(ws.req + e));
+    const int qblk = uni(inline_plan ? plan.qblk[e] : *gptr(ws.qblk + e));
+    A::begin(inline_plan ? plan.facts[req] : get_req(A::a.b, A::a.kv.page, req), req, qblk, kh);
+    return qblk;
+  }
+  __device__ __forceinline__ int64_t at(int row) const { return A::out_at(row); }
+  __device__ __forceinline__ void put(int64_t at, int d, const f4& v, float, float l) const { A::store(at + d, v, l); }
+  __device__ __forceinline__ void put_nan(int64_t at, int d) const { A::store_nan(at + d); }
 };
 
 // Entries (request, block of qb query rows) in order and the first tile of
@@ -122,30 +135,15 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvAttnLaunch a, Attn
 template <int KIND, int D, int NQ, bool SPLIT, bool F32, bool BIG>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 void attn_kernel(KvAttnLaunch a, AttnWs ws, int least, int slices, int inline_plan) {
-  using A = Attn<KIND, D, NQ, SPLIT, F32, BIG>;
+  using A = Batch<KIND, D, NQ, SPLIT, F32, BIG>;
   __shared__ typename A::Work sh;
   __shared__ Plan plan;
-  A t(a);
+  A t(a, ws, plan, inline_plan);
   const int n_entries =
       inline_plan ? make_plan<int>(a, A::kQb, A::kExtra, ws.max_entries, plan.first, plan.req, plan.qblk,
                                    plan.facts, &plan.longest, plan.tmp, kThreads)
                   : *gptr(ws.n_entries);
-  const int g = a.q_heads / a.kv.heads;
-  run_line(
-      t, sh, ws.line, n_entries, [&](int e) { return inline_plan ? plan.first[e] : *gptr(ws.first + e); },
-      [&] { return uni(inline_plan ? plan.longest : *gptr(ws.n_entries + 1)); },
-      [&](int e, int kh) {
-        const int req = uni(inline_plan ? plan.req[e] : *gptr(ws.req + e));
-        const int qblk = uni(inline_plan ? plan.qblk[e] : *gptr(ws.qblk + e));
-        const Req f = inline_plan ? plan.facts[req] : get_req(a.b, a.kv.page, req);
-        const int n = uni(f.n), pos0 = uni(f.len) - n, i0 = qblk * A::kQb;
-        const Req q = {uni(f.t0), n, uni(f.len), uni(f.keys)};
-        const int i1 = min(i0 + A::kQb, n * g);
-        const Span s = get_span(q, pos0 + i0 / g, pos0 + (i1 - 1) / g, a.window, a.sinks);
-        t.template begin<false>(q, s, req, qblk, kh, [&](int tok) { return pos0 + tok; });
-        return qblk;
-      },
-      Out<A>{t}, least, (int)blockIdx.x, slices);
+  run_line(t, sh, ws.line, n_entries, least, (int)blockIdx.x, slices);
 }
 
 // How a call is cut: query rows per item, workgroups, entries at most.

@@ -102,7 +102,11 @@ __device__ __forceinline__ Span get_span(const Req& q, int p0, int p1, int windo
   s.ta = lo / kTile;
   s.ns = sk > from ? min((sk - 1) / kTile + 1, s.ta) - s.t0 : 0;
   s.n = s.ns + (hi >= lo ? hi / kTile - s.ta + 1 : 0);
-  if (s.n <= 0) s = {s.t0, 0, s.t0, 1};  // rows that see nothing still get their zeros
+  if (s.n <= 0) {  // rows that see nothing still get their zeros
+    s.ns = 0;
+    s.ta = s.t0;
+    s.n = 1;
+  }
   return s;
 }
 
@@ -146,6 +150,12 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t c) {
 __device__ __forceinline__ void put2(f2* p, f2 v) {
   __hip_atomic_store((uint64_t*)p, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
+}
+// The same of two numbers that are not a pair: made as whole numbers, for else the
+// arrays that they come from are kept in memory.
+__device__ __forceinline__ void put2(f2* p, float x, float y) {
+  const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ f2 get2(const f2* p) {
   return __builtin_bit_cast(f2, __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED,
@@ -369,25 +379,30 @@ struct Attn {
     vs = *gptr(a.kv.vscale + ph);
   }
 
-  // The item of block qblk of `facts`' rows and kv head kh_, over the pages of row
-  // `row` of the table; pos_of(token of the request): its position, which
-  // ascends unless ANY.
+  // The item of block qblk of `facts`' rows and kv head kh_, over the keys from
+  // `from` on in the pages of row `req` of the table.
+  __device__ __forceinline__ void begin(const Req& facts, int req, int qblk, int kh_, int from = 0) {
+    begin_by<false>(facts, req, qblk, kh_, from, 0, 0, [&](int tok) { return rq.len - rq.n + tok; });
+  }
+  // The same where pos_of(token) is a token's position, p0 the lowest of them all
+  // and p1 the highest (ANY: they do not ascend).
   template <bool ANY, typename P>
-  __device__ __forceinline__ void begin(const Req& facts, const Span& span, int row, int qblk, int kh_,
-                                        P pos_of) {
+  __device__ __forceinline__ void begin_by(const Req& facts, int req, int qblk, int kh_, int from, int p0,
+                                           int p1, P pos_of) {
     const int g = a.q_heads / a.kv.heads;
     kh = kh_;
     rq = {uni(facts.t0), uni(facts.n), uni(facts.len), uni(facts.keys)};
-    tab = a.b.table + (int64_t)row * a.b.ldt;
+    tab = a.b.table + (int64_t)req * a.b.ldt;
     const int rows = rq.n * g;  // < 2^31: n_tok rows of q_heads * head_dim elements exist
     const int item0 = qblk * kQb, item1 = min(item0 + kQb, rows);
     row0 = item0 + (SPLIT ? 0 : wave * kRows);
     nrows = min(item1 - row0, kRows);
-    sp = span;
     if constexpr (!ANY) {
+      sp = get_span(rq, pos_of(item0 / g), pos_of((item1 - 1) / g), a.window, a.sinks, from);
       pmin = pos_of(min(row0, item1 - 1) / g);
       pmax = pos_of((min(row0 + kRows, item1) - 1) / g);
     } else {
+      sp = get_span(rq, p0, p1, a.window, a.sinks, from);
       pmin = INT32_MAX;
       pmax = INT32_MIN;
     }
@@ -726,16 +741,17 @@ struct Line {
   f2* group_ml;     // the same of a group of slices, at its first slice's slot
 };
 
-// Slice `slice` of a line of items.  first(e): the line's position where entry e
-// starts (a plan has made it), first(n_entries) its end; longest(): the most tiles
-// an item has; begin(e, kv head) readies t for an item and returns its block of
-// rows; sink takes the rows that are complete: at(row of the entry's requests),
-// put(at, dim, four sums, reference of the weights and their sum).
-template <typename A, typename F, typename L, typename B, typename S>
-__device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line& ln, int n_entries, F first,
-                                         L longest, B begin, S sink, int least, int slice, int slices) {
+// Slice `slice` of a line of items.  A is an Attn that knows its line as well:
+// first(e) is the line's position where entry e starts (a plan has made it),
+// first(n_entries) its end; longest() the most tiles an item has; ready(e, kv head)
+// readies t for an item and returns its block of rows; the rows that are complete
+// go to at(row of the entry's requests), by put(at, dim, four sums, reference of
+// the weights, their sum) and put_nan(at, dim).
+template <typename A>
+__device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line& ln, int n_entries, int least,
+                                         int slice, int slices) {
   if (n_entries == 0) return;
-  const int64_t total = first(n_entries);
+  const int64_t total = t.first(n_entries);
   const int64_t per = max((int64_t)least, (total + slices - 1) / slices);
   const int64_t xs = slice * per, xe = min(xs + per, total);
   if (xs >= total) return;
@@ -744,7 +760,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
   for (int n = n_entries; n > 1;) {
     const int stride = (n + kThreads - 1) / kThreads;
     const int at = (int)threadIdx.x * stride;
-    const int below = __syncthreads_count(at < n && first(e + at) <= xs);
+    const int below = __syncthreads_count(at < n && t.first(e + at) <= xs);
     e += (below - 1) * stride;
     n = min(stride, n_entries - e);
   }
@@ -752,13 +768,12 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
   // whole.  A part and its join cost as much as some tiles (four prompts of 500
   // tokens, 8 tiles at most: 46 us split, 38 us whole; windows of 512 tokens, 11
   // tiles: 70 us split, 82 us whole).
-  const bool keep =
-      !A::kSplit && longest() <= kWhole;
+  const bool keep = !A::kSplit && t.longest() <= kWhole;
   for (int64_t x = xs; x < xe;) {
-    while (first(e + 1) <= x) ++e;
-    const int64_t fe = first(e);
+    while (t.first(e + 1) <= x) ++e;
+    const int64_t fe = t.first(e);
     // an item is its tiles, and then the extra ones
-    const int n_line = uni((int)((first(e + 1) - fe) / t.a.kv.heads)), n_tiles = n_line - A::kExtra;
+    const int n_line = uni((int)((t.first(e + 1) - fe) / t.a.kv.heads)), n_tiles = n_line - A::kExtra;
     const int kh = uni((int)((x - fe) / n_line));
     const int64_t item0 = fe + (int64_t)kh * n_line, item1 = item0 + n_tiles;
     if (keep ? x > item0 : x >= item1) {  // another slice's, or only extra ones are left of it
@@ -767,13 +782,13 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
     }
     const int u0 = uni((int)(x - item0)), u1 = uni(keep ? n_tiles : (int)(min(item1, xe) - item0));
     x = u1 == n_tiles ? item0 + n_line : item0 + u1;
-    const int qblk = begin(e, kh);
+    const int qblk = t.ready(e, kh);
     const int v0 = A::kSplit ? u0 + t.wave : u0, step = A::kSplit ? kWaves : 1;
     const int v1 = A::kSplit || t.nrows > 0 ? u1 : u0;  // this wave's tiles: v0, v0 + step, ... below v1
     t.template tiles<false>(v0, v1, step);
     const bool nans = A::kNan && t.any_nan();
     if (A::kNan && nans) {
-      begin(e, kh);
+      t.ready(e, kh);
       t.template tiles<true>(v0, v1, step);
     }
     t.finish();
@@ -814,7 +829,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
           v += *(f4*)&sh.o[(w * A::kRows + row) * A::kD + d] * f;
         }
         if (whole) {
-          sink.put(sink.at(t.row0 + row), d, v, f2{mm, l});
+          t.put(t.at(t.row0 + row), d, v, mm, l);
         } else {
           put4(&ln.part_o[(slot * A::kQb + row) * A::kD + d], v);
           if (d == 0) put2(&ln.part_ml[slot * A::kQb + row], f2{mm, l});
@@ -825,14 +840,14 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
       for (int i = 0; i < A::kNq; ++i) {
         const int row = 16 * i + t.r16;
         if (row < t.nrows) {
-          const int64_t at = whole ? sink.at(t.row0 + row) : 0;
+          const int64_t at = whole ? t.at(t.row0 + row) : 0;
           const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
 #pragma unroll
           for (int d = 0; d < A::kDims; ++d) {
-            if (whole) sink.put(at, d * 16 + t.q4 * 4, t.o[i][d], f2{t.m[i], t.l[i]});
+            if (whole) t.put(at, d * 16 + t.q4 * 4, t.o[i][d], t.m[i], t.l[i]);
             else put4(&ln.part_o[pr * A::kD + d * 16 + t.q4 * 4], t.o[i][d]);
           }
-          if (!whole && t.q4 == 0) put2(&ln.part_ml[pr], f2{t.m[i], t.l[i]});
+          if (!whole && t.q4 == 0) put2(&ln.part_ml[pr], t.m[i], t.l[i]);
         }
       }
       if (A::kNan && nans)
@@ -840,7 +855,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
           const int row = 16 * i + t.r16;
           if (row >= t.nrows) return;
           if (whole) {
-            sink.put_nan(sink.at(t.row0 + row), d);
+            t.put_nan(t.at(t.row0 + row), d);
           } else {
             const int64_t pr = slot * A::kQb + t.wave * A::kRows + row;
             __hip_atomic_store(&ln.part_o[pr * A::kD + d], __builtin_nanf(""), __ATOMIC_RELAXED,
@@ -863,7 +878,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
         join<A::kD>(ln.part_ml, ln.part_o, A::kQb, rows, g1 - g0 + 1,
                 [&](int i) { return slot_of(g0 + i); }, [&](int row, int d, const f4& v, f2 ml) {
                   if (groups == 1) {
-                    sink.put(sink.at(qblk * A::kQb + row), d, v, ml);
+                    t.put(t.at(qblk * A::kQb + row), d, v, ml.x, ml.y);
                   } else {
                     const int64_t pr = slot_of(g0) * A::kQb + row;
                     put4(ln.part_o + pr * A::kD + d, v);
@@ -874,7 +889,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
           join<A::kD>(ln.group_ml, ln.part_o, A::kQb, rows, groups,
                   [&](int i) { return slot_of(w0 + i * kJoin); },
                   [&](int row, int d, const f4& v, f2 ml) {
-                    sink.put(sink.at(qblk * A::kQb + row), d, v, ml);
+                    t.put(t.at(qblk * A::kQb + row), d, v, ml.x, ml.y);
                   });
       }
     }

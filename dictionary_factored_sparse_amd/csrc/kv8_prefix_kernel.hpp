@@ -8,23 +8,55 @@
 namespace dfs {
 namespace {
 
-// Complete sums of a line.
-template <typename A>
-struct Sums {
-  const A& t;
-  float* o;
-  f2* ml;
+// The items of one line; complete rows are sums of it.
+template <typename B>
+struct Part : B {
+  const PrefixWs& ws;
+  const PrefixLine& w;
+  __device__ __forceinline__ Part(const KvAttnLaunch& a, const PrefixWs& s, const PrefixLine& l)
+      : B(a), ws(s), w(l) {}
+  __device__ __forceinline__ int64_t first(int e) const { return *gptr(w.first + e); }
+  __device__ __forceinline__ int longest() const { return uni(*gptr(w.n + 1)); }
   __device__ __forceinline__ int64_t at(int row) const {
-    const int g = t.a.q_heads / t.a.kv.heads;
-    const int tok = row / g, h = t.kh * g + row - tok * g;
-    return (int64_t)(t.rq.t0 + tok) * t.a.q_heads + h;
+    const int g = B::a.q_heads / B::a.kv.heads;
+    const int tok = row / g, h = B::kh * g + row - tok * g;
+    return (int64_t)(B::rq.t0 + tok) * B::a.q_heads + h;
   }
-  __device__ __forceinline__ void put(int64_t at, int d, const f4& v, f2 w) const {
-    *gptr_w((f4*)(o + at * A::kD + d)) = v;
-    if (d == 0) *gptr_w(ml + at) = w;
+  __device__ __forceinline__ void put(int64_t at, int d, const f4& v, float m, float l) const {
+    *gptr_w((f4*)(w.sum_o + at * B::kD + d)) = v;
+    if (d == 0) *gptr_w(w.sum_ml + at) = f2{m, l};
   }
   __device__ __forceinline__ void put_nan(int64_t at, int d) const {
-    *gptr_w(o + at * A::kD + d) = __builtin_nanf("");
+    *gptr_w(w.sum_o + at * B::kD + d) = __builtin_nanf("");
+  }
+};
+// The keys that groups share.
+template <typename B>
+struct SharedPart : Part<B> {
+  using P = Part<B>;
+  __device__ __forceinline__ SharedPart(const KvAttnLaunch& a, const PrefixWs& s) : P(a, s, s.shared) {}
+  __device__ __forceinline__ int ready(int e, int kh) {
+    const int i = uni(*gptr(P::w.of + e)), qblk = uni(*gptr(P::w.qblk + e));
+    const PrefixGroup* f = P::ws.groups + i;
+    const int t0 = uni(*gptr(&f->t0)), keys = uni(*gptr(&f->keys));
+    const int32_t* pos = P::ws.pos + t0;
+    B::template begin_by<true>(Req{t0, uni(*gptr(&f->n)), keys, keys}, uni(*gptr(&f->row)), qblk, kh, 0,
+                               uni(*gptr(&f->p0)), uni(*gptr(&f->p1)),
+                               [=](int tok) { return *gptr(pos + tok); });
+    return qblk;
+  }
+};
+// Each request's own keys.
+template <typename B>
+struct OwnPart : Part<B> {
+  using P = Part<B>;
+  __device__ __forceinline__ OwnPart(const KvAttnLaunch& a, const PrefixWs& s) : P(a, s, s.own) {}
+  __device__ __forceinline__ int ready(int e, int kh) {
+    const int req = uni(*gptr(P::w.of + e)), qblk = uni(*gptr(P::w.qblk + e));
+    const int grp = uni(*gptr(P::ws.group_of + req));
+    const int from = grp < 0 ? 0 : uni(*gptr(&P::ws.groups[grp].keys));
+    B::begin(get_req(B::a.b, B::a.kv.page, req), req, qblk, kh, from);
+    return qblk;
   }
 };
 __device__ __forceinline__ Line line_of(const PrefixLine& p) {
@@ -34,50 +66,20 @@ __device__ __forceinline__ Line line_of(const PrefixLine& p) {
 template <int KIND, int D, int NQ, bool SPLIT, int OWN, bool BIG>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 void prefix_kernel(KvAttnLaunch a, PrefixWs ws, int slices) {
-  using P = Attn<KIND, D, NQ, SPLIT, false, BIG>;
-  using S = Attn<KIND, D, OWN, true, false, BIG>;
+  using P = SharedPart<Attn<KIND, D, NQ, SPLIT, false, BIG>>;
+  using S = OwnPart<Attn<KIND, D, OWN, true, false, BIG>>;
   __shared__ union {
     typename P::Work p;
     typename S::Work s;
   } sh;
-  const int g = a.q_heads / a.kv.heads;
   {
-    P t(a);
-    const PrefixLine& w = ws.shared;
-    run_line(
-        t, sh.p, line_of(w), *gptr(w.n), [&](int e) { return *gptr(w.first + e); },
-        [&] { return uni(*gptr(w.n + 1)); },
-        [&](int e, int kh) {
-          const int i = uni(*gptr(w.of + e)), qblk = uni(*gptr(w.qblk + e));
-          const PrefixGroup* f = ws.groups + i;
-          const int t0 = uni(*gptr(&f->t0)), keys = uni(*gptr(&f->keys));
-          const Req q = {t0, uni(*gptr(&f->n)), keys, keys};
-          const Span s = get_span(q, uni(*gptr(&f->p0)), uni(*gptr(&f->p1)), a.window, a.sinks);
-          t.template begin<true>(q, s, uni(*gptr(&f->row)), qblk, kh,
-                                 [&](int tok) { return *gptr(ws.pos + t0 + tok); });
-          return qblk;
-        },
-        Sums<P>{t, w.sum_o, w.sum_ml}, SPLIT ? kWaves : 1, (int)blockIdx.x, slices);
+    P t(a, ws);
+    run_line(t, sh.p, line_of(ws.shared), *gptr(ws.shared.n), SPLIT ? kWaves : 1, (int)blockIdx.x, slices);
   }
   __syncthreads();
   {
-    S t(a);
-    const PrefixLine& w = ws.own;
-    run_line(
-        t, sh.s, line_of(w), *gptr(w.n), [&](int e) { return *gptr(w.first + e); },
-        [&] { return uni(*gptr(w.n + 1)); },
-        [&](int e, int kh) {
-          const int req = uni(*gptr(w.of + e)), qblk = uni(*gptr(w.qblk + e));
-          const int grp = uni(*gptr(ws.group_of + req));
-          const int from = grp < 0 ? 0 : uni(*gptr(&ws.groups[grp].keys));
-          const Req f = get_req(a.b, a.kv.page, req);
-          const Req q = {uni(f.t0), uni(f.n), uni(f.len), uni(f.keys)};
-          const int pos0 = q.len - q.n, i0 = qblk * S::kQb, i1 = min(i0 + S::kQb, q.n * g);
-          const Span s = get_span(q, pos0 + i0 / g, pos0 + (i1 - 1) / g, a.window, a.sinks, from);
-          t.template begin<false>(q, s, req, qblk, kh, [&](int tok) { return pos0 + tok; });
-          return qblk;
-        },
-        Sums<S>{t, w.sum_o, w.sum_ml}, kWaves, (int)blockIdx.x, slices);
+    S t(a, ws);
+    run_line(t, sh.s, line_of(ws.own), *gptr(ws.own.n), kWaves, (int)blockIdx.x, slices);
   }
 }
 
