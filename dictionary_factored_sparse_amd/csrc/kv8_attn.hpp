@@ -282,6 +282,9 @@ struct Attn {
   // under a window of 512: 74, 64)
   static constexpr int kExtra = SPLIT ? 4 : 3;
   static constexpr bool kSplit = SPLIT, kNan = KIND == DFS_FP8;  // kNan: codes may be NaN
+  static constexpr bool kJoinHere = true;
+  static constexpr int kEach = 0;          // items of at most so many tiles are dealt out whole
+  static constexpr int kKeep = SPLIT ? 0 : kWhole;  // or taken whole by the slice they start in
   static constexpr int kD = D, kNq = NQ;
   static constexpr int kRows = 16 * NQ;                      // per wave
   static constexpr int kQb = SPLIT ? kRows : kRows * kWaves;  // per item
@@ -746,18 +749,21 @@ struct Line {
 // first(n_entries) its end; longest() the most tiles an item has; ready(e, kv head)
 // readies t for an item and returns its block of rows; the rows that are complete
 // go to at(row of the entry's requests), by put(at, dim, four sums, reference of
-// the weights, their sum) and put_nan(at, dim).
+// the weights, their sum) and put_nan(at, dim).  Where A::kJoinHere, the parts of an
+// item are joined as they come; else they stay where they are for a later kernel.
 template <typename A>
 __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line& ln, int n_entries, int least,
                                          int slice, int slices) {
   if (n_entries == 0) return;
+  const bool each = A::kEach > 0 && t.longest() <= A::kEach;
   const int64_t total = t.first(n_entries);
   const int64_t per = max((int64_t)least, (total + slices - 1) / slices);
-  const int64_t xs = slice * per, xe = min(xs + per, total);
-  if (xs >= total) return;
+  const int64_t xs = each ? slice : slice * per;
+  const int64_t xe = each ? (int64_t)n_entries * t.a.kv.heads : min(xs + per, total);
+  if (xs >= (each ? xe : total)) return;
   // the entry e with first(e) <= xs < first(e + 1)
   int e = 0;
-  for (int n = n_entries; n > 1;) {
+  for (int n = each ? 1 : n_entries; n > 1;) {
     const int stride = (n + kThreads - 1) / kThreads;
     const int at = (int)threadIdx.x * stride;
     const int below = __syncthreads_count(at < n && t.first(e + at) <= xs);
@@ -768,20 +774,24 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
   // whole.  A part and its join cost as much as some tiles (four prompts of 500
   // tokens, 8 tiles at most: 46 us split, 38 us whole; windows of 512 tokens, 11
   // tiles: 70 us split, 82 us whole).
-  const bool keep = !A::kSplit && t.longest() <= kWhole;
+  const bool keep = A::kKeep > 0 && t.longest() <= A::kKeep;
   for (int64_t x = xs; x < xe;) {
-    while (t.first(e + 1) <= x) ++e;
+    if (each) e = (int)(x / t.a.kv.heads);
+    else
+      while (t.first(e + 1) <= x) ++e;
     const int64_t fe = t.first(e);
     // an item is its tiles, and then the extra ones
     const int n_line = uni((int)((t.first(e + 1) - fe) / t.a.kv.heads)), n_tiles = n_line - A::kExtra;
-    const int kh = uni((int)((x - fe) / n_line));
+    const int kh = uni(each ? (int)(x % t.a.kv.heads) : (int)((x - fe) / n_line));
     const int64_t item0 = fe + (int64_t)kh * n_line, item1 = item0 + n_tiles;
-    if (keep ? x > item0 : x >= item1) {  // another slice's, or only extra ones are left of it
+    if (!each && (keep ? x > item0 : x >= item1)) {  // another slice's, or only extra ones are left of it
       x = item0 + n_line;
       continue;
     }
-    const int u0 = uni((int)(x - item0)), u1 = uni(keep ? n_tiles : (int)(min(item1, xe) - item0));
-    x = u1 == n_tiles ? item0 + n_line : item0 + u1;
+    const int u0 = uni(each ? 0 : (int)(x - item0));
+    const int u1 = uni(each || keep ? n_tiles : (int)(min(item1, xe) - item0));
+    if (each) x += slices;
+    else x = u1 == n_tiles ? item0 + n_line : item0 + u1;
     const int qblk = t.ready(e, kh);
     const int v0 = A::kSplit ? u0 + t.wave : u0, step = A::kSplit ? kWaves : 1;
     const int v1 = A::kSplit || t.nrows > 0 ? u1 : u0;  // this wave's tiles: v0, v0 + step, ... below v1
@@ -863,7 +873,7 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
           }
         });
     }
-    if (!whole) {
+    if (A::kJoinHere && !whole) {
       // The parts of an item are joined in groups of kJoin slices, each by the
       // slice of the group that comes last, then the groups' results by the
       // group that comes last: always in slice order.

@@ -5,8 +5,8 @@
 // of query rows of all the group's requests, and each request's own keys from
 // there on.  A workgroup takes its slice of the one and then its slice of the
 // other, so that both load every CU alike whatever their share of the work, with
-// no gap between them.  Each line leaves sums of its own for each row, in fp32;
-// a second kernel puts them together.
+// no gap between them.  What an item or a part of one gives for its rows stays in
+// fp32 sums; a second kernel, over all rows at once, joins them.
 #pragma once
 
 #include "dfs_internal.hpp"
@@ -23,26 +23,37 @@ struct PrefixGroup {
   int32_t keys;    // shared keys, a multiple of the tile; 0: nothing is shared
   int32_t row;     // row of the page table
 };
-// One line's plan and parts.
-struct PrefixLine {
+// One line's plan.
+struct PrefixEntries {
   int64_t* first;  // where each entry starts, then the total
   int32_t* of;     // group or request of each entry
   int32_t* qblk;   // its block of rows
   int32_t* n;      // entries, and the most tiles of an item
-  int32_t most;    // entries at most
-  uint32_t* count;
-  float* part_o;
-  f2* part_ml;
-  f2* group_ml;
-  float* sum_o;    // [tokens * q_heads][D]: what the line gives for each row
-  f2* sum_ml;
 };
-struct PrefixWs {
+// What the second kernel needs to know of a token: the first entries of its
+// request and of its group, and the token's first row in them; -1: none.
+struct PrefixToken {
+  int32_t own, own_row, shared, shared_row;
+};
+struct PrefixPlan {
   PrefixGroup* groups;  // [n_groups]
   int32_t* live;        // [n_groups]: requests with tokens
-  int32_t* group_of;    // [n_req]: group of each request, or -1
+  int32_t* from;        // [n_req]: first key of its own
   int32_t* pos;         // [n_tok]: position of each token
-  PrefixLine shared, own;
+  PrefixEntries shared, own;
+};
+// One line's sums.
+struct PrefixSums {
+  float* part_o;  // [2 * slices][rows][D], as run_line places them
+  f2* part_ml;
+  float* o;       // [tokens * q_heads][D]: of items that are not split
+  f2* ml;
+};
+struct PrefixWs {
+  PrefixPlan plan;
+  PrefixToken* tokens;  // [n_tok]
+  PrefixSums shared, own;
+  int32_t most_shared, most_own;  // entries at most
 };
 // The forms of the two lines.
 struct PrefixCut {
@@ -50,12 +61,19 @@ struct PrefixCut {
   int nq, qb;       // groups of 16 rows a wave, rows an item
   int nq_own;       // of the own keys, always in turn
   int slices;
+  int in;           // the workgroups plan for themselves
 };
 struct PrefixLaunch {
   KvAttnLaunch a;
   int32_t n_groups;
   const int32_t *group_start, *shared;
 };
+
+// Up to these the workgroups plan for themselves, in LDS.
+constexpr int kPrefixInline = 128;         // requests
+constexpr int kPrefixInlineTokens = 256;
+constexpr int kPrefixInlineEntries = 128;  // of either line, at most
+constexpr int kPrefixEach = 16;            // own keys: tiles up to which items are not split
 
 template <int D>
 void launch_prefix(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s);

@@ -2,106 +2,133 @@
 // translation unit.
 #pragma once
 
-#include "kv8_attn.hpp"
-#include "kv8_prefix.hpp"
+#include "kv8_prefix_plan.hpp"
 
 namespace dfs {
 namespace {
 
+// The plan, where it is.
+struct PrefixAt {
+  const PrefixPlan* ws;
+  const PrefixInline* lds;
+  bool in;  // in LDS
+};
+
 // The items of one line; complete rows are sums of it.
-template <typename B>
+template <typename B, bool SHARED>
 struct Part : B {
-  const PrefixWs& ws;
-  const PrefixLine& w;
-  __device__ __forceinline__ Part(const KvAttnLaunch& a, const PrefixWs& s, const PrefixLine& l)
-      : B(a), ws(s), w(l) {}
-  __device__ __forceinline__ int64_t first(int e) const { return *gptr(w.first + e); }
-  __device__ __forceinline__ int longest() const { return uni(*gptr(w.n + 1)); }
+  static constexpr bool kJoinHere = false;
+  static constexpr int kEach = SHARED ? 0 : kPrefixEach, kKeep = 0;
+  const PrefixAt& at_;
+  const PrefixSums& sums;
+  __device__ __forceinline__ Part(const KvAttnLaunch& a, const PrefixAt& p, const PrefixSums& s)
+      : B(a), at_(p), sums(s) {}
+  __device__ __forceinline__ const PrefixInline::Entries& lds() const {
+    return SHARED ? at_.lds->line_shared : at_.lds->line_own;
+  }
+  __device__ __forceinline__ const PrefixEntries& far() const { return SHARED ? at_.ws->shared : at_.ws->own; }
+  __device__ __forceinline__ int entries() const { return at_.in ? lds().n[0] : *gptr(far().n); }
+  __device__ __forceinline__ int64_t first(int e) const { return at_.in ? lds().first[e] : *gptr(far().first + e); }
+  __device__ __forceinline__ int longest() const { return uni(at_.in ? lds().n[1] : *gptr(far().n + 1)); }
+  __device__ __forceinline__ int ready(int e, int kh) {
+    const int i = uni(at_.in ? lds().of[e] : *gptr(far().of + e));
+    const int qblk = uni(at_.in ? lds().qblk[e] : *gptr(far().qblk + e));
+    if constexpr (SHARED) {
+      const PrefixGroup f = at_.in ? at_.lds->groups[i] : at_.ws->groups[i];
+      const int t0 = uni(f.t0), keys = uni(f.keys);
+      B::template begin_by<true>(Req{t0, f.n, keys, keys}, uni(f.row), qblk, kh, 0, uni(f.p0), uni(f.p1),
+                                 [&](int tok) { return at_.in ? at_.lds->pos[t0 + tok] : *gptr(at_.ws->pos + t0 + tok); });
+    } else {
+      B::begin(at_.in ? at_.lds->facts[i] : get_req(B::a.b, B::a.kv.page, i), i, qblk, kh,
+               uni(at_.in ? at_.lds->from[i] : *gptr(at_.ws->from + i)));
+    }
+    return qblk;
+  }
   __device__ __forceinline__ int64_t at(int row) const {
     const int g = B::a.q_heads / B::a.kv.heads;
     const int tok = row / g, h = B::kh * g + row - tok * g;
     return (int64_t)(B::rq.t0 + tok) * B::a.q_heads + h;
   }
   __device__ __forceinline__ void put(int64_t at, int d, const f4& v, float m, float l) const {
-    *gptr_w((f4*)(w.sum_o + at * B::kD + d)) = v;
-    if (d == 0) *gptr_w(w.sum_ml + at) = f2{m, l};
+    *gptr_w((f4*)(sums.o + at * B::kD + d)) = v;
+    if (d == 0) {  // as one whole number: see put2
+      *gptr_w((uint64_t*)(sums.ml + at)) = (uint64_t)__float_as_uint(l) << 32 | __float_as_uint(m);
+    }
   }
   __device__ __forceinline__ void put_nan(int64_t at, int d) const {
-    *gptr_w(w.sum_o + at * B::kD + d) = __builtin_nanf("");
+    *gptr_w(sums.o + at * B::kD + d) = __builtin_nanf("");
   }
 };
-// The keys that groups share.
-template <typename B>
-struct SharedPart : Part<B> {
-  using P = Part<B>;
-  __device__ __forceinline__ SharedPart(const KvAttnLaunch& a, const PrefixWs& s) : P(a, s, s.shared) {}
-  __device__ __forceinline__ int ready(int e, int kh) {
-    const int i = uni(*gptr(P::w.of + e)), qblk = uni(*gptr(P::w.qblk + e));
-    const PrefixGroup* f = P::ws.groups + i;
-    const int t0 = uni(*gptr(&f->t0)), keys = uni(*gptr(&f->keys));
-    const int32_t* pos = P::ws.pos + t0;
-    B::template begin_by<true>(Req{t0, uni(*gptr(&f->n)), keys, keys}, uni(*gptr(&f->row)), qblk, kh, 0,
-                               uni(*gptr(&f->p0)), uni(*gptr(&f->p1)),
-                               [=](int tok) { return *gptr(pos + tok); });
-    return qblk;
-  }
-};
-// Each request's own keys.
-template <typename B>
-struct OwnPart : Part<B> {
-  using P = Part<B>;
-  __device__ __forceinline__ OwnPart(const KvAttnLaunch& a, const PrefixWs& s) : P(a, s, s.own) {}
-  __device__ __forceinline__ int ready(int e, int kh) {
-    const int req = uni(*gptr(P::w.of + e)), qblk = uni(*gptr(P::w.qblk + e));
-    const int grp = uni(*gptr(P::ws.group_of + req));
-    const int from = grp < 0 ? 0 : uni(*gptr(&P::ws.groups[grp].keys));
-    B::begin(get_req(B::a.b, B::a.kv.page, req), req, qblk, kh, from);
-    return qblk;
-  }
-};
-__device__ __forceinline__ Line line_of(const PrefixLine& p) {
-  return {p.count, p.part_o, p.part_ml, p.group_ml};
-}
+__device__ __forceinline__ Line line_of(const PrefixSums& p) { return {nullptr, p.part_o, p.part_ml, nullptr}; }
 
 template <int KIND, int D, int NQ, bool SPLIT, int OWN, bool BIG>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
-void prefix_kernel(KvAttnLaunch a, PrefixWs ws, int slices) {
-  using P = SharedPart<Attn<KIND, D, NQ, SPLIT, false, BIG>>;
-  using S = OwnPart<Attn<KIND, D, OWN, true, false, BIG>>;
+void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
+  using P = Part<Attn<KIND, D, NQ, SPLIT, false, BIG>, true>;
+  using S = Part<Attn<KIND, D, OWN, true, false, BIG>, false>;
   __shared__ union {
     typename P::Work p;
     typename S::Work s;
   } sh;
+  __shared__ PrefixInline lds;
+  const KvAttnLaunch& a = p.a;
+  const PrefixAt at = {&ws.plan, &lds, in != 0};
+  if (in) {
+    const int tid = threadIdx.x;
+    if (tid < a.b.n_req) lds.facts[tid] = get_req(a.b, a.kv.page, tid);
+    if (tid <= p.n_groups) lds.group_start[tid] = *gptr(p.group_start + tid);
+    if (tid < p.n_groups) lds.shared[tid] = *gptr(p.shared + tid);
+    __syncthreads();
+    const PrefixPlan w = {lds.groups, lds.live, lds.from, lds.pos,
+                          {lds.line_shared.first, lds.line_shared.of, lds.line_shared.qblk, lds.line_shared.n},
+                          {lds.line_own.first, lds.line_own.of, lds.line_own.qblk, lds.line_own.n}};
+    make_prefix_plan<kThreads>(
+        p, w, [&](int r) { return lds.facts[r]; }, [&](int i) { return lds.group_start[i]; },
+        [&](int i) { return lds.shared[i]; }, lds.group_of, lds.first_entry, lds.first_shared, ws.most_shared,
+        ws.most_own, P::kQb, P::kExtra, S::kQb, S::kExtra,
+        [&](int t, const PrefixToken& k) {
+          if (blockIdx.x == 0) ws.tokens[t] = k;
+        },
+        lds.tmp, &lds.longest);
+    if (blockIdx.x == 0) {  // what the second kernel reads of it
+      for (int l = 0; l < 2; ++l) {
+        const PrefixInline::Entries& e = l ? lds.line_own : lds.line_shared;
+        const PrefixEntries& f = l ? ws.plan.own : ws.plan.shared;
+        for (int i = tid; i <= e.n[0]; i += kThreads) f.first[i] = e.first[i];
+        if (tid < 2) f.n[tid] = e.n[tid];
+      }
+    }
+  }
   {
-    P t(a, ws);
-    run_line(t, sh.p, line_of(ws.shared), *gptr(ws.shared.n), SPLIT ? kWaves : 1, (int)blockIdx.x, slices);
+    P t(a, at, ws.shared);
+    run_line(t, sh.p, line_of(ws.shared), t.entries(), SPLIT ? kWaves : 1, (int)blockIdx.x, slices);
   }
   __syncthreads();
   {
-    S t(a, ws);
-    run_line(t, sh.s, line_of(ws.own), *gptr(ws.own.n), kWaves, (int)blockIdx.x, slices);
+    S t(a, at, ws.own);
+    run_line(t, sh.s, line_of(ws.own), t.entries(), kWaves, (int)blockIdx.x, slices);
   }
 }
 
 template <int KIND, int D, int NQ, bool SPLIT, int OWN>
-void go(const KvAttnLaunch& a, const PrefixWs& w, const PrefixCut& c, hipStream_t s) {
-  if (a.kv.page >= kTile)
+void go(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s) {
+  if (p.a.kv.page >= kTile)
     hipLaunchKernelGGL((prefix_kernel<KIND, D, NQ, SPLIT, OWN, true>), dim3(c.slices), dim3(kThreads), 0,
-                       s, a, w, c.slices);
+                       s, p, w, c.slices, c.in);
   else
     hipLaunchKernelGGL((prefix_kernel<KIND, D, NQ, SPLIT, OWN, false>), dim3(c.slices), dim3(kThreads), 0,
-                       s, a, w, c.slices);
+                       s, p, w, c.slices, c.in);
 }
 template <int KIND, int D>
-void go_cut(const KvAttnLaunch& a, const PrefixWs& w, const PrefixCut& c, hipStream_t s) {
+void go_cut(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s) {
   if (!c.split) {
-    if (c.nq_own == 1) go<KIND, D, 2, false, 1>(a, w, c, s);
-    else go<KIND, D, 2, false, 2>(a, w, c, s);
+    if (c.nq_own == 1) go<KIND, D, 2, false, 1>(p, w, c, s);
+    else go<KIND, D, 2, false, 2>(p, w, c, s);
   } else if (c.nq == 1) {
-    go<KIND, D, 1, true, 1>(a, w, c, s);
+    go<KIND, D, 1, true, 1>(p, w, c, s);
   } else {
-    if (c.nq_own == 1) go<KIND, D, 2, true, 1>(a, w, c, s);
-    else go<KIND, D, 2, true, 2>(a, w, c, s);
+    if (c.nq_own == 1) go<KIND, D, 2, true, 1>(p, w, c, s);
+    else go<KIND, D, 2, true, 2>(p, w, c, s);
   }
 }
 
@@ -109,8 +136,8 @@ void go_cut(const KvAttnLaunch& a, const PrefixWs& w, const PrefixCut& c, hipStr
 
 template <int D>
 void launch_prefix(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s) {
-  if (p.a.kv.dtype == DFS_FP8) go_cut<DFS_FP8, D>(p.a, w, c, s);
-  else go_cut<DFS_INT8, D>(p.a, w, c, s);
+  if (p.a.kv.dtype == DFS_FP8) go_cut<DFS_FP8, D>(p, w, c, s);
+  else go_cut<DFS_INT8, D>(p, w, c, s);
 }
 
 }  // namespace dfs
