@@ -3,10 +3,10 @@
 //
 // Two lines of items (kv8_attn.hpp): the groups' shared keys, each item a block
 // of query rows of all the group's requests, and each request's own keys from
-// there on.  A workgroup takes its slice of the one and then its slice of the
-// other, so that both load every CU alike whatever their share of the work, with
-// no gap between them.  What an item or a part of one gives for its rows stays in
-// fp32 sums; a second kernel, over all rows at once, joins them.
+// there on.  The workgroups are dealt out between the two by their work.  (With a
+// slice of both for every workgroup, one after the other, the chain of reads that
+// starts an item was paid twice.)  What an item or a part of one gives for its rows
+// stays in fp32 sums; a second kernel, over all rows at once, joins them.
 #pragma once
 
 #include "dfs_internal.hpp"
@@ -74,6 +74,7 @@ constexpr int kPrefixInline = 128;         // requests
 constexpr int kPrefixInlineTokens = 256;
 constexpr int kPrefixInlineEntries = 128;  // of either line, at most
 constexpr int kPrefixEach = 16;            // own keys: tiles up to which items are not split
+constexpr int kPrefixLone = 4;             // and up to which a wave takes one alone, if they are few
 
 template <int D>
 void launch_prefix(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s);

@@ -12,21 +12,21 @@ constexpr int kPlanThreads = 1024;
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, PrefixWs ws, int32_t* scratch, int qb,
                                                             int extra, int qb_own, int extra_own) {
-  __shared__ int64_t tmp[kPlanThreads / kWave];
-  __shared__ int longest;
+  __shared__ int64_t tmp[kPlanThreads / kWave][2];
+  __shared__ int longest[2];
   const int n = p.a.b.n_req;
   make_prefix_plan<kPlanThreads>(
       p, ws.plan, [&](int r) { return get_req(p.a.b, p.a.kv.page, r); },
       [&](int i) { return *gptr(p.group_start + i); }, [&](int i) { return *gptr(p.shared + i); }, scratch,
       scratch + n, scratch + 2 * n, ws.most_shared, ws.most_own, qb, extra, qb_own, extra_own,
-      [&](int t, const PrefixToken& k) { ws.tokens[t] = k; }, tmp, &longest);
+      [&](int t, const PrefixToken& k) { ws.tokens[t] = k; }, tmp, longest);
 }
 
 // How a line is cut.
 struct LineCut {
   PrefixEntries plan;
   PrefixSums sums;
-  int qb, extra, least, each;
+  int qb, extra, least, each, split;
 };
 
 // What one line gives for row `row` (counted from its entry's first one) of kv head
@@ -44,6 +44,7 @@ __device__ __forceinline__ void line_sums(const LineCut& c, int first_entry, int
   m = -1e30f;
   l = 0.0f;
   v = f4{0, 0, 0, 0};
+  // items that were not split: those dealt out whole, and those of one slice
   if (longest <= c.each || w0 == w1) {
     if (wave == 0) {
       const f2 w = *gptr(c.sums.ml + at);
@@ -97,13 +98,15 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(KvAttnLaunch a, const P
   const bool real = place < a.q_heads * quads;
   const int h = real ? place / quads : 0, d = real ? place % quads * 4 : 0, kh = h / g;
   const int64_t at = (int64_t)tok * a.q_heads + h;
+  const int n = shared_slices(*gptr(shared.plan.first + *gptr(shared.plan.n)), *gptr(own.plan.first + *gptr(own.plan.n)),
+                              shared.split != 0, slices);
   float m, l;
   f4 v;
-  line_sums(own, k.own, k.own_row + h - kh * g, kh, a.kv.heads, slices, at, D, d, wave, m, l, v);
+  line_sums(own, k.own, k.own_row + h - kh * g, kh, a.kv.heads, slices - n, at, D, d, wave, m, l, v);
   if (k.shared >= 0) {
     float y, z;
     f4 x;
-    line_sums(shared, k.shared, k.shared_row + h - kh * g, kh, a.kv.heads, slices, at, D, d, wave, y, z, x);
+    line_sums(shared, k.shared, k.shared_row + h - kh * g, kh, a.kv.heads, n, at, D, d, wave, y, z, x);
     const float top = fmaxf(m, y);
     const float fm = __builtin_amdgcn_exp2f(m - top), fy = __builtin_amdgcn_exp2f(y - top);
     l = l * fm + z * fy;
@@ -250,8 +253,8 @@ hipError_t launch_kv8_prefix_attention(const KvAttnLaunch& a, int32_t n_groups, 
   else if (a.kv.head_dim == 96) launch_prefix<96>(p, w, c, s);
   else if (a.kv.head_dim == 128) launch_prefix<128>(p, w, c, s);
   else launch_prefix<256>(p, w, c, s);
-  const LineCut shared_cut = {w.plan.shared, w.shared, c.qb, extra, c.split ? kWaves : 1, 0};
-  const LineCut own_cut = {w.plan.own, w.own, 16 * c.nq_own, Turns::kExtra, kWaves, kPrefixEach};
+  const LineCut shared_cut = {w.plan.shared, w.shared, c.qb, extra, c.split ? kWaves : 1, 0, c.split};
+  const LineCut own_cut = {w.plan.own, w.own, 16 * c.nq_own, Turns::kExtra, kWaves, kPrefixEach, 1};
   const int wide = (uintptr_t)a.O % (a.odt == DFS_F32 ? 16 : 8) == 0 && a.ldo % 4 == 0;
   const dim3 grid(a.b.n_tok, (a.q_heads * (a.kv.head_dim / 4) + kWave - 1) / kWave);
   if (a.odt == DFS_F32)

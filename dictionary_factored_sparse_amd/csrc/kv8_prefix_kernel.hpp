@@ -61,6 +61,40 @@ struct Part : B {
 };
 __device__ __forceinline__ Line line_of(const PrefixSums& p) { return {nullptr, p.part_o, p.part_ml, nullptr}; }
 
+// Short items of few rows, one a wave: wave `at` of n takes items at, at + n, ...
+// of the line; there is no barrier and nothing to join.
+template <typename A>
+__device__ __forceinline__ void run_lone(A& t, int n_entries, int at, int n) {
+  const int heads = t.a.kv.heads;
+  const int64_t items = (int64_t)n_entries * heads;
+  for (int64_t x = at; x < items; x += n) {
+    const int e = uni((int)((uint32_t)x / (uint32_t)heads)), kh = uni((int)x - e * heads);
+    const int n_tiles = uni((int)((t.first(e + 1) - t.first(e)) / heads)) - A::kExtra;
+    t.ready(e, kh);
+    t.template tiles<false>(0, n_tiles, 1);
+    const bool nans = A::kNan && t.any_nan();
+    if (A::kNan && nans) {
+      t.ready(e, kh);
+      t.template tiles<true>(0, n_tiles, 1);
+    }
+    t.finish();
+#pragma unroll
+    for (int i = 0; i < A::kNq; ++i) {
+      const int row = 16 * i + t.r16;
+      if (row < t.nrows) {
+        const int64_t at = t.at(t.row0 + row);
+#pragma unroll
+        for (int d = 0; d < A::kDims; ++d) t.put(at, d * 16 + t.q4 * 4, t.o[i][d], t.m[i], t.l[i]);
+      }
+    }
+    if (A::kNan && nans)
+      t.spread_nan(0, n_tiles, 1, [&](int i, int d) {
+        const int row = 16 * i + t.r16;
+        if (row < t.nrows) t.put_nan(t.at(t.row0 + row), d);
+      });
+  }
+}
+
 template <int KIND, int D, int NQ, bool SPLIT, int OWN, bool BIG>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
@@ -89,7 +123,7 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
         [&](int t, const PrefixToken& k) {
           if (blockIdx.x == 0) ws.tokens[t] = k;
         },
-        lds.tmp, &lds.longest);
+        lds.tmp, lds.longest);
     if (blockIdx.x == 0) {  // what the second kernel reads of it
       for (int l = 0; l < 2; ++l) {
         const PrefixInline::Entries& e = l ? lds.line_own : lds.line_shared;
@@ -99,14 +133,22 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
       }
     }
   }
-  {
+  auto length = [&](const PrefixInline::Entries& e, const PrefixEntries& f) {
+    return in ? e.first[e.n[0]] : *gptr(f.first + *gptr(f.n));
+  };
+  const int n = shared_slices(length(lds.line_shared, ws.plan.shared), length(lds.line_own, ws.plan.own), SPLIT, slices);
+  const int slice = blockIdx.x;
+  if (slice < n) {
     P t(a, at, ws.shared);
-    run_line(t, sh.p, line_of(ws.shared), t.entries(), SPLIT ? kWaves : 1, (int)blockIdx.x, slices);
-  }
-  __syncthreads();
-  {
+    run_line(t, sh.p, line_of(ws.shared), t.entries(), SPLIT ? kWaves : 1, slice, n);
+  } else {
     S t(a, at, ws.own);
-    run_line(t, sh.s, line_of(ws.own), t.entries(), kWaves, (int)blockIdx.x, slices);
+    const int entries = t.entries(), longest = t.longest();
+    const int64_t items = (int64_t)entries * a.kv.heads;
+    if (longest <= kPrefixLone || (longest <= kPrefixEach && items >= 2 * (slices - n)))
+      run_lone(t, entries, slice - n + t.wave * (slices - n), (slices - n) * kWaves);
+    else
+      run_line(t, sh.s, line_of(ws.own), entries, kWaves, slice - n, slices - n);
   }
 }
 
