@@ -12,14 +12,17 @@
 //
 // The largest elements of a piece.  The width-th largest of the 64 lanes'
 // maxima of one wave bounds the width-th largest element from below; it takes
-// 32 steps of a compare and a count of the lanes, no memory.  The few elements
-// above the bound go to a list in LDS, where each is ranked by counting those
-// above it.  If more than the list holds are equal to the bound, the elements
-// are taken one by one.
+// 32 steps of a compare and a count of the lanes, no memory.  The elements above
+// the bound (some four to eight times the width) go to a list in LDS; the same
+// count over the list finds the width-th largest of them, and what reaches it is
+// ranked within one wave by broadcasts of its registers.  (Ranking the whole list by
+// reads of LDS took 330 us for 256 rows of 131072 and width 32.)  If too many are
+// equal, they are ranked over the whole list, and if the list does not hold them,
+// taken one by one.
 //
 // Precision.  Beams of different rows compete by sums that may be close: the
-// exponentials are summed in 64 bits, with the rounding error of their
-// arguments put back in, and totals are compared in 64 bits.
+// exponentials, with the rounding error of their arguments put back in, are added
+// in pairs in 32 bits and from there on in 64, and totals are compared in 64 bits.
 #include <algorithm>
 
 #include "dfs_internal.hpp"
@@ -55,15 +58,61 @@ __device__ __forceinline__ double value_of(uint64_t k) {
   return __longlong_as_double((int64_t)(k ^ ((uint64_t)((int64_t)~k >> 63) | 0x8000000000000000ull)));
 }
 
-// The largest t that at least n lanes of the wave reach (0 where fewer have a key).
+// The largest t, of bits kLow and above, that at least n lanes of the wave reach (0
+// where fewer have a key): eleven bits of a number's fraction bound closely enough.
+constexpr int kLow = 12, kLow64 = 9;  // of a float's key, of the upper half of a double's
+template <int LOW>
 __device__ __forceinline__ uint32_t nth_largest(uint32_t k, int n) {
   uint32_t t = 0;
 #pragma unroll
-  for (int b = 31; b >= 0; --b) {
+  for (int b = 31; b >= LOW; --b) {
     const uint32_t u = t | 1u << b;
     if (__popcll(__ballot(k >= u)) >= n) t = u;
   }
   return t;
+}
+// The same of a list's `many` keys, f(i) being key i.
+template <int LOW, int PER, typename F>
+__device__ __forceinline__ uint32_t nth_of(int many, int n, F f) {
+  const int lane = threadIdx.x % kWave;
+  uint32_t k[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) k[j] = lane + j * kWave < many ? f(lane + j * kWave) : 0;
+  uint32_t t = 0;
+#pragma unroll 1
+  for (int b = 31; b >= LOW; --b) {
+    const uint32_t u = t | 1u << b;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c += __popcll(__ballot(k[j] >= u));
+    if (c >= n) t = u;
+  }
+  return t;
+}
+template <int LOW, typename F>
+__device__ __forceinline__ uint32_t nth_of_list(int many, int n, F f) {
+  if (many <= kWave) return 0;  // all of them can be ranked
+  return many <= 4 * kWave ? nth_of<LOW, 4>(many, n, f) : nth_of<LOW, kList / kWave>(many, n, f);
+}
+// The first 64 of the list's places whose key reaches t, in order, to `to`; how many
+// do.  By one wave.
+template <typename F>
+__device__ __forceinline__ int gather(int many, uint32_t t, F f, int* to) {
+  const int lane = threadIdx.x % kWave;
+  int m = 0;
+  for (int i0 = 0; i0 < many; i0 += kWave) {
+    const int i = i0 + lane;
+    const bool hit = i < many && f(i) >= t;
+    const uint64_t mask = __ballot(hit);
+    const int at = m + __popcll(mask & ((1ull << lane) - 1));
+    if (hit && at < kWave) to[at] = i;
+    m += __popcll(mask);
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, int l) {
+  return (uint64_t)lane_of((uint32_t)(v >> 32), l) << 32 | lane_of((uint32_t)v, l);
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
@@ -91,7 +140,8 @@ struct Cand {
 struct Shared {
   uint32_t wmax[kWaves], bound[kWaves];
   double wsum[kWaves];
-  int n, last;
+  int n, last, picked;
+  int pick[kWave];
   uint64_t best[kWaves];
   union {
     uint64_t list[kList];
@@ -120,30 +170,54 @@ __device__ __forceinline__ int state_of(const BeamLaunch& a, int row) {
   return a.done && *gptr(a.done + row) != 0 ? 2 : 1;
 }
 
+// Adds a piece's sum (in units of its largest exponential) to another.
+__device__ __forceinline__ void join_sums(uint32_t& top, double& sum, uint32_t k, double s) {
+  if (k <= kNone) return;
+  const uint32_t m = max(top, k);
+  if (top <= kNone) {
+    sum = s;
+  } else {
+    const double f = exp((double)value_of(min(top, k)) - (double)value_of(m));
+    sum = m == top ? sum + s * f : sum * f + s;
+  }
+  top = m;
+}
+
 // The request's choice, by the workgroup that came last.
 __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Shared& sh, int req, int chunks) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, W = a.width;
   const int64_t row0 = (int64_t)req * W;
-  for (int w = wave; w < W; w += kWaves) {
+  const int per_row = chunks * W, all = per_row * W;
+  const uint64_t* cands = ws.cand + row0 * per_row;
+  // the first candidates of this thread's first piece, on their way while the sums
+  // are joined (those of a row without logits are not used)
+  constexpr int kAhead = 8;
+  uint64_t x[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) x[k] = get(cands + min(tid * W, all - W) + min(k, W - 1));
+  // each row's sum, by 8 to 64 lanes of a wave
+  int lanes = kWave;
+  while (lanes * W > kThreads) lanes /= 2;
+  const int w = tid / lanes, sub = tid % lanes;
+  if (w < W) {
     const int st = state_of(a, (int)(row0 + w));
-    double lse = 0.0;
+    uint32_t top = 0;
+    double sum = 0.0;
     if (st == 1) {
       const uint64_t* p = ws.part + (row0 + w) * chunks * 2;
-      uint32_t m = 0;
-      for (int c = lane; c < chunks; c += kWave) m = max(m, (uint32_t)get(p + 2 * c));
-      m = wave_max(m);
-      const double top = value_of(m);
-      double s = 0.0;
-      if (m > kNone)
-        for (int c = lane; c < chunks; c += kWave) {
-          const uint32_t k = (uint32_t)get(p + 2 * c);
-          if (k > kNone) s += __longlong_as_double((int64_t)get(p + 2 * c + 1)) * exp((double)value_of(k) - top);
-        }
-      s = wave_sum(s);
-      lse = top + log(s);
+      for (int c = sub; c < chunks; c += lanes) {
+        const uint32_t k = (uint32_t)get(p + 2 * c);
+        const double s = __longlong_as_double((int64_t)get(p + 2 * c + 1));
+        join_sums(top, sum, k, s);
+      }
     }
-    if (lane == 0) {
-      sh.f.lse[w] = lse;
+    uint32_t best = top;
+    for (int o = lanes / 2; o > 0; o >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, o, kWave));
+    if (top != best) sum *= top > kNone ? exp((double)value_of(top) - (double)value_of(best)) : 0.0;
+    for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    top = best;
+    if (sub == 0) {
+      sh.f.lse[w] = top > kNone ? (double)value_of(top) + log(sum) : 0.0;
       sh.f.score[w] = a.score[row0 + w];
       sh.f.norm[w] = a.norm ? a.norm[row0 + w] : 1.0f;
       sh.f.state[w] = st;
@@ -151,39 +225,59 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
   }
   if (tid == 0) sh.n = 0;
   __syncthreads();
-  const int per_row = chunks * W, all = per_row * W;
-  const uint64_t* cands = ws.cand + row0 * per_row;
   auto total_of = [&](const Cand& c) {
     return sh.f.state[c.row] == 2 ? sh.f.score[c.row]
                                   : sh.f.score[c.row] + ((double)value_of((uint32_t)(c.elem >> 32)) - sh.f.lse[c.row]);
   };
-  // candidate i; key 0: none
-  auto cand_at = [&](int i) {
+  // A candidate of a row whose element is x, `first` in its list of the row's first
+  // piece (rows without logits have one, their eos); key 0: none.
+  auto cand_of = [&](int w, uint64_t x, bool first) {
     Cand c;
     c.key = 0;
-    c.row = i / per_row;
-    c.elem = 0;
-    const int st = sh.f.state[c.row];
-    if (st == 1) c.elem = get(cands + i);
-    if (st == 2 && i % per_row == 0) c.elem = (uint64_t)(kNone + 1) << 32 | (uint32_t)~a.eos;
-    if ((uint32_t)(c.elem >> 32) > kNone) c.key = key_of(total_of(c) * sh.f.norm[c.row]);
+    c.row = w;
+    c.elem = x;
+    const int st = sh.f.state[w];
+    if (st != 1) c.elem = st == 2 && first ? (uint64_t)(kNone + 1) << 32 | (uint32_t)~a.eos : 0;
+    if ((uint32_t)(c.elem >> 32) > kNone) c.key = key_of(total_of(c) * sh.f.norm[w]);
     return c;
   };
+  auto cand_at = [&](int i) {
+    const int w = i / per_row;
+    return cand_of(w, sh.f.state[w] == 1 ? get(cands + i) : 0, i == w * per_row);
+  };
+  // A piece's candidates descend: the width-th largest of the threads' first ones
+  // bounds those to look at.
+  const int lists = W * chunks;
   uint32_t mine = 0;
-  for (int i = tid; i < all; i += kThreads) mine = max(mine, (uint32_t)(cand_at(i).key >> 32));
-  const uint32_t b = nth_largest(mine, W);
+  for (int j = tid; j < lists; j += kThreads) {
+    const int w = j / chunks;
+    mine = max(mine, (uint32_t)(cand_of(w, j == tid ? x[0] : get(cands + j * W), j == w * chunks).key >> 32));
+  }
+  const uint32_t b = nth_largest<kLow64>(mine, W);
   if (lane == 0) sh.bound[wave] = b;
   __syncthreads();
   uint32_t bound = 0;
-  for (int w = 0; w < kWaves; ++w) bound = max(bound, sh.bound[w]);
-  for (int i = tid; i < all; i += kThreads) {
-    const Cand c = cand_at(i);
-    if (c.key != 0 && (uint32_t)(c.key >> 32) >= bound) {
-      const int at = atomicAdd(&sh.n, 1);
-      if (at < kList) {
-        sh.f.key[at] = c.key;
-        sh.f.elem[at] = c.elem;
-        sh.f.row[at] = c.row;
+  for (int v = 0; v < kWaves; ++v) bound = max(bound, sh.bound[v]);
+  for (int j = tid; j < lists; j += kThreads) {
+    const int w = j / chunks;
+    bool more = true;
+    for (int k0 = 0; k0 < W && more; k0 += kAhead) {
+      if (k0 > 0 || j != tid) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = get(cands + j * W + min(k0 + k, W - 1));
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (!more || k0 + k >= W) continue;
+        const Cand c = cand_of(w, x[k], k0 + k == 0 && j == w * chunks);
+        more = c.key != 0 && (uint32_t)(c.key >> 32) >= bound;
+        if (!more) continue;
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kList) {
+          sh.f.key[at] = c.key;
+          sh.f.elem[at] = c.elem;
+          sh.f.row[at] = c.row;
+        }
       }
     }
   }
@@ -198,12 +292,27 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
     if (a.done_out) a.done_out[o] = sh.f.state[c.row] == 2 || token == a.eos;
   };
   int found = min(n, W);
+  auto listed = [&](int i) { return Cand{sh.f.key[i], sh.f.elem[i], sh.f.row[i]}; };
   if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const Cand c = {sh.f.key[i], sh.f.elem[i], sh.f.row[i]};
+    if (wave == 0) {
+      auto hi = [&](int i) { return (uint32_t)(sh.f.key[i] >> 32); };
+      const int m = gather(n, nth_of_list<kLow64>(n, W, hi), hi, sh.pick);
+      if (lane == 0) sh.picked = m;
+    }
+    __syncthreads();
+    const int m = sh.picked;
+    if (m > kWave) {
+      for (int i = tid; i < n; i += kThreads) {
+        const Cand c = listed(i);
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += listed(j).above(c);
+        if (rank < W) write(rank, c);
+      }
+    } else if (wave == 0) {
+      const Cand c = listed(lane < m ? sh.pick[lane] : 0);
       int rank = 0;
-      for (int j = 0; j < n; ++j) rank += Cand{sh.f.key[j], sh.f.elem[j], sh.f.row[j]}.above(c);
-      if (rank < W) write(rank, c);
+      for (int j = 0; j < m; ++j) rank += Cand{lane_of(c.key, j), lane_of(c.elem, j), lane_of(c.row, j)}.above(c);
+      if (lane < m && rank < W) write(rank, c);
     }
   } else {
     // more than the list holds reach the bound: one after the other
@@ -246,14 +355,14 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, W = a.width;
   const int row = blockIdx.y, chunk = blockIdx.x, req = row / W;
-  if (state_of(a, row) == 1) {
-    const T* x = (const T*)a.logits + row * a.ldl;
-    float v[E];
+  const T* x = (const T*)a.logits + row * a.ldl;
+  float v[E];
+  auto load = [&] {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
       const int64_t i0 = ((int64_t)(chunk * kPieces + p) * kThreads + tid) * kN;
       if (i0 + kN <= a.vocab) {
-        const V w = *gptr((const V*)(x + i0));
+        const V w = *(const __attribute__((address_space(1))) V*)(x + i0);
 #pragma unroll
         for (int c = 0; c < kN; ++c) v[p * kN + c] = (float)w[c];
       } else {
@@ -262,38 +371,53 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
           v[p * kN + c] = i0 + c < a.vocab ? (float)*gptr(x + i0 + c) : -INFINITY;
       }
     }
-    uint32_t best = kNone;
+  };
+  // few rows: the logits come while the row's state is looked up; else rows without
+  // continuations of their own are not read
+  constexpr bool kEarly = E <= 8;
+  if constexpr (kEarly) load();
+  if (state_of(a, row) == 1) {
+    if constexpr (!kEarly) load();
+    float big = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      // NaN counts as no continuation, infinity as the largest number
-      v[e] = v[e] != v[e] ? -INFINITY : fminf(v[e], 3.402823466e38f);
-      best = max(best, key_of(v[e]));
+      // NaN counts as no continuation (a maximum passes over it), infinity as the
+      // largest number
+      v[e] = fminf(fmaxf(v[e], -INFINITY), 3.402823466e38f);
+      big = fmaxf(big, v[e]);
     }
-    const uint32_t wm = wave_max(best), wb = nth_largest(best, W);
+    const uint32_t best = key_of(big + 0.0f);
+    const uint32_t wm = wave_max(best), wb = nth_largest<kLow>(best, W);
     if (lane == 0) {
       sh.wmax[wave] = wm;
       sh.bound[wave] = wb;
     }
     if (tid == 0) sh.n = 0;
     __syncthreads();
-    uint32_t top = 0, bound = kNone + 1;
+    uint32_t top = 0, least = kNone + 1;
     for (int w = 0; w < kWaves; ++w) {
       top = max(top, sh.wmax[w]);
-      bound = max(bound, sh.bound[w]);
+      least = max(least, sh.bound[w]);
     }
-    const float m = value_of(top);
+    // as numbers: the least one of a list is the lowest finite float
+    const float m = value_of(top), bound = value_of(least);
     double sum = 0.0;
     if (top > kNone) {
-      constexpr double kLog2e = 1.44269504088896340736;
-      constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+      constexpr double kLn2 = 0.69314718055994530942;
+      constexpr float kHi = (float)(1.0 / kLn2), kLo = (float)((1.0 / kLn2 - (double)kHi) * kLn2);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = v[e] - m;
-        const float t = d * kHi;
-        // what the product's rounding lost, and the rest of log2 e
-        const float lost = d > -1e4f ? __builtin_fmaf(d, kHi, -t) + d * kLo : 0.0f;
-        const float y = __builtin_amdgcn_exp2f(t);
-        sum += (double)__builtin_fmaf(y, lost * 0.69314718f, y);
+      for (int e = 0; e < E; e += 2) {
+        float y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float d = fmaxf(v[e + i] - m, -1000.0f);
+          const float t = d * kHi;
+          // what the product's rounding lost, and the rest of 1 / ln 2, as a factor
+          const float lost = __builtin_fmaf(d, kLo, __builtin_fmaf(d, kHi, -t) * (float)kLn2);
+          const float z = __builtin_amdgcn_exp2f(t);
+          y[i] = __builtin_fmaf(z, lost, z);
+        }
+        sum += (double)(y[0] + y[1]);
       }
     }
     sum = wave_sum(sum);
@@ -301,23 +425,45 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
     // what may be among the largest
     auto elem_of = [&](int e) {
       const int64_t i = ((int64_t)(chunk * kPieces + e / kN) * kThreads + tid) * kN + e % kN;
-      return (uint64_t)key_of(v[e]) << 32 | (uint32_t)~(uint32_t)i;
+      return (uint64_t)key_of(v[e] + 0.0f) << 32 | (uint32_t)~(uint32_t)i;  // zeros of either sign are equal
     };
+    int mine = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (key_of(v[e]) >= bound) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < kList) sh.list[at] = elem_of(e);
+    for (int e = 0; e < E; ++e) mine += __popcll(__ballot(v[e] >= bound));
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sh.n, mine);
+    at = __builtin_amdgcn_readfirstlane(at);
+    if (at + mine <= kList) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint64_t hits = __ballot(v[e] >= bound);
+        if (v[e] >= bound) sh.list[at + __popcll(hits & ((1ull << lane) - 1))] = elem_of(e);
+        at += __popcll(hits);
       }
+    }
     __syncthreads();
     const int n = sh.n;
     uint64_t* out = ws.cand + ((int64_t)row * chunks + chunk) * W;
     if (n <= kList) {
-      for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = sh.list[i];
+      if (wave == 0) {
+        auto hi = [&](int i) { return (uint32_t)(sh.list[i] >> 32); };
+        const int m = gather(n, nth_of_list<kLow>(n, W, hi), hi, sh.pick);
+        if (lane == 0) sh.picked = m;
+      }
+      __syncthreads();
+      const int m = sh.picked;
+      if (m > kWave) {
+        for (int i = tid; i < n; i += kThreads) {
+          const uint64_t k = sh.list[i];
+          int rank = 0;
+          for (int j = 0; j < n; ++j) rank += sh.list[j] > k;
+          if (rank < W) put(out + rank, k);
+        }
+      } else if (wave == 0) {
+        const uint64_t k = sh.list[lane < m ? sh.pick[lane] : 0];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.list[j] > k;
-        if (rank < W) put(out + rank, k);
+        for (int j = 0; j < m; ++j) rank += lane_of(k, j) > k;
+        if (lane < m && rank < W) put(out + rank, k);
       }
       for (int i = n + tid; i < W; i += kThreads) put(out + i, 0);
     } else {

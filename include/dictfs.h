@@ -637,7 +637,8 @@ dfs_status beam_select_workspace_size(int32_t n_req, int32_t width, int32_t voca
  *   positive and finite, has none (the first step gives the beams 1 .. width-1 a
  *   score of -inf).  Where a request has fewer continuations than width, parent
  *   is its first row, token -1, score -inf and done_out 0.
- * Exponentials are fp32, their sums and the totals 64 bits.
+ * Exponentials and the sums of two of them are fp32, all other sums and the totals
+ * 64 bits.
  * 1 <= width <= 32, n_req <= 16384, n_req * width <= 65535 (DFS_E_RANGE).
  * Outputs must not overlap inputs.  The workspace's first 64 KiB must be zero
  * before its first use; every call leaves them zero again.  Calls sharing a
