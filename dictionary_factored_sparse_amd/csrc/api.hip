@@ -1104,7 +1104,7 @@ dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* 
   for (const void* out : {(const void*)parent, (const void*)token, (const void*)score_out, (const void*)done_out})
     for (const void* in : {(const void*)score, (const void*)done, (const void*)norm})
       if (overlap(out, rows, in, rows)) return DFS_E_INVALID;
-  DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab, dtype)));
+  DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab)));
   const BeamLaunch a = {n_req, width, vocab,  logits, dtype,     ldl,     score,
                         done,  norm,  eos,    parent, token,     score_out, done_out};
   DFS_HIP(launch_beam_select(a, ws, (hipStream_t)stream));

@@ -4,21 +4,20 @@
 // total(w, v) = score_w + x_wv - lse_w, lse_w = m_w + log sum_v 2^((x_wv - m_w) log2 e),
 // ranked by total * norm_w.
 //
-// One launch, one pass over the logits: a workgroup takes a piece of a row and
-// keeps its elements in registers, sums its exponentials and finds its `width`
-// largest elements (within a row the order of the totals is that of the
-// logits).  The workgroup that comes last of a request's joins the sums and
-// picks from what the pieces offer.
+// One launch, one pass over the logits.  A wave takes a part of a row, a step of 8
+// or 32 elements a lane at a time with the next step's loads on their way, sums the
+// exponentials and keeps what may be among the part's `width` largest elements
+// (within a row the order of the totals is that of the logits); there is no barrier
+// on the way.  The workgroup that comes last of a request's joins the sums and picks
+// from what the parts offer.
 //
-// The largest elements of a piece.  The width-th largest of the 64 lanes'
-// maxima of one wave bounds the width-th largest element from below; it takes
-// 32 steps of a compare and a count of the lanes, no memory.  The elements above
-// the bound (some four to eight times the width) go to a list in LDS; the same
-// count over the list finds the width-th largest of them, and what reaches it is
-// ranked within one wave by broadcasts of its registers.  (Ranking the whole list by
-// reads of LDS took 330 us for 256 rows of 131072 and width 32.)  If too many are
-// equal, they are ranked over the whole list, and if the list does not hold them,
-// taken one by one.
+// The largest elements of a part.  The width-th largest of the lanes' maxima of the
+// first step bounds the width-th largest element from below; it takes 20 steps of a
+// compare and a count of the lanes, no memory.  The elements above the bound go to a
+// list in LDS; where it fills, the same count over the list raises the bound.  In the
+// end what reaches the list's width-th largest is ranked by broadcasts of registers.
+// (Ranking a list by reads of LDS took 330 us for 256 rows of 131072 and width 32.)
+// If too many are equal for that, the elements are taken one by one, from memory.
 //
 // Precision.  Beams of different rows compete by sums that may be close: the
 // exponentials, with the rounding error of their arguments put back in, are added
@@ -137,14 +136,16 @@ struct Cand {
   }
 };
 
+constexpr int kPart = 256;  // entries of a wave's list
 struct Shared {
-  uint32_t wmax[kWaves], bound[kWaves];
-  double wsum[kWaves];
+  uint32_t bound[kWaves];
   int n, last, picked;
   int pick[kWave];
-  uint64_t best[kWaves];
   union {
-    uint64_t list[kList];
+    struct {
+      uint64_t list[kPart];
+      int pick[kWave];
+    } part[kWaves];
     struct {
       double lse[kMaxBeams], score[kMaxBeams], norm[kMaxBeams];
       int state[kMaxBeams];  // 0: no continuation, 1: its logits', 2: its eos
@@ -154,6 +155,12 @@ struct Shared {
     } f;
   };
 };
+
+// What a wave has written to LDS, its lanes may read.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 __device__ __forceinline__ void put(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -346,63 +353,87 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
   }
 }
 
+// A part's `width` largest, taken one by one from memory.
+template <typename T>
+__device__ void one_by_one(const T* x, int64_t from, int64_t to, int W, uint64_t* out) {
+  const int lane = threadIdx.x % kWave;
+  uint64_t limit = ~0ull;
+  for (int k = 0; k < W; ++k) {
+    uint64_t c = 0;
+#pragma unroll 8
+    for (int64_t i = from + lane; i < to; i += kWave) {
+      const float v = fminf(fmaxf((float)*gptr(x + i), -INFINITY), 3.402823466e38f) + 0.0f;
+      const uint64_t y = (uint64_t)key_of(v) << 32 | (uint32_t)~(uint32_t)i;
+      if (y < limit && y > c) c = y;
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+      const uint64_t y = (uint64_t)__shfl_xor((unsigned long long)c, o, kWave);
+      c = y > c ? y : c;
+    }
+    if (lane == 0) put(out + k, c);
+    limit = c;
+  }
+}
+
 template <typename T, int E>
-__global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws, int chunks) {
+__global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws, int chunks, int steps) {
   constexpr int kN = 16 / sizeof(T), kPieces = E / kN;
-  // Which thread takes an element depends on its place in the row alone, so that
+  // Which lane takes an element depends on its place in the row alone, so that
   // equal rows give equal sums: loads are of 16 bytes wherever the row starts.
   typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
   __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, W = a.width;
-  const int row = blockIdx.y, chunk = blockIdx.x, req = row / W;
+  const int tid = threadIdx.x, lane = tid % kWave, W = a.width;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int row = blockIdx.y, chunk = (int)blockIdx.x * kWaves + wave, req = row / W;
   const T* x = (const T*)a.logits + row * a.ldl;
-  float v[E];
-  auto load = [&] {
+  const int64_t step = (int64_t)kWave * E, from = chunk * steps * step;
+  const int64_t to = from + steps * step < a.vocab ? from + steps * step : a.vocab;
+  V raw[kPieces];
+  auto load = [&](int64_t at) {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-      const int64_t i0 = ((int64_t)(chunk * kPieces + p) * kThreads + tid) * kN;
+      const int64_t i0 = at + (p * kWave + lane) * kN;
       if (i0 + kN <= a.vocab) {
-        const V w = *(const __attribute__((address_space(1))) V*)(x + i0);
-#pragma unroll
-        for (int c = 0; c < kN; ++c) v[p * kN + c] = (float)w[c];
+        raw[p] = *(const __attribute__((address_space(1))) V*)(x + i0);
       } else {
 #pragma unroll
-        for (int c = 0; c < kN; ++c)
-          v[p * kN + c] = i0 + c < a.vocab ? (float)*gptr(x + i0 + c) : -INFINITY;
+        for (int c = 0; c < kN; ++c) raw[p][c] = i0 + c < a.vocab ? *gptr(x + i0 + c) : (T)-INFINITY;
       }
     }
   };
   // few rows: the logits come while the row's state is looked up; else rows without
   // continuations of their own are not read
   constexpr bool kEarly = E <= 8;
-  if constexpr (kEarly) load();
+  if (kEarly && from < to) load(from);
   if (state_of(a, row) == 1) {
-    if constexpr (!kEarly) load();
-    float big = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      // NaN counts as no continuation (a maximum passes over it), infinity as the
-      // largest number
-      v[e] = fminf(fmaxf(v[e], -INFINITY), 3.402823466e38f);
-      big = fmaxf(big, v[e]);
-    }
-    const uint32_t best = key_of(big + 0.0f);
-    const uint32_t wm = wave_max(best), wb = nth_largest<kLow>(best, W);
-    if (lane == 0) {
-      sh.wmax[wave] = wm;
-      sh.bound[wave] = wb;
-    }
-    if (tid == 0) sh.n = 0;
-    __syncthreads();
-    uint32_t top = 0, least = kNone + 1;
-    for (int w = 0; w < kWaves; ++w) {
-      top = max(top, sh.wmax[w]);
-      least = max(least, sh.bound[w]);
-    }
-    // as numbers: the least one of a list is the lowest finite float
-    const float m = value_of(top), bound = value_of(least);
+    if (!kEarly && from < to) load(from);
+    uint64_t* list = sh.part[wave].list;
+    uint64_t* out = ws.cand + ((int64_t)row * chunks + chunk) * W;
+    float bound = -3.402823466e38f, ref = -INFINITY;  // the bound; what exponentials are relative to
     double sum = 0.0;
-    if (top > kNone) {
+    int n = 0;
+    bool full = false, first = true;
+#pragma unroll 1
+    for (int64_t at = from; at < to; at += step) {
+      float v[E], big = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        // NaN counts as no continuation (a maximum passes over it), infinity as the
+        // largest number
+        v[e] = fminf(fmaxf((float)raw[e / kN][e % kN], -INFINITY), 3.402823466e38f);
+        big = fmaxf(big, v[e]);
+      }
+      if (at + step < to) load(at + step);
+      if (__ballot(big > ref + 40.0f) != 0) {
+        const float m = value_of(wave_max(key_of(big)));
+        if (ref > -INFINITY) sum *= exp((double)ref - (double)m);
+        ref = m;
+      }
+      if (ref == -INFINITY) continue;
+      if (first) {
+        bound = fmaxf(bound, value_of(max(nth_largest<kLow>(key_of(big), W), kNone + 1)));
+        first = false;
+      }
       constexpr double kLn2 = 0.69314718055994530942;
       constexpr float kHi = (float)(1.0 / kLn2), kLo = (float)((1.0 / kLn2 - (double)kHi) * kLn2);
 #pragma unroll
@@ -410,7 +441,7 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
         float y[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float d = fmaxf(v[e + i] - m, -1000.0f);
+          const float d = fmaxf(v[e + i] - ref, -1000.0f);
           const float t = d * kHi;
           // what the product's rounding lost, and the rest of 1 / ln 2, as a factor
           const float lost = __builtin_fmaf(d, kLo, __builtin_fmaf(d, kHi, -t) * (float)kLn2);
@@ -419,87 +450,84 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
         }
         sum += (double)(y[0] + y[1]);
       }
-    }
-    sum = wave_sum(sum);
-    if (lane == 0) sh.wsum[wave] = sum;
-    // what may be among the largest
-    auto elem_of = [&](int e) {
-      const int64_t i = ((int64_t)(chunk * kPieces + e / kN) * kThreads + tid) * kN + e % kN;
-      return (uint64_t)key_of(v[e] + 0.0f) << 32 | (uint32_t)~(uint32_t)i;  // zeros of either sign are equal
-    };
-    int mine = 0;
+      // what may be among the largest
+      auto hits_of = [&] {
+        int c = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) mine += __popcll(__ballot(v[e] >= bound));
-    int at = 0;
-    if (lane == 0) at = atomicAdd(&sh.n, mine);
-    at = __builtin_amdgcn_readfirstlane(at);
-    if (at + mine <= kList) {
+        for (int e = 0; e < E; ++e) c += __popcll(__ballot(v[e] >= bound));
+        return c;
+      };
+      int mine = full ? 0 : hits_of();
+      if (n + mine > kPart) {
+        // only what reaches the list's own width-th largest
+        auto hi = [&](int i) { return (uint32_t)(list[i] >> 32); };
+        const uint32_t t = nth_of<kLow, kPart / kWave>(n, W, hi);
+        uint64_t keep[kPart / kWave];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint64_t hits = __ballot(v[e] >= bound);
-        if (v[e] >= bound) sh.list[at + __popcll(hits & ((1ull << lane) - 1))] = elem_of(e);
-        at += __popcll(hits);
-      }
-    }
-    __syncthreads();
-    const int n = sh.n;
-    uint64_t* out = ws.cand + ((int64_t)row * chunks + chunk) * W;
-    if (n <= kList) {
-      if (wave == 0) {
-        auto hi = [&](int i) { return (uint32_t)(sh.list[i] >> 32); };
-        const int m = gather(n, nth_of_list<kLow>(n, W, hi), hi, sh.pick);
-        if (lane == 0) sh.picked = m;
-      }
-      __syncthreads();
-      const int m = sh.picked;
-      if (m > kWave) {
-        for (int i = tid; i < n; i += kThreads) {
-          const uint64_t k = sh.list[i];
-          int rank = 0;
-          for (int j = 0; j < n; ++j) rank += sh.list[j] > k;
-          if (rank < W) put(out + rank, k);
+        for (int j = 0; j < kPart / kWave; ++j) keep[j] = lane + j * kWave < n ? list[lane + j * kWave] : 0;
+        int m = 0;
+#pragma unroll
+        for (int j = 0; j < kPart / kWave; ++j) {
+          const bool hit = keep[j] != 0 && (uint32_t)(keep[j] >> 32) >= t;
+          const uint64_t mask = __ballot(hit);
+          if (hit) list[m + __popcll(mask & ((1ull << lane) - 1))] = keep[j];
+          m += __popcll(mask);
         }
-      } else if (wave == 0) {
-        const uint64_t k = sh.list[lane < m ? sh.pick[lane] : 0];
-        int rank = 0;
-        for (int j = 0; j < m; ++j) rank += lane_of(k, j) > k;
-        if (lane < m && rank < W) put(out + rank, k);
+        wave_sync();
+        n = m;
+        bound = fmaxf(bound, value_of(max(t, kNone + 1)));
+        mine = hits_of();
+        full = n + mine > kPart;
       }
-      for (int i = n + tid; i < W; i += kThreads) put(out + i, 0);
-    } else {
-      uint64_t limit = ~0ull;
-      for (int k = 0; k < W; ++k) {
-        uint64_t c = 0;
+      if (!full && mine > 0) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const uint64_t y = elem_of(e);
-          if (y < limit && y > c) c = y;
+          const uint64_t hits = __ballot(v[e] >= bound);
+          if (hits != 0) {
+            const uint32_t i = (uint32_t)(at + ((e / kN) * kWave + lane) * kN + e % kN);
+            // zeros of either sign are equal
+            if (v[e] >= bound) list[n + __popcll(hits & ((1ull << lane) - 1))] = (uint64_t)key_of(v[e] + 0.0f) << 32 | ~i;
+            n += __popcll(hits);
+          }
         }
-        for (int o = 32; o > 0; o >>= 1) {
-          const uint64_t y = (uint64_t)__shfl_xor((unsigned long long)c, o, kWave);
-          c = y > c ? y : c;
-        }
-        __syncthreads();
-        if (lane == 0) sh.best[wave] = c;
-        __syncthreads();
-        for (int w = 0; w < kWaves; ++w) c = sh.best[w] > c ? sh.best[w] : c;
-        if (tid == 0) put(out + k, c);
-        limit = c;
+        wave_sync();
       }
     }
-    if (tid == 0) {
-      double s = 0.0;
-      for (int w = 0; w < kWaves; ++w) s += sh.wsum[w];
+    sum = wave_sum(sum);
+    auto hi = [&](int i) { return (uint32_t)(list[i] >> 32); };
+    int m = 0;
+    if (!full) {
+      m = gather(n, n <= kWave ? 0 : nth_of<kLow, kPart / kWave>(n, W, hi), hi, sh.part[wave].pick);
+      wave_sync();
+    }
+    if (full) {
+      one_by_one(x, from, to, W, out);
+    } else if (m > kWave) {
+      for (int i = lane; i < n; i += kWave) {
+        const uint64_t k = list[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += list[j] > k;
+        if (rank < W) put(out + rank, k);
+      }
+    } else {
+      const uint64_t k = list[lane < m ? sh.part[wave].pick[lane] : 0];
+      int rank = 0;
+      for (int j = 0; j < m; ++j) rank += lane_of(k, j) > k;
+      if (lane < m && rank < W) put(out + rank, k);
+      if (lane >= m && lane < W) put(out + lane, 0);
+    }
+    if (lane == 0) {
       uint64_t* p = ws.part + ((int64_t)row * chunks + chunk) * 2;
-      put(p, top);
-      put(p + 1, (uint64_t)__double_as_longlong(s));
+      put(p, key_of(ref));
+      put(p + 1, (uint64_t)__double_as_longlong(sum));
     }
   }
   // the stores have completed before this workgroup counts as done
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (tid == 0) {
-    const uint32_t all = (uint32_t)(W * chunks);
+    const uint32_t all = (uint32_t)(W * (chunks / kWaves));
     sh.last = __hip_atomic_fetch_add(ws.count + req, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == all - 1;
     if (sh.last) __hip_atomic_store(ws.count + req, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -507,51 +535,62 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
   if (sh.last) choose(a, ws, sh, req, chunks);
 }
 
-// Elements a thread: 32 where that still fills the device, else 8.
+// How a call is cut: 32 elements a lane and step where that still gives every CU a
+// wave, else 8; steps of a part as many as leave four waves to a SIMD.  Parts of a
+// row, a multiple of the waves of a workgroup.
 constexpr int kMany = 32, kFew = 8;
-int64_t chunks_of(int32_t vocab, int32_t dtype, int e) {
-  const int64_t n = dtype == DFS_F16 ? 8 : 4;
-  const int64_t pieces = (vocab + n - 1) / n;
-  const int64_t per = (int64_t)kThreads * (e / n);
-  return (pieces + per - 1) / per;
+struct Cut {
+  int e, steps;
+  int64_t chunks;
+};
+int64_t chunks_of(int32_t vocab, int e, int steps) {
+  const int64_t per = (int64_t)kWave * e * steps * kWaves;
+  return (vocab + per - 1) / per * kWaves;
 }
-int elements(int64_t rows, int32_t vocab, int32_t dtype) {
-  return rows * chunks_of(vocab, dtype, kMany) >= 256 ? kMany : kFew;
+Cut get_cut(int64_t rows, int32_t vocab) {
+  Cut c;
+  c.e = rows * chunks_of(vocab, kMany, 1) >= 256 ? kMany : kFew;
+  c.steps = (int)std::max<int64_t>(1, rows * vocab / ((int64_t)kWave * kMany * 4096));
+  if (c.e == kFew) c.steps = 1;
+  c.chunks = chunks_of(vocab, c.e, c.steps);
+  return c;
 }
-size_t layout(int64_t rows, int64_t chunks, int32_t width, size_t* cand) {
-  *cand = kCounterBytes + (size_t)rows * chunks * 16;
-  return *cand + (size_t)rows * chunks * width * 8;
+size_t layout(int64_t parts, int32_t width, size_t* cand) {
+  *cand = kCounterBytes + (size_t)parts * 16;
+  return *cand + (size_t)parts * width * 8;
 }
 
 }  // namespace
 
-size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab, int32_t dtype) {
+size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab) {
   const int64_t rows = (int64_t)n_req * width;
   size_t cand;
-  return layout(rows, chunks_of(vocab, dtype, elements(rows, vocab, dtype)), width, &cand);
+  return layout(rows * get_cut(rows, vocab).chunks, width, &cand);
 }
-// Of any smaller call: one with few rows takes small pieces.
+// Of any smaller call: the small steps of one with few rows make at most four times
+// as many parts as the 255 that large ones would, and rounding adds at most 3 a row.
 size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab) {
   const int64_t rows = (int64_t)n_req * width;
   size_t cand;
-  return layout(rows, chunks_of(vocab, DFS_F32, kFew), width, &cand);
+  return layout(std::max(rows * chunks_of(vocab, kMany, 1), std::min<int64_t>(rows * chunks_of(vocab, kFew, 1), 7 * 256)),
+                width, &cand);
 }
 
 hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s) {
   const int64_t rows = (int64_t)a.n_req * a.width;
-  const int e = elements(rows, a.vocab, a.dtype);
-  const int chunks = (int)chunks_of(a.vocab, a.dtype, e);
+  const Cut c = get_cut(rows, a.vocab);
   size_t cand;
-  layout(rows, chunks, a.width, &cand);
+  layout(rows * c.chunks, a.width, &cand);
   const BeamWs w = {(uint32_t*)ws, (uint64_t*)((char*)ws + kCounterBytes), (uint64_t*)((char*)ws + cand)};
   auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(chunks, (unsigned)rows), dim3(kThreads), 0, s, a, w, chunks);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(c.chunks / kWaves), (unsigned)rows), dim3(kThreads), 0, s, a, w,
+                       (int)c.chunks, c.steps);
   };
   if (a.dtype == DFS_F16) {
-    if (e == kMany) run(beam_kernel<_Float16, kMany>);
+    if (c.e == kMany) run(beam_kernel<_Float16, kMany>);
     else run(beam_kernel<_Float16, kFew>);
   } else {
-    if (e == kMany) run(beam_kernel<float, kMany>);
+    if (c.e == kMany) run(beam_kernel<float, kMany>);
     else run(beam_kernel<float, kFew>);
   }
   return hipGetLastError();

@@ -369,7 +369,7 @@ struct BeamLaunch {
   float* score_out;
   int32_t* done_out;  // may be null
 };
-size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab, int32_t dtype);
+size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab);
 size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab);
 hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s);
 
