@@ -37,7 +37,7 @@ constexpr uint32_t kNone = 0x007FFFFFu;  // key of -inf: no continuation
 
 struct BeamWs {
   uint32_t* count;  // [n_req]: workgroups that are done
-  uint64_t* part;   // [rows][chunks]: key of the largest logit, sum of the exponentials
+  uint64_t* part;   // [rows][chunks][waves]: key of the reference, sum of the exponentials
   uint64_t* cand;   // [rows][chunks][width]: key of a logit, complement of its token
 };
 
@@ -140,11 +140,11 @@ constexpr int kPart = 256;  // entries of a wave's list
 struct Shared {
   uint32_t bound[kWaves];
   int n, last, picked;
-  int pick[kWave];
+  int pick[kWave], rank[kWaves][kWave];
   union {
     struct {
-      uint64_t list[kPart];
-      int pick[kWave];
+      uint64_t list[kPart], best[kMaxBeams];
+      int many, pick[kWave];
     } part[kWaves];
     struct {
       double lse[kMaxBeams], score[kMaxBeams], norm[kMaxBeams];
@@ -169,13 +169,18 @@ __device__ __forceinline__ uint64_t get(const uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Whether a row offers continuations, and which.
-__device__ __forceinline__ int state_of(const BeamLaunch& a, int row) {
-  const float sc = *gptr(a.score + row);
-  const float nm = a.norm ? *gptr(a.norm + row) : 1.0f;
-  if (!(sc > -INFINITY && sc < INFINITY) || !(nm > 0.0f && nm < INFINITY)) return 0;
-  return a.done && *gptr(a.done + row) != 0 ? 2 : 1;
-}
+// Whether a row offers continuations, and which: its three facts are read at once.
+struct RowFacts {
+  float score, norm;
+  int done;
+  __device__ __forceinline__ RowFacts(const BeamLaunch& a, int64_t row)
+      : score(*gptr(a.score + row)), norm(a.norm ? *gptr(a.norm + row) : 1.0f),
+        done(a.done ? *gptr(a.done + row) : 0) {}
+  __device__ __forceinline__ int state() const {
+    const bool fine = score > -INFINITY && score < INFINITY && norm > 0.0f && norm < INFINITY;
+    return !fine ? 0 : done != 0 ? 2 : 1;
+  }
+};
 
 // Adds a piece's sum (in units of its largest exponential) to another.
 __device__ __forceinline__ void join_sums(uint32_t& top, double& sum, uint32_t k, double s) {
@@ -207,16 +212,20 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
   while (lanes * W > kThreads) lanes /= 2;
   const int w = tid / lanes, sub = tid % lanes;
   if (w < W) {
-    const int st = state_of(a, (int)(row0 + w));
+    const RowFacts f(a, row0 + w);
+    const int parts = chunks * kWaves;
+    const uint64_t* p = ws.part + (row0 + w) * parts * 2;
+    uint32_t k = (uint32_t)get(p + 2 * min(sub, parts - 1));
+    double s = __longlong_as_double((int64_t)get(p + 2 * min(sub, parts - 1) + 1));
+    const int st = f.state();
     uint32_t top = 0;
     double sum = 0.0;
-    if (st == 1) {
-      const uint64_t* p = ws.part + (row0 + w) * chunks * 2;
-      for (int c = sub; c < chunks; c += lanes) {
-        const uint32_t k = (uint32_t)get(p + 2 * c);
-        const double s = __longlong_as_double((int64_t)get(p + 2 * c + 1));
-        join_sums(top, sum, k, s);
+    for (int c = sub; st == 1 && c < parts; c += lanes) {
+      if (c != sub) {
+        k = (uint32_t)get(p + 2 * c);
+        s = __longlong_as_double((int64_t)get(p + 2 * c + 1));
       }
+      join_sums(top, sum, k, s);
     }
     uint32_t best = top;
     for (int o = lanes / 2; o > 0; o >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, o, kWave));
@@ -225,8 +234,8 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
     top = best;
     if (sub == 0) {
       sh.f.lse[w] = top > kNone ? (double)value_of(top) + log(sum) : 0.0;
-      sh.f.score[w] = a.score[row0 + w];
-      sh.f.norm[w] = a.norm ? a.norm[row0 + w] : 1.0f;
+      sh.f.score[w] = f.score;
+      sh.f.norm[w] = f.norm;
       sh.f.state[w] = st;
     }
   }
@@ -252,16 +261,38 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
     const int w = i / per_row;
     return cand_of(w, sh.f.state[w] == 1 ? get(cands + i) : 0, i == w * per_row);
   };
-  // A piece's candidates descend: the width-th largest of the threads' first ones
-  // bounds those to look at.
+  // A piece's candidates descend: the width-th largest of the first ones of a wave's
+  // pieces bounds those to look at; of the first eight, where the pieces are few.
   const int lists = W * chunks;
-  uint32_t mine = 0;
-  for (int j = tid; j < lists; j += kThreads) {
-    const int w = j / chunks;
-    mine = max(mine, (uint32_t)(cand_of(w, j == tid ? x[0] : get(cands + j * W), j == w * chunks).key >> 32));
+  uint32_t best = 0;
+  for (int j0 = 0; j0 < lists; j0 += kThreads) {
+    const int j = j0 + tid, w = min(j / chunks, W - 1);
+    if (j0 > 0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) x[k] = get(cands + min(j, lists - 1) * W + min(k, W - 1));
+    }
+    auto key = [&](int k) {
+      return j < lists && k < W ? (uint32_t)(cand_of(w, x[k], k == 0 && j == w * chunks).key >> 32) : 0;
+    };
+    const uint32_t first = key(0);
+    uint32_t t = nth_largest<kLow64>(first, W);
+    const int live = __popcll(__ballot(first != 0));
+    if (live < W && live * kAhead >= W) {
+      uint32_t keys[kAhead] = {first};
+#pragma unroll
+      for (int k = 1; k < kAhead; ++k) keys[k] = key(k);
+#pragma unroll 1
+      for (int b = 31; b >= kLow64; --b) {
+        const uint32_t u = t | 1u << b;
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) c += __popcll(__ballot(keys[k] >= u));
+        if (c >= W) t = u;
+      }
+    }
+    best = max(best, t);
   }
-  const uint32_t b = nth_largest<kLow64>(mine, W);
-  if (lane == 0) sh.bound[wave] = b;
+  if (lane == 0) sh.bound[wave] = best;
   __syncthreads();
   uint32_t bound = 0;
   for (int v = 0; v < kWaves; ++v) bound = max(bound, sh.bound[v]);
@@ -269,7 +300,7 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
     const int w = j / chunks;
     bool more = true;
     for (int k0 = 0; k0 < W && more; k0 += kAhead) {
-      if (k0 > 0 || j != tid) {
+      if (k0 > 0 || lists > kThreads) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) x[k] = get(cands + j * W + min(k0 + k, W - 1));
       }
@@ -315,11 +346,17 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
         for (int j = 0; j < n; ++j) rank += listed(j).above(c);
         if (rank < W) write(rank, c);
       }
-    } else if (wave == 0) {
+    } else {  // each wave counts a quarter of those above
       const Cand c = listed(lane < m ? sh.pick[lane] : 0);
       int rank = 0;
-      for (int j = 0; j < m; ++j) rank += Cand{lane_of(c.key, j), lane_of(c.elem, j), lane_of(c.row, j)}.above(c);
-      if (lane < m && rank < W) write(rank, c);
+      for (int j = wave; j < m; j += kWaves)
+        rank += Cand{lane_of(c.key, j), lane_of(c.elem, j), lane_of(c.row, j)}.above(c);
+      sh.rank[wave][lane] = rank;
+      __syncthreads();
+      if (wave == 0) {
+        for (int v = 1; v < kWaves; ++v) rank += sh.rank[v][lane];
+        if (lane < m && rank < W) write(rank, c);
+      }
     }
   } else {
     // more than the list holds reach the bound: one after the other
@@ -370,7 +407,7 @@ __device__ void one_by_one(const T* x, int64_t from, int64_t to, int W, uint64_t
       const uint64_t y = (uint64_t)__shfl_xor((unsigned long long)c, o, kWave);
       c = y > c ? y : c;
     }
-    if (lane == 0) put(out + k, c);
+    if (lane == 0) out[k] = c;
     limit = c;
   }
 }
@@ -384,9 +421,9 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid % kWave, W = a.width;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int row = blockIdx.y, chunk = (int)blockIdx.x * kWaves + wave, req = row / W;
+  const int row = blockIdx.y, chunk = (int)blockIdx.x, req = row / W;
   const T* x = (const T*)a.logits + row * a.ldl;
-  const int64_t step = (int64_t)kWave * E, from = chunk * steps * step;
+  const int64_t step = (int64_t)kWave * E, from = ((int64_t)chunk * kWaves + wave) * steps * step;
   const int64_t to = from + steps * step < a.vocab ? from + steps * step : a.vocab;
   V raw[kPieces];
   auto load = [&](int64_t at) {
@@ -405,23 +442,30 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
   // continuations of their own are not read
   constexpr bool kEarly = E <= 8;
   if (kEarly && from < to) load(from);
-  if (state_of(a, row) == 1) {
+  if (RowFacts(a, row).state() == 1) {
     if (!kEarly && from < to) load(from);
     uint64_t* list = sh.part[wave].list;
-    uint64_t* out = ws.cand + ((int64_t)row * chunks + chunk) * W;
+    uint64_t* best = sh.part[wave].best;  // the part's largest, in order
     float bound = -3.402823466e38f, ref = -INFINITY;  // the bound; what exponentials are relative to
     double sum = 0.0;
     int n = 0;
     bool full = false, first = true;
 #pragma unroll 1
     for (int64_t at = from; at < to; at += step) {
+      // NaN counts as no continuation (a maximum passes over it), infinity as the
+      // largest number
       float v[E], big = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        // NaN counts as no continuation (a maximum passes over it), infinity as the
-        // largest number
-        v[e] = fminf(fmaxf((float)raw[e / kN][e % kN], -INFINITY), 3.402823466e38f);
-        big = fmaxf(big, v[e]);
+      for (int p = 0; p < kPieces; ++p) {
+        V w = __builtin_elementwise_max(raw[p], (V)((T)-INFINITY));
+        if constexpr (sizeof(T) == 4) w = __builtin_elementwise_min(w, (V)((T)3.402823466e38f));
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          float y = (float)w[c];
+          if constexpr (sizeof(T) == 2) y = fminf(y, 3.402823466e38f);
+          v[p * kN + c] = y;
+          big = fmaxf(big, y);
+        }
       }
       if (at + step < to) load(at + step);
       if (__ballot(big > ref + 40.0f) != 0) {
@@ -451,46 +495,43 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
         sum += (double)(y[0] + y[1]);
       }
       // what may be among the largest
-      auto hits_of = [&] {
-        int c = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) c += __popcll(__ballot(v[e] >= bound));
-        return c;
-      };
-      int mine = full ? 0 : hits_of();
-      if (n + mine > kPart) {
-        // only what reaches the list's own width-th largest
-        auto hi = [&](int i) { return (uint32_t)(list[i] >> 32); };
-        const uint32_t t = nth_of<kLow, kPart / kWave>(n, W, hi);
-        uint64_t keep[kPart / kWave];
-#pragma unroll
-        for (int j = 0; j < kPart / kWave; ++j) keep[j] = lane + j * kWave < n ? list[lane + j * kWave] : 0;
-        int m = 0;
-#pragma unroll
-        for (int j = 0; j < kPart / kWave; ++j) {
-          const bool hit = keep[j] != 0 && (uint32_t)(keep[j] >> 32) >= t;
-          const uint64_t mask = __ballot(hit);
-          if (hit) list[m + __popcll(mask & ((1ull << lane) - 1))] = keep[j];
-          m += __popcll(mask);
-        }
-        wave_sync();
-        n = m;
-        bound = fmaxf(bound, value_of(max(t, kNone + 1)));
-        mine = hits_of();
-        full = n + mine > kPart;
-      }
-      if (!full && mine > 0) {
+      if (full) continue;
+      auto add = [&](int c) {  // as far as the list goes; how many it would hold
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const uint64_t hits = __ballot(v[e] >= bound);
           if (hits != 0) {
             const uint32_t i = (uint32_t)(at + ((e / kN) * kWave + lane) * kN + e % kN);
+            const int to = c + __popcll(hits & ((1ull << lane) - 1));
             // zeros of either sign are equal
-            if (v[e] >= bound) list[n + __popcll(hits & ((1ull << lane) - 1))] = (uint64_t)key_of(v[e] + 0.0f) << 32 | ~i;
-            n += __popcll(hits);
+            if (v[e] >= bound && to < kPart) list[to] = (uint64_t)key_of(v[e] + 0.0f) << 32 | ~i;
+            c += __popcll(hits);
           }
         }
         wave_sync();
+        return c;
+      };
+      const int was = n;
+      n = add(was);
+      if (n > kPart) {
+        // of those before, only what reaches their own width-th largest; then once more
+        auto hi = [&](int i) { return (uint32_t)(list[i] >> 32); };
+        const uint32_t t = nth_of<kLow, kPart / kWave>(was, W, hi);
+        uint64_t keep[kPart / kWave];
+#pragma unroll
+        for (int j = 0; j < kPart / kWave; ++j) keep[j] = lane + j * kWave < was ? list[lane + j * kWave] : 0;
+        n = 0;
+#pragma unroll
+        for (int j = 0; j < kPart / kWave; ++j) {
+          const bool hit = keep[j] != 0 && (uint32_t)(keep[j] >> 32) >= t;
+          const uint64_t mask = __ballot(hit);
+          if (hit) list[n + __popcll(mask & ((1ull << lane) - 1))] = keep[j];
+          n += __popcll(mask);
+        }
+        wave_sync();
+        bound = fmaxf(bound, value_of(max(t, kNone + 1)));
+        n = add(n);
+        full = n > kPart;
       }
     }
     sum = wave_sum(sum);
@@ -500,34 +541,60 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
       m = gather(n, n <= kWave ? 0 : nth_of<kLow, kPart / kWave>(n, W, hi), hi, sh.part[wave].pick);
       wave_sync();
     }
+    if (lane < W) best[lane] = 0;
+    wave_sync();
     if (full) {
-      one_by_one(x, from, to, W, out);
+      one_by_one(x, from, to, W, best);
     } else if (m > kWave) {
       for (int i = lane; i < n; i += kWave) {
         const uint64_t k = list[i];
         int rank = 0;
 #pragma unroll 8
         for (int j = 0; j < n; ++j) rank += list[j] > k;
-        if (rank < W) put(out + rank, k);
+        if (rank < W) best[rank] = k;
       }
     } else {
       const uint64_t k = list[lane < m ? sh.part[wave].pick[lane] : 0];
       int rank = 0;
       for (int j = 0; j < m; ++j) rank += lane_of(k, j) > k;
-      if (lane < m && rank < W) put(out + rank, k);
-      if (lane >= m && lane < W) put(out + lane, 0);
+      if (lane < m && rank < W) best[rank] = k;
     }
     if (lane == 0) {
-      uint64_t* p = ws.part + ((int64_t)row * chunks + chunk) * 2;
+      sh.part[wave].many = full ? W : min(n, W);
+      uint64_t* p = ws.part + (((int64_t)row * chunks + chunk) * kWaves + wave) * 2;
       put(p, key_of(ref));
       put(p + 1, (uint64_t)__double_as_longlong(sum));
+    }
+    __syncthreads();
+    // the waves' parts together: an element's rank is its own in its part and how many
+    // of each other part are above it
+    uint64_t* out = ws.cand + ((int64_t)row * chunks + chunk) * W;
+    if (tid < kWaves * W) {
+      const int own = tid / W, i = tid - own * W;
+      const uint64_t k = sh.part[own].best[i];
+      int rank = i;
+      for (int w = 0; w < kWaves; ++w) {
+        if (w == own) continue;
+        int lo = 0, hi = W;  // how many are above k
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (sh.part[w].best[mid] > k) lo = mid + 1;
+          else hi = mid;
+        }
+        rank += lo;
+      }
+      if (i < sh.part[own].many && rank < W) put(out + rank, k);
+    } else if (tid >= kThreads - kWave) {
+      int all = 0;
+      for (int w = 0; w < kWaves; ++w) all += sh.part[w].many;
+      for (int i = all + lane; i < W; i += kWave) put(out + i, 0);
     }
   }
   // the stores have completed before this workgroup counts as done
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (tid == 0) {
-    const uint32_t all = (uint32_t)(W * (chunks / kWaves));
+    const uint32_t all = (uint32_t)(W * chunks);
     sh.last = __hip_atomic_fetch_add(ws.count + req, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == all - 1;
     if (sh.last) __hip_atomic_store(ws.count + req, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -536,8 +603,8 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
 }
 
 // How a call is cut: 32 elements a lane and step where that still gives every CU a
-// wave, else 8; steps of a part as many as leave four waves to a SIMD.  Parts of a
-// row, a multiple of the waves of a workgroup.
+// wave, else 8; steps of a part as many as leave four waves to a SIMD.  A workgroup
+// takes four parts of a row.
 constexpr int kMany = 32, kFew = 8;
 struct Cut {
   int e, steps;
@@ -545,18 +612,18 @@ struct Cut {
 };
 int64_t chunks_of(int32_t vocab, int e, int steps) {
   const int64_t per = (int64_t)kWave * e * steps * kWaves;
-  return (vocab + per - 1) / per * kWaves;
+  return (vocab + per - 1) / per;
 }
 Cut get_cut(int64_t rows, int32_t vocab) {
   Cut c;
-  c.e = rows * chunks_of(vocab, kMany, 1) >= 256 ? kMany : kFew;
+  c.e = rows * chunks_of(vocab, kMany, 1) >= 64 ? kMany : kFew;
   c.steps = (int)std::max<int64_t>(1, rows * vocab / ((int64_t)kWave * kMany * 4096));
   if (c.e == kFew) c.steps = 1;
   c.chunks = chunks_of(vocab, c.e, c.steps);
   return c;
 }
 size_t layout(int64_t parts, int32_t width, size_t* cand) {
-  *cand = kCounterBytes + (size_t)parts * 16;
+  *cand = kCounterBytes + (size_t)parts * kWaves * 16;
   return *cand + (size_t)parts * width * 8;
 }
 
@@ -567,12 +634,12 @@ size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab) {
   size_t cand;
   return layout(rows * get_cut(rows, vocab).chunks, width, &cand);
 }
-// Of any smaller call: the small steps of one with few rows make at most four times
-// as many parts as the 255 that large ones would, and rounding adds at most 3 a row.
+// Of any smaller call: where few rows take small steps, these make at most four times
+// as many pieces as the 63 that large ones would.
 size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab) {
   const int64_t rows = (int64_t)n_req * width;
   size_t cand;
-  return layout(std::max(rows * chunks_of(vocab, kMany, 1), std::min<int64_t>(rows * chunks_of(vocab, kFew, 1), 7 * 256)),
+  return layout(std::max(rows * chunks_of(vocab, kMany, 1), std::min<int64_t>(rows * chunks_of(vocab, kFew, 1), 4 * 63)),
                 width, &cand);
 }
 
@@ -583,7 +650,7 @@ hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s) {
   layout(rows * c.chunks, a.width, &cand);
   const BeamWs w = {(uint32_t*)ws, (uint64_t*)((char*)ws + kCounterBytes), (uint64_t*)((char*)ws + cand)};
   auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(c.chunks / kWaves), (unsigned)rows), dim3(kThreads), 0, s, a, w,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)c.chunks, (unsigned)rows), dim3(kThreads), 0, s, a, w,
                        (int)c.chunks, c.steps);
   };
   if (a.dtype == DFS_F16) {
