@@ -1072,8 +1072,7 @@ dfs_status kv8_copy_pages(int32_t n_kv, const dfs_kv8* kv, int32_t n, const int3
 namespace {
 dfs_status check_beams(int32_t n_req, int32_t width, int32_t vocab) {
   if (n_req < 0 || width <= 0 || vocab <= 0) return DFS_E_INVALID;
-  if (width > kMaxBeams || n_req > kMaxBeamRequests || (int64_t)n_req * width > 65535 ||
-      vocab > 1 << 30)
+  if (width > kMaxBeams || (int64_t)n_req * width > kMaxBeamRows || vocab > 1 << 30)
     return DFS_E_RANGE;
   return DFS_OK;
 }
@@ -1104,7 +1103,7 @@ dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* 
   for (const void* out : {(const void*)parent, (const void*)token, (const void*)score_out, (const void*)done_out})
     for (const void* in : {(const void*)score, (const void*)done, (const void*)norm})
       if (overlap(out, rows, in, rows)) return DFS_E_INVALID;
-  DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab)));
+  DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab, dtype)));
   const BeamLaunch a = {n_req, width, vocab,  logits, dtype,     ldl,     score,
                         done,  norm,  eos,    parent, token,     score_out, done_out};
   DFS_HIP(launch_beam_select(a, ws, (hipStream_t)stream));

@@ -31,12 +31,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kList = 1024;
+constexpr int kList = 512;
 constexpr size_t kCounterBytes = 65536;
+static_assert(2 * kMaxBeamRows * 4 == kCounterBytes, "counters");
 constexpr uint32_t kNone = 0x007FFFFFu;  // key of -inf: no continuation
 
 struct BeamWs {
-  uint32_t* count;  // [n_req]: workgroups that are done
+  uint32_t* count;  // [kMaxBeamRows]: rows of each request that are done; then workgroups of each row
   uint64_t* part;   // [rows][chunks][waves]: key of the reference, sum of the exponentials
   uint64_t* cand;   // [rows][chunks][width]: key of a logit, complement of its token
 };
@@ -264,38 +265,42 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
   // A piece's candidates descend: the width-th largest of the first ones of a wave's
   // pieces bounds those to look at; of the first eight, where the pieces are few.
   const int lists = W * chunks;
-  uint32_t best = 0;
-  for (int j0 = 0; j0 < lists; j0 += kThreads) {
-    const int j = j0 + tid, w = min(j / chunks, W - 1);
-    if (j0 > 0) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) x[k] = get(cands + min(j, lists - 1) * W + min(k, W - 1));
-    }
-    auto key = [&](int k) {
-      return j < lists && k < W ? (uint32_t)(cand_of(w, x[k], k == 0 && j == w * chunks).key >> 32) : 0;
-    };
-    const uint32_t first = key(0);
-    uint32_t t = nth_largest<kLow64>(first, W);
-    const int live = __popcll(__ballot(first != 0));
-    if (live < W && live * kAhead >= W) {
-      uint32_t keys[kAhead] = {first};
-#pragma unroll
-      for (int k = 1; k < kAhead; ++k) keys[k] = key(k);
-#pragma unroll 1
-      for (int b = 31; b >= kLow64; --b) {
-        const uint32_t u = t | 1u << b;
-        int c = 0;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) c += __popcll(__ballot(keys[k] >= u));
-        if (c >= W) t = u;
-      }
-    }
-    best = max(best, t);
-  }
-  if (lane == 0) sh.bound[wave] = best;
-  __syncthreads();
   uint32_t bound = 0;
-  for (int v = 0; v < kWaves; ++v) bound = max(bound, sh.bound[v]);
+  for (int deep = 0; deep < 2 && bound == 0; ++deep) {
+    uint32_t best = 0;
+    for (int j0 = 0; j0 < lists; j0 += kThreads) {
+      const int j = j0 + tid, w = min(j / chunks, W - 1);
+      if (lists > kThreads) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = get(cands + min(j, lists - 1) * W + min(k, W - 1));
+      }
+      auto key = [&](int k) {
+        return j < lists && k < W ? (uint32_t)(cand_of(w, x[k], k == 0 && j == w * chunks).key >> 32) : 0;
+      };
+      uint32_t t = 0;
+      if (deep == 0) {
+        t = nth_largest<kLow64>(key(0), W);
+      } else {
+        uint32_t keys[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) keys[k] = key(k);
+#pragma unroll 1
+        for (int b = 31; b >= kLow64; --b) {
+          const uint32_t u = t | 1u << b;
+          int c = 0;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) c += __popcll(__ballot(keys[k] >= u));
+          if (c >= W) t = u;
+        }
+      }
+      best = max(best, t);
+    }
+    if (deep) __syncthreads();  // the first round's bounds have been read
+    if (lane == 0) sh.bound[wave] = best;
+    __syncthreads();
+    for (int v = 0; v < kWaves; ++v) bound = max(bound, sh.bound[v]);
+    if (lists * W <= kList / 4) break;  // few enough to look at them all
+  }
   for (int j = tid; j < lists; j += kThreads) {
     const int w = j / chunks;
     bool more = true;
@@ -594,31 +599,39 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (tid == 0) {
-    const uint32_t all = (uint32_t)(W * chunks);
-    sh.last = __hip_atomic_fetch_add(ws.count + req, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == all - 1;
-    if (sh.last) __hip_atomic_store(ws.count + req, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // first the row's counter, then its last one the request's: the arrivals at one
+    // address follow each other at some 0.1 us (24 requests of 5 beams 30 us with one
+    // counter a request, 22 so)
+    auto last_of = [](uint32_t* count, uint32_t n) {
+      if (__hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != n - 1) return false;
+      __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      return true;
+    };
+    sh.last = last_of(ws.count + kMaxBeamRows + row, (uint32_t)chunks) && last_of(ws.count + req, (uint32_t)W);
   }
   __syncthreads();
   if (sh.last) choose(a, ws, sh, req, chunks);
 }
 
-// How a call is cut: 32 elements a lane and step where that still gives every CU a
-// wave, else 8; steps of a part as many as leave four waves to a SIMD.  A workgroup
-// takes four parts of a row.
-constexpr int kMany = 32, kFew = 8;
+// How a call is cut: 64 bytes a lane and step (32 f16 elements, 16 fp32 ones; with 32
+// fp32 ones, 137 registers and 24 us for 24 requests of 5 beams) where that still gives
+// every CU a wave, else 8 elements; steps of a part as many as leave four waves to a
+// SIMD.  A workgroup takes four parts of a row.
+constexpr int kBytes = 64, kFew = 8;
 struct Cut {
   int e, steps;
   int64_t chunks;
 };
+int many_of(int32_t dtype) { return kBytes / (dtype == DFS_F16 ? 2 : 4); }
 int64_t chunks_of(int32_t vocab, int e, int steps) {
   const int64_t per = (int64_t)kWave * e * steps * kWaves;
   return (vocab + per - 1) / per;
 }
-Cut get_cut(int64_t rows, int32_t vocab) {
+Cut get_cut(int64_t rows, int32_t vocab, int32_t dtype) {
   Cut c;
-  c.e = rows * chunks_of(vocab, kMany, 1) >= 64 ? kMany : kFew;
-  c.steps = (int)std::max<int64_t>(1, rows * vocab / ((int64_t)kWave * kMany * 4096));
-  if (c.e == kFew) c.steps = 1;
+  const int many = many_of(dtype);
+  c.e = rows * chunks_of(vocab, many, 1) >= 64 ? many : kFew;
+  c.steps = c.e == kFew ? 1 : (int)std::max<int64_t>(1, rows * vocab / ((int64_t)kWave * many * 4096));
   c.chunks = chunks_of(vocab, c.e, c.steps);
   return c;
 }
@@ -629,23 +642,23 @@ size_t layout(int64_t parts, int32_t width, size_t* cand) {
 
 }  // namespace
 
-size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab) {
+size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab, int32_t dtype) {
   const int64_t rows = (int64_t)n_req * width;
   size_t cand;
-  return layout(rows * get_cut(rows, vocab).chunks, width, &cand);
+  return layout(rows * get_cut(rows, vocab, dtype).chunks, width, &cand);
 }
 // Of any smaller call: where few rows take small steps, these make at most four times
 // as many pieces as the 63 that large ones would.
 size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab) {
   const int64_t rows = (int64_t)n_req * width;
   size_t cand;
-  return layout(std::max(rows * chunks_of(vocab, kMany, 1), std::min<int64_t>(rows * chunks_of(vocab, kFew, 1), 4 * 63)),
+  return layout(std::max(rows * chunks_of(vocab, kBytes / 4, 1), std::min<int64_t>(rows * chunks_of(vocab, kFew, 1), 4 * 63)),
                 width, &cand);
 }
 
 hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s) {
   const int64_t rows = (int64_t)a.n_req * a.width;
-  const Cut c = get_cut(rows, a.vocab);
+  const Cut c = get_cut(rows, a.vocab, a.dtype);
   size_t cand;
   layout(rows * c.chunks, a.width, &cand);
   const BeamWs w = {(uint32_t*)ws, (uint64_t*)((char*)ws + kCounterBytes), (uint64_t*)((char*)ws + cand)};
@@ -654,11 +667,11 @@ hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s) {
                        (int)c.chunks, c.steps);
   };
   if (a.dtype == DFS_F16) {
-    if (c.e == kMany) run(beam_kernel<_Float16, kMany>);
-    else run(beam_kernel<_Float16, kFew>);
+    if (c.e == kFew) run(beam_kernel<_Float16, kFew>);
+    else run(beam_kernel<_Float16, kBytes / 2>);
   } else {
-    if (c.e == kMany) run(beam_kernel<float, kMany>);
-    else run(beam_kernel<float, kFew>);
+    if (c.e == kFew) run(beam_kernel<float, kFew>);
+    else run(beam_kernel<float, kBytes / 4>);
   }
   return hipGetLastError();
 }

@@ -355,7 +355,7 @@ hipError_t launch_kv8_copy(const KvCopy& a, hipStream_t s);
 
 // Selection of beam search
 constexpr int kMaxBeams = 32;
-constexpr int kMaxBeamRequests = 16384;  // counters in the first 64 KiB of the workspace
+constexpr int kMaxBeamRows = 8192;  // counters of requests and rows in the workspace's first 64 KiB
 struct BeamLaunch {
   int32_t n_req, width, vocab;
   const void* logits;
@@ -369,7 +369,7 @@ struct BeamLaunch {
   float* score_out;
   int32_t* done_out;  // may be null
 };
-size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab);
+size_t beam_ws_need(int32_t n_req, int32_t width, int32_t vocab, int32_t dtype);
 size_t beam_ws_bytes(int32_t n_req, int32_t width, int32_t vocab);
 hipError_t launch_beam_select(const BeamLaunch& a, void* ws, hipStream_t s);
 

@@ -639,7 +639,7 @@ dfs_status beam_select_workspace_size(int32_t n_req, int32_t width, int32_t voca
  *   is its first row, token -1, score -inf and done_out 0.
  * Exponentials and the sums of two of them are fp32, all other sums and the totals
  * 64 bits.
- * 1 <= width <= 32, n_req <= 16384, n_req * width <= 65535 (DFS_E_RANGE).
+ * 1 <= width <= 32, n_req * width <= 8192, vocab <= 2^30 (DFS_E_RANGE).
  * Outputs must not overlap inputs.  The workspace's first 64 KiB must be zero
  * before its first use; every call leaves them zero again.  Calls sharing a
  * workspace must not run concurrently. */

@@ -131,7 +131,7 @@ def test_beam_validation():
     assert _beam(ws=P + 8, ws_bytes=1 << 40) == ALIGN
     for change, status in ((dict(n_req=-1), INVALID), (dict(width=0), INVALID),
                            (dict(vocab=0), INVALID), (dict(width=33), RANGE),
-                           (dict(n_req=16385, width=1), RANGE), (dict(n_req=16384, width=4), RANGE),
+                           (dict(n_req=8193, width=1), RANGE), (dict(n_req=1025, width=8), RANGE),
                            (dict(vocab=(1 << 30) + 1, ldl=1 << 31), RANGE),
                            (dict(dt=B.DFS_FP8), UNSUPPORTED), (dict(dt=B.DFS_NVFP4), UNSUPPORTED),
                            (dict(ldl=99), INVALID), (dict(eos=-1), INVALID),
