@@ -892,11 +892,14 @@ def kv8_prefix_attention(kv: DeviceKV8, Q, tok_start, length, table, group_start
     _ints(group_start, "group_start", n_groups + 1)
     if Q.dtype != torch.float16:
         raise TypeError("Q must be float16")
+    given = (kv.k, Q, tok_start, length, table, group_start, shared)
     if O is None:
-        O = torch.empty(n_tok, cols, dtype=odtype, device=Q.device)
-    ldo = _matrix(O, "O", n_tok, cols)
+        O, ldo = torch.empty(n_tok, cols, dtype=odtype, device=Q.device), cols
+    else:
+        ldo = _matrix(O, "O", n_tok, cols)
+        given += (O,)
     odt = _dt(O)
-    _on_device((kv.k, Q, O, tok_start, length, table, group_start, shared), "cache")
+    _on_device(given, "cache")
     if ws is None:
         ws = kv8_prefix_attention_workspace(kv, n_req, n_tok, q_heads, Q.device)
     st = lib().kv8_prefix_attention(kv._ref, n_req, n_tok, tok_start.data_ptr(), length.data_ptr(),
@@ -1030,16 +1033,20 @@ def kv8_reorder(refs, page: int, table, length, parent, table_out, keep: bool = 
     ldt, ldo = _table(table, "table", n_in), _table(table_out, "table_out", n_out)
     if table.shape[1] != table_out.shape[1]:
         raise ValueError("table and table_out: rows of the same entries required")
-    made = lambda t, n: torch.empty(n, dtype=torch.int32,  # noqa: E731
-                                    device=refs.device) if t is None else t
-    length_out, src, dst = made(length_out, n_out), made(src, n_out), made(dst, n_out)
-    missing = made(missing, 1)
-    for t, what in ((length_out, "length_out"), (src, "src"), (dst, "dst")):
-        _ints(t, what, n_out)
-    _ints(missing, "missing", 1)
+    given = [refs, table, length, parent, table_out]
+    made = []
+    for t, n, what in ((length_out, n_out, "length_out"), (src, n_out, "src"), (dst, n_out, "dst"),
+                       (missing, 1, "missing")):
+        if t is None:
+            t = torch.empty(n, dtype=torch.int32, device=refs.device)
+        else:
+            _ints(t, what, n)
+            given.append(t)
+        made.append(t)
+    length_out, src, dst, missing = made
     if ws is None:
         ws = kv8_reorder_workspace(n_in, refs.device)
-    _on_device((refs, table, length, parent, table_out, length_out, src, dst, missing), "pages")
+    _on_device(given, "pages")
     st = lib().kv8_reorder(n_in, n_out, page, refs.shape[0], refs.data_ptr(), table.data_ptr(), ldt,
                            length.data_ptr(), parent.data_ptr(), int(keep), table_out.data_ptr(),
                            ldo, table.shape[1], length_out.data_ptr(), src.data_ptr(),
@@ -1092,19 +1099,23 @@ def beam_select(logits, score, width: int, eos: int = -1, done=None, norm=None, 
         raise ValueError("logits: (requests * width, vocab) required")
     rows, vocab = logits.shape
     ldl = _matrix(logits, "logits", None, vocab)
-    made = lambda t, dt: torch.empty(rows, dtype=dt, device=logits.device  # noqa: E731
-                                     ) if t is None else t
-    parent, token = made(parent, torch.int32), made(token, torch.int32)
-    score_out, done_out = made(score_out, torch.float32), made(done_out, torch.int32)
-    given = [logits, score, parent, token, score_out, done_out]
-    for t, what in ((parent, "parent"), (token, "token"), (done, "done"), (done_out, "done_out")):
+    given = [logits, score]
+    made = []
+    for t, what in ((parent, "parent"), (token, "token"), (done_out, "done_out"), (done, "done")):
         if t is not None:
             _ints(t, what, rows)
+            given.append(t)
+        elif what != "done":
+            t = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        made.append(t)
+    parent, token, done_out, done = made
     for t, what in ((score, "score"), (norm, "norm"), (score_out, "score_out")):
-        if t is not None and (t.shape != (rows,) or t.dtype != torch.float32
-                              or not t.is_contiguous()):
-            raise ValueError(f"{what}: contiguous float32 of {rows} values required")
-    given += [t for t in (done, norm) if t is not None]
+        if t is not None:
+            if t.shape != (rows,) or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError(f"{what}: contiguous float32 of {rows} values required")
+            given.append(t)
+    if score_out is None:
+        score_out = torch.empty(rows, dtype=torch.float32, device=logits.device)
     dt = _dt(logits)
     _on_device(given, "beams")
     if ws is None:

@@ -263,10 +263,11 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
     return cand_of(w, sh.f.state[w] == 1 ? get(cands + i) : 0, i == w * per_row);
   };
   // A piece's candidates descend: the width-th largest of the first ones of a wave's
-  // pieces bounds those to look at; of the first eight, where the pieces are few.
+  // pieces bounds those to look at; of the first eight, where the pieces are few or the
+  // width is large (8 requests of width 32 with heads alone: 600 candidates and 62 us).
   const int lists = W * chunks;
   uint32_t bound = 0;
-  for (int deep = 0; deep < 2 && bound == 0; ++deep) {
+  for (int deep = W > kAhead ? 1 : 0; deep < 2 && bound == 0; ++deep) {
     uint32_t best = 0;
     for (int j0 = 0; j0 < lists; j0 += kThreads) {
       const int j = j0 + tid, w = min(j / chunks, W - 1);
@@ -295,36 +296,46 @@ __device__ __forceinline__ void choose(const BeamLaunch& a, const BeamWs& ws, Sh
       }
       best = max(best, t);
     }
-    if (deep) __syncthreads();  // the first round's bounds have been read
+    __syncthreads();  // an earlier round's bounds have been read
     if (lane == 0) sh.bound[wave] = best;
     __syncthreads();
     for (int v = 0; v < kWaves; ++v) bound = max(bound, sh.bound[v]);
     if (lists * W <= kList / 4) break;  // few enough to look at them all
   }
-  for (int j = tid; j < lists; j += kThreads) {
-    const int w = j / chunks;
-    bool more = true;
-    for (int k0 = 0; k0 < W && more; k0 += kAhead) {
-      if (k0 > 0 || lists > kThreads) {
+  for (bool again = false;; again = true) {
+    for (int j = tid; j < lists; j += kThreads) {
+      const int w = j / chunks;
+      bool more = true;
+      for (int k0 = 0; k0 < W && more; k0 += kAhead) {
+        if (k0 > 0 || again || lists > kThreads) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) x[k] = get(cands + j * W + min(k0 + k, W - 1));
-      }
+          for (int k = 0; k < kAhead; ++k) x[k] = get(cands + j * W + min(k0 + k, W - 1));
+        }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (!more || k0 + k >= W) continue;
-        const Cand c = cand_of(w, x[k], k0 + k == 0 && j == w * chunks);
-        more = c.key != 0 && (uint32_t)(c.key >> 32) >= bound;
-        if (!more) continue;
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < kList) {
-          sh.f.key[at] = c.key;
-          sh.f.elem[at] = c.elem;
-          sh.f.row[at] = c.row;
+        for (int k = 0; k < kAhead; ++k) {
+          if (!more || k0 + k >= W) continue;
+          const Cand c = cand_of(w, x[k], k0 + k == 0 && j == w * chunks);
+          more = c.key != 0 && (uint32_t)(c.key >> 32) >= bound;
+          if (!more) continue;
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kList) {
+            sh.f.key[at] = c.key;
+            sh.f.elem[at] = c.elem;
+            sh.f.row[at] = c.row;
+          }
         }
       }
     }
+    __syncthreads();
+    // too many: the width-th largest of those that the list holds is a higher bound
+    if (sh.n <= kList) break;
+    const uint32_t t = nth_of<kLow64, kList / kWave>(kList, W, [&](int i) { return (uint32_t)(sh.f.key[i] >> 32); });
+    if (t <= bound) break;  // they are equal
+    bound = t;
+    __syncthreads();
+    if (tid == 0) sh.n = 0;
+    __syncthreads();
   }
-  __syncthreads();
   const int n = sh.n;
   auto write = [&](int rank, const Cand& c) {
     const int64_t o = row0 + rank;

@@ -88,8 +88,17 @@ struct FreePages {
     for (int s = kWords / 2; s > 0; s >>= 1)
       if (sh.before[w + s] <= k) w += s;
     uint64_t m = sh.bits[w];
-    for (int i = k - sh.before[w]; i > 0; --i) m &= m - 1;
-    return (int)(page0 + w * kWave + __builtin_ctzll(m));
+    int i = k - sh.before[w], at = 0;  // its place among the word's set bits, by halves
+#pragma unroll
+    for (int s = kWave / 2; s > 0; s >>= 1) {
+      const int low = __popcll(m & ((1ull << s) - 1));
+      if (i >= low) {
+        i -= low;
+        at += s;
+        m >>= s;
+      }
+    }
+    return (int)(page0 + w * kWave + at);
   }
   // Hands pages to the threads that want one, lowest rank first; `done` ranks
   // went out before.  -1 where there are none left.
@@ -153,13 +162,16 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
   FreePages pages(fs, a.refs, a.n_pages);
   const int tid = threadIdx.x;
   int64_t tok = 0, ranks = 0;
+  int ci = tid < a.n_req ? *gptr(a.cached + tid) : 0, ni = tid < a.n_req ? *gptr(a.n_new + tid) : 0;
+  pages.round();  // its reads go with those of the first requests
   for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
     const int r = r0 + tid;
-    int64_t c = 0, n = 0;
-    if (r < a.n_req) {
-      c = max(*gptr(a.cached + r), 0);
-      n = max(*gptr(a.n_new + r), 0);
+    if (r0 > 0) {
+      ci = r < a.n_req ? *gptr(a.cached + r) : 0;
+      ni = r < a.n_req ? *gptr(a.n_new + r) : 0;
     }
+    const int64_t c = max(ci, 0);
+    int64_t n = max(ni, 0);
     int64_t all;
     const int64_t at = tok + block_scan<int64_t>(n, tmp, &all, kThreads);
     const int64_t t0 = least(at, a.n_tok);
@@ -294,6 +306,7 @@ __global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int3
   __shared__ int tmp[kWaves];
   FreePages pages(fs, a.refs, a.n_pages);
   int64_t ranks = 0;
+  pages.round();
   // the entry in question of row b, or null
   auto entry = [&](int b, int& p) -> int32_t* {
     if (b >= a.n_out) return nullptr;
