@@ -12,9 +12,11 @@ constexpr int kPlanThreads = 1024;
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, PrefixWs ws, int32_t* scratch, int qb,
                                                             int extra, int qb_own, int extra_own) {
-  __shared__ int64_t tmp[kPlanThreads / kWave][2];
+  __shared__ Scan3 tmp[kPlanThreads / kWave];
   __shared__ int longest[2];
   const int n = p.a.b.n_req;
+  clear_prefix_plan<kPlanThreads>(p, ws.plan, [&](int i) { return *gptr(p.group_start + i); }, longest);
+  __syncthreads();
   make_prefix_plan<kPlanThreads>(
       p, ws.plan, [&](int r) { return get_req(p.a.b, p.a.kv.page, r); },
       [&](int i) { return *gptr(p.group_start + i); }, [&](int i) { return *gptr(p.shared + i); }, scratch,

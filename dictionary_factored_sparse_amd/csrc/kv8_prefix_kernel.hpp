@@ -109,13 +109,16 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
   const PrefixAt at = {&ws.plan, &lds, in != 0};
   if (in) {
     const int tid = threadIdx.x;
-    if (tid < a.b.n_req) lds.facts[tid] = get_req(a.b, a.kv.page, tid);
-    if (tid <= p.n_groups) lds.group_start[tid] = *gptr(p.group_start + tid);
-    if (tid < p.n_groups) lds.shared[tid] = *gptr(p.shared + tid);
-    __syncthreads();
     const PrefixPlan w = {lds.groups, lds.live, lds.from, lds.pos,
                           {lds.line_shared.first, lds.line_shared.of, lds.line_shared.qblk, lds.line_shared.n},
                           {lds.line_own.first, lds.line_own.of, lds.line_own.qblk, lds.line_own.n}};
+    const int start = tid <= p.n_groups ? *gptr(p.group_start + tid) : 0;
+    const int shared = tid < p.n_groups ? *gptr(p.shared + tid) : 0;
+    if (tid < a.b.n_req) lds.facts[tid] = get_req(a.b, a.kv.page, tid);
+    if (tid <= p.n_groups) lds.group_start[tid] = start;
+    if (tid < p.n_groups) lds.shared[tid] = shared;
+    clear_prefix_plan<kThreads>(p, w, [&](int) { return start; }, lds.longest);
+    __syncthreads();
     make_prefix_plan<kThreads>(
         p, w, [&](int r) { return lds.facts[r]; }, [&](int i) { return lds.group_start[i]; },
         [&](int i) { return lds.shared[i]; }, lds.group_of, lds.first_entry, lds.first_shared, ws.most_shared,

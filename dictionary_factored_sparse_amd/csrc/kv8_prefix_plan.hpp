@@ -8,9 +8,43 @@
 namespace dfs {
 namespace {
 
+// Three sums over the threads before this one, and over all of them.
+struct Scan3 {
+  int64_t v[3];
+};
+template <int T>
+__device__ __forceinline__ Scan3 block_scan3(const Scan3& x, Scan3* tmp, Scan3& all) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  Scan3 s = x;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    int64_t u[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) u[i] = __shfl_up(s.v[i], o, kWave);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s.v[i] += lane >= o ? u[i] : 0;
+  }
+  if (lane == kWave - 1) tmp[wave] = s;
+  __syncthreads();
+  all = {};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) s.v[i] -= x.v[i];
+#pragma unroll
+  for (int w = 0; w < T / kWave; ++w) {
+    const Scan3 u = tmp[w];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      s.v[i] += w < wave ? u.v[i] : 0;
+      all.v[i] += u.v[i];
+    }
+  }
+  __syncthreads();
+  return s;
+}
+
 // The facts of a small batch, in LDS.
 struct PrefixInline {
-  int64_t tmp[kWaves][2];
+  Scan3 tmp[kWaves];
   int32_t longest[2];
   Req facts[kPrefixInline];
   int32_t group_start[kPrefixInline + 1], shared[kPrefixInline];
@@ -22,41 +56,6 @@ struct PrefixInline {
     int32_t of[kPrefixInlineEntries], qblk[kPrefixInlineEntries], n[2];
   } line_shared, line_own;
 };
-
-// Two sums over the threads before this one, and over all of them.
-template <int T>
-__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t (*tmp)[2], int64_t& all_x,
-                                            int64_t& all_y) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  int64_t sx = x, sy = y;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int64_t ux = __shfl_up(sx, o, kWave), uy = __shfl_up(sy, o, kWave);
-    if (lane >= o) {
-      sx += ux;
-      sy += uy;
-    }
-  }
-  if (lane == kWave - 1) {
-    tmp[wave][0] = sx;
-    tmp[wave][1] = sy;
-  }
-  __syncthreads();
-  all_x = all_y = 0;
-  x = sx - x;
-  y = sy - y;
-#pragma unroll
-  for (int w = 0; w < T / kWave; ++w) {
-    const int64_t ux = tmp[w][0], uy = tmp[w][1];
-    if (w < wave) {
-      x += ux;
-      y += uy;
-    }
-    all_x += ux;
-    all_y += uy;
-  }
-  __syncthreads();
-}
 
 // Workgroups that take shared keys, of all; the others take own ones.  By the two
 // lines' work: a tile of shared keys takes as long as kTileCost of own ones where
@@ -71,25 +70,21 @@ __device__ __forceinline__ int shared_slices(int64_t shared, int64_t own, bool s
 
 // The plan, by one workgroup of T threads.  facts(r): request r; starts(i), shared(i):
 // of group i; group_of, entry_own, entry_shared: scratch of one int a request, a
-// request, a group; put_token takes what the second kernel needs.
+// request, a group; put_token takes what the second kernel needs.  Begins after a
+// barrier that facts, starts and shared want.
 template <int T, typename Q, typename S, typename H, typename P>
 __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const PrefixPlan& w, Q facts, S starts,
                                                  H shared, int32_t* group_of, int32_t* entry_own,
                                                  int32_t* entry_shared, int most_shared, int most_own, int qb,
                                                  int extra, int qb_own, int extra_own, P put_token,
-                                                 int64_t (*tmp)[2], int* longest) {
+                                                 Scan3* tmp, int* longest) {
   const KvAttnLaunch& a = p.a;
-  const int tid = threadIdx.x, g = a.q_heads / a.kv.heads;
+  const int tid = threadIdx.x, heads = a.kv.heads;
+  const uint32_t g = a.q_heads / heads;
   // tokens that group i shares, as far as the table goes
   auto shared_of = [&](int i) {
     return (int)min((int64_t)max(shared(i), 0), (int64_t)a.b.table_pages * a.kv.page);
   };
-  for (int i = tid; i < p.n_groups; i += T) {
-    const int r = min(max(starts(i), 0), max(a.b.n_req - 1, 0));
-    w.groups[i] = PrefixGroup{INT32_MAX, INT32_MIN, INT32_MAX, INT32_MIN, 0, r};
-    w.live[i] = 0;
-  }
-  __syncthreads();
   for (int r = tid; r < a.b.n_req; r += T) {
     const Req q = facts(r);
     int lo = 0, hi = p.n_groups;  // the last group that starts at or before r, if any does
@@ -109,91 +104,95 @@ __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const Pr
     atomicAdd(w.live + lo, 1);
   }
   __syncthreads();
-  for (int i = tid; i < p.n_groups; i += T) {
-    PrefixGroup f = w.groups[i];
-    f.keys = shared_of(i) / kTile * kTile;
-    // worth it for two requests that see some of it
-    if (w.live[i] < 2) f.keys = 0;
-    else f.n -= f.t0;  // with the tokens between of requests that stand alone, whose sums nobody takes
-    if (f.keys > 0) {
-      const int hi = min(f.p1, f.keys - 1), lo = a.window > 0 && f.p0 >= a.window ? f.p0 - a.window + 1 : 0;
-      if (hi < 0 || (hi < lo && a.sinks <= 0)) f.keys = 0;
-    }
-    w.groups[i].n = f.n;
-    w.groups[i].keys = f.keys;
-  }
-  __syncthreads();
-  for (int r = tid; r < a.b.n_req; r += T) {
-    const int i = group_of[r];
-    w.from[r] = i < 0 ? 0 : w.groups[i].keys;
-  }
-  // entries in order: first those of both lines' groups and requests, then where
-  // each starts in its line
-  auto put_entries = [&](const PrefixEntries& l, int64_t at, int nb, int most, int i) {
-    for (int b = 0; b < nb && at + b < most; ++b) {
-      l.of[at + b] = i;
-      l.qblk[at + b] = b;
-    }
+  // what a group shares: worth it for two requests that see some of it
+  auto keys_of = [&](int i, const PrefixGroup& f) {
+    const int keys = w.live[i] < 2 ? 0 : shared_of(i) / kTile * kTile;
+    const int hi = min(f.p1, keys - 1), lo = a.window > 0 && f.p0 >= a.window ? f.p0 - a.window + 1 : 0;
+    return hi < 0 || (hi < lo && a.sinks <= 0) ? 0 : keys;
   };
   const int n = max(p.n_groups, a.b.n_req);
-  int64_t n_shared = 0, n_own = 0;
+  int64_t n_shared = 0, n_own = 0, base_shared = 0, base_own = 0;
+  int top_shared = 0, top_own = 0;
   for (int i0 = 0; i0 < n; i0 += T) {
     const int i = i0 + tid;
-    int nb_shared = 0, nb_own = 0;
-    if (i < p.n_groups && w.groups[i].keys > 0) nb_shared = (int)(((uint32_t)(w.groups[i].n * g) + qb - 1) / qb);
-    if (i < a.b.n_req) nb_own = (int)(((uint32_t)(facts(i).n * g) + qb_own - 1) / qb_own);
-    int64_t x = nb_shared, y = nb_own, all_x, all_y;
-    block_scan2<T>(x, y, tmp, all_x, all_y);
-    x += n_shared;
-    y += n_own;
-    if (i < p.n_groups) entry_shared[i] = (int)min(x, (int64_t)most_shared);
-    if (i < a.b.n_req) entry_own[i] = (int)min(y, (int64_t)most_own);
-    put_entries(w.shared, x, nb_shared, most_shared, i);
-    put_entries(w.own, y, nb_own, most_own, i);
-    n_shared += all_x;
-    n_own += all_y;
-  }
-  n_shared = min(n_shared, (int64_t)most_shared);
-  n_own = min(n_own, (int64_t)most_own);
-  if (tid < 2) longest[tid] = 0;
-  __syncthreads();
-  int64_t base_shared = 0, base_own = 0;
-  int top_shared = 0, top_own = 0;
-  for (int e0 = 0; e0 < max(n_shared, n_own); e0 += T) {
-    const int e = e0 + tid;
-    int64_t x = 0, y = 0, all_x, all_y;
-    if (e < n_shared) {
-      const PrefixGroup& f = w.groups[w.shared.of[e]];
-      const int m = get_span(Req{f.t0, f.n, f.keys, f.keys}, f.p0, f.p1, a.window, a.sinks).n;
-      top_shared = max(top_shared, m);
-      x = ((int64_t)m + extra) * a.kv.heads;
-    }
-    if (e < n_own) {
-      const int r = w.own.of[e];
-      const Req q = facts(r);
-      const uint32_t r0 = w.own.qblk[e] * qb_own, r1 = min(r0 + qb_own, (uint32_t)(q.n * g)) - 1;
+    PrefixGroup f = {};
+    Span fs = {}, rs = {};
+    uint32_t nb_shared = 0, nb_own = 0;
+    Scan3 x = {}, all;
+    Req q = {};
+    int from = 0;
+    bool uniform = true;  // whether all blocks of a request have the same tiles
+    auto span_of = [&](uint32_t b) {
+      const uint32_t r0 = b * qb_own, r1 = min(r0 + qb_own, (uint32_t)q.n * g) - 1;
       const int p0 = q.len - q.n;
-      const int m = get_span(q, p0 + (int)(r0 / g), p0 + (int)(r1 / g), a.window, a.sinks, w.from[r]).n;
-      top_own = max(top_own, m);
-      y = ((int64_t)m + extra_own) * a.kv.heads;
+      return get_span(q, p0 + (int)(r0 / g), p0 + (int)(r1 / g), a.window, a.sinks, from);
+    };
+    if (i < p.n_groups) {
+      f = w.groups[i];
+      f.keys = keys_of(i, f);
+      if (f.keys > 0) {
+        f.n -= f.t0;  // with the tokens between of requests that stand alone, whose sums nobody takes
+        nb_shared = ((uint32_t)f.n * g + qb - 1) / qb;
+        fs = get_span(Req{f.t0, f.n, f.keys, f.keys}, f.p0, f.p1, a.window, a.sinks);
+        top_shared = max(top_shared, fs.n);
+      }
     }
-    block_scan2<T>(x, y, tmp, all_x, all_y);
-    if (e < n_shared) w.shared.first[e] = base_shared + x;
-    if (e < n_own) w.own.first[e] = base_own + y;
-    base_shared += all_x;
-    base_own += all_y;
+    if (i < a.b.n_req) {
+      q = facts(i);
+      const int grp = group_of[i];
+      if (grp >= 0) from = keys_of(grp, w.groups[grp]);
+      w.from[i] = from;
+      nb_own = ((uint32_t)q.n * g + qb_own - 1) / qb_own;
+      uniform = nb_own <= 1;
+      for (uint32_t b = 0; b < nb_own; ++b) {
+        rs = span_of(b);
+        top_own = max(top_own, rs.n);
+        x.v[2] += ((int64_t)rs.n + extra_own) * heads;
+      }
+    }
+    x.v[0] = (int64_t)nb_shared << 32 | nb_own;
+    x.v[1] = ((int64_t)fs.n + extra) * heads * nb_shared;
+    // before the barriers of the sums, after which the groups may be written
+    const Scan3 at = block_scan3<T>(x, tmp, all);
+    int64_t e = n_shared + (at.v[0] >> 32), o = n_own + (uint32_t)at.v[0];
+    if (i < p.n_groups) {
+      w.groups[i].n = f.n;
+      w.groups[i].keys = f.keys;
+      entry_shared[i] = (int)min(e, (int64_t)most_shared);
+      for (uint32_t b = 0; b < nb_shared && e < most_shared; ++b, ++e) {
+        w.shared.of[e] = i;
+        w.shared.qblk[e] = b;
+        w.shared.first[e] = base_shared + at.v[1] + (int64_t)b * (fs.n + extra) * heads;
+      }
+    }
+    if (i < a.b.n_req) {
+      entry_own[i] = (int)min(o, (int64_t)most_own);
+      int64_t start = base_own + at.v[2];
+      for (uint32_t b = 0; b < nb_own && o < most_own; ++b, ++o) {
+        w.own.of[o] = i;
+        w.own.qblk[o] = b;
+        w.own.first[o] = start;
+        start += ((int64_t)(uniform ? rs.n : span_of(b).n) + extra_own) * heads;
+      }
+    }
+    n_shared += all.v[0] >> 32;
+    n_own += (uint32_t)all.v[0];
+    base_shared += all.v[1];
+    base_own += all.v[2];
   }
   if (top_shared > 0) atomicMax(longest, top_shared);
   if (top_own > 0) atomicMax(longest + 1, top_own);
-  __syncthreads();
   if (tid == 0) {
+    n_shared = min(n_shared, (int64_t)most_shared);
+    n_own = min(n_own, (int64_t)most_own);
     w.shared.first[n_shared] = base_shared;
     w.own.first[n_own] = base_own;
     w.shared.n[0] = (int)n_shared;
     w.own.n[0] = (int)n_own;
-    w.shared.n[1] = longest[0];
-    w.own.n[1] = longest[1];
   }
+  __syncthreads();
+  if (tid == 0) w.shared.n[1] = longest[0];
+  if (tid == 0) w.own.n[1] = longest[1];
   for (int t = tid; t < a.b.n_tok; t += T) {
     int lo = 0, hi = a.b.n_req;  // the last request that starts at or before t
     while (hi - lo > 1) {
@@ -206,16 +205,26 @@ __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const Pr
     PrefixToken k = {-1, 0, -1, 0};
     if (t >= q.t0 && t < q.t0 + q.n) {
       k.own = entry_own[lo];
-      k.own_row = (t - q.t0) * g;
+      k.own_row = (t - q.t0) * (int)g;
       const int i = group_of[lo];
       if (i >= 0 && w.groups[i].keys > 0) {
         k.shared = entry_shared[i];
-        k.shared_row = (t - w.groups[i].t0) * g;
+        k.shared_row = (t - w.groups[i].t0) * (int)g;
       }
     }
     put_token(t, k);
   }
   __syncthreads();
+}
+// What the plan starts from, for thread tid of T; a barrier follows.
+template <int T, typename S>
+__device__ __forceinline__ void clear_prefix_plan(const PrefixLaunch& p, const PrefixPlan& w, S starts, int* longest) {
+  for (int i = threadIdx.x; i < p.n_groups; i += T) {
+    const int r = min(max(starts(i), 0), max(p.a.b.n_req - 1, 0));
+    w.groups[i] = PrefixGroup{INT32_MAX, INT32_MIN, INT32_MAX, INT32_MIN, 0, r};
+    w.live[i] = 0;
+  }
+  if (threadIdx.x < 2) longest[threadIdx.x] = 0;
 }
 
 }  // namespace
