@@ -744,6 +744,18 @@ struct Line {
   f2* group_ml;     // the same of a group of slices, at its first slice's slot
 };
 
+// A part, for this kernel's other workgroups or for a later kernel.
+template <typename A>
+__device__ __forceinline__ void put_part(float* p, const f4& v) {
+  if constexpr (A::kJoinHere) put4(p, v);
+  else *gptr_w((f4*)p) = v;
+}
+template <typename A>
+__device__ __forceinline__ void put_part(f2* p, float x, float y) {
+  if constexpr (A::kJoinHere) put2(p, x, y);
+  else *gptr_w((uint64_t*)p) = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+}
+
 // Slice `slice` of a line of items.  A is an Attn that knows its line as well:
 // first(e) is the line's position where entry e starts (a plan has made it),
 // first(n_entries) its end; longest() the most tiles an item has; ready(e, kv head)
@@ -841,8 +853,8 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
         if (whole) {
           t.put(t.at(t.row0 + row), d, v, mm, l);
         } else {
-          put4(&ln.part_o[(slot * A::kQb + row) * A::kD + d], v);
-          if (d == 0) put2(&ln.part_ml[slot * A::kQb + row], f2{mm, l});
+          put_part<A>(&ln.part_o[(slot * A::kQb + row) * A::kD + d], v);
+          if (d == 0) put_part<A>(&ln.part_ml[slot * A::kQb + row], mm, l);
         }
       }
     } else {
@@ -855,9 +867,9 @@ __device__ __forceinline__ void run_line(A& t, typename A::Work& sh, const Line&
 #pragma unroll
           for (int d = 0; d < A::kDims; ++d) {
             if (whole) t.put(at, d * 16 + t.q4 * 4, t.o[i][d], t.m[i], t.l[i]);
-            else put4(&ln.part_o[pr * A::kD + d * 16 + t.q4 * 4], t.o[i][d]);
+            else put_part<A>(&ln.part_o[pr * A::kD + d * 16 + t.q4 * 4], t.o[i][d]);
           }
-          if (!whole && t.q4 == 0) put2(&ln.part_ml[pr], t.m[i], t.l[i]);
+          if (!whole && t.q4 == 0) put_part<A>(&ln.part_ml[pr], t.m[i], t.l[i]);
         }
       }
       if (A::kNan && nans)

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(KvAttnLaunch a, const P
   const int h = real ? place / quads : 0, d = real ? place % quads * 4 : 0, kh = h / g;
   const int64_t at = (int64_t)tok * a.q_heads + h;
   const int n = shared_slices(*gptr(shared.plan.first + *gptr(shared.plan.n)), *gptr(own.plan.first + *gptr(own.plan.n)),
-                              shared.split != 0, slices);
+                              *gptr(own.plan.n + 1), shared.split != 0, slices);
   float m, l;
   f4 v;
   line_sums(own, k.own, k.own_row + h - kh * g, kh, a.kv.heads, slices - n, at, D, d, wave, m, l, v);

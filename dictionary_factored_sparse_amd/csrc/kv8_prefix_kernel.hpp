@@ -139,7 +139,8 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
   auto length = [&](const PrefixInline::Entries& e, const PrefixEntries& f) {
     return in ? e.first[e.n[0]] : *gptr(f.first + *gptr(f.n));
   };
-  const int n = shared_slices(length(lds.line_shared, ws.plan.shared), length(lds.line_own, ws.plan.own), SPLIT, slices);
+  const int n = shared_slices(length(lds.line_shared, ws.plan.shared), length(lds.line_own, ws.plan.own),
+                              in ? lds.line_own.n[1] : *gptr(ws.plan.own.n + 1), SPLIT, slices);
   const int slice = blockIdx.x;
   if (slice < n) {
     P t(a, at, ws.shared);

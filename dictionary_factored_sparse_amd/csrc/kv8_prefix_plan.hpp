@@ -59,13 +59,16 @@ struct PrefixInline {
 
 // Workgroups that take shared keys, of all; the others take own ones.  By the two
 // lines' work: a tile of shared keys takes as long as kTileCost of own ones where
-// each wave has rows of its own (3.6 us, 1.5).
-constexpr float kTileCost = 2.4f;
-__device__ __forceinline__ int shared_slices(int64_t shared, int64_t own, bool split, int slices) {
+// each wave has rows of its own (3.6 us, 1.5), and beside those, own items that are not
+// split cost kWholeCost of what they count in the line, where `extra` stands for a join
+// as well (24 questions to a document 92 us without, 88 so).
+constexpr float kTileCost = 2.4f, kWholeCost = 0.6f;
+__device__ __forceinline__ int shared_slices(int64_t shared, int64_t own, int longest, bool split, int slices) {
   if (own <= 0) return slices;
   if (shared <= 0) return 0;
   const float x = (float)shared * (split ? 1.0f : kTileCost);
-  return min(max((int)(x / (x + (float)own) * (float)slices + 0.5f), 1), slices - 1);
+  const float y = (float)own * (!split && longest <= kPrefixEach ? kWholeCost : 1.0f);
+  return min(max((int)(x / (x + y) * (float)slices + 0.5f), 1), slices - 1);
 }
 
 // The plan, by one workgroup of T threads.  facts(r): request r; starts(i), shared(i):
