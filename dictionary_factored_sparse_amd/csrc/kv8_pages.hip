@@ -27,6 +27,30 @@ __device__ __forceinline__ int pages_of(int64_t len, int page, int most) {
   return (int)least((len + page - 1) / page, most);
 }
 
+// Sum of v over the threads before this one, and over all of them.  The waves' sums
+// are added by the lanes of each wave.
+template <typename T>
+__device__ __forceinline__ T scan(T v, T* tmp, T* total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const T y = __shfl_up(x, o, kWave);
+    x += lane >= o ? y : 0;
+  }
+  if (lane == kWave - 1) tmp[wave] = x;
+  __syncthreads();
+  T w = tmp[lane % kWaves];
+#pragma unroll
+  for (int o = 1; o < kWaves; o <<= 1) {
+    const T y = __shfl_up(w, o, kWaves);
+    w += lane % kWaves >= o ? y : 0;
+  }
+  __syncthreads();
+  *total = __shfl(w, kWaves - 1, kWave);
+  return (wave > 0 ? __shfl(w, wave - 1, kWave) : 0) + x - v;
+}
+
 // The free pages in order, as one workgroup finds them: a round of kRound pages
 // at a time, held as one bit a page.  Every call is made by all threads.
 struct FreePages {
@@ -69,11 +93,13 @@ struct FreePages {
     if (lane < kLoads) sh.bits[wave * kLoads + lane] = mine;
     if (lane == kLoads - 1) sh.sum[wave] = x;
     __syncthreads();
-    int base = 0, all = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) base += sh.sum[w];
-      all += sh.sum[w];
+    int w = sh.sum[lane % kWaves];
+#pragma unroll
+    for (int o = 1; o < kWaves; o <<= 1) {
+      const int y = __shfl_up(w, o, kWaves);
+      w += lane % kWaves >= o ? y : 0;
     }
+    const int all = __shfl(w, kWaves - 1, kWave), base = wave > 0 ? __shfl(w, wave - 1, kWave) : 0;
     if (lane < kLoads) sh.before[wave * kLoads + lane] = base + x - own;
     __syncthreads();
     lo = hi;
@@ -104,7 +130,7 @@ struct FreePages {
   // went out before.  -1 where there are none left.
   __device__ __forceinline__ int take(bool want, int64_t& done, int* tmp) {
     int total;
-    const int at = block_scan<int>(want ? 1 : 0, tmp, &total, kThreads);
+    const int at = scan<int>(want ? 1 : 0, tmp, &total);
     const int64_t r = done + at;
     int got = -1;
     done += total;
@@ -122,11 +148,11 @@ struct FreePages {
 
 // ------------------------------------------------------------------ tables
 
-__device__ __forceinline__ void map_token(const KvTables& a, int t, int r, int start) {
+__device__ __forceinline__ void map_token(const KvTables& a, int t, int r, int start, int cached) {
   int pos = -1;
   int64_t slot = -1;
   if (r >= 0) {
-    const int64_t p = (int64_t)max(*gptr(a.cached + r), 0) + (t - start);
+    const int64_t p = (int64_t)max(cached, 0) + (t - start);
     pos = (int)least(p, INT32_MAX);
     const int i = pos / a.page;
     if (i < a.table_pages) {
@@ -158,7 +184,7 @@ template <bool MAP>
 __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
   __shared__ FreePages::Shared fs;
   __shared__ int64_t tmp[kWaves];
-  __shared__ int first[kThreads], entry[kThreads], start[kThreads + 1];
+  __shared__ int first[kThreads], entry[kThreads], start[kThreads + 1], have[kThreads];
   FreePages pages(fs, a.refs, a.n_pages);
   const int tid = threadIdx.x;
   int64_t tok = 0, ranks = 0;
@@ -173,19 +199,22 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
     const int64_t c = max(ci, 0);
     int64_t n = max(ni, 0);
     int64_t all;
-    const int64_t at = tok + block_scan<int64_t>(n, tmp, &all, kThreads);
+    const int64_t at = tok + scan<int64_t>(n, tmp, &all);
     const int64_t t0 = least(at, a.n_tok);
     n = least(at + n, a.n_tok) - t0;
     tok += all;
     if (r < a.n_req) {
       a.tok_start[r] = (int)t0;
       a.length[r] = (int)least(c + n, INT32_MAX);
-      if (MAP) start[tid] = (int)t0;
+      if (MAP) {
+        start[tid] = (int)t0;
+        have[tid] = ci;
+      }
     }
     const int i0 = pages_of(c, a.page, a.table_pages);
     const int many = pages_of(c + n, a.page, a.table_pages) - i0;
     int total;
-    first[tid] = block_scan<int>(many, (int*)tmp, &total, kThreads);
+    first[tid] = scan<int>(many, (int*)tmp, &total);
     entry[tid] = i0;
     __syncthreads();
     for (int e0 = 0; e0 < total; e0 += kThreads) {
@@ -216,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
     __syncthreads();
     for (int t = tid; t < a.n_tok; t += kThreads) {
       const int r = request_of(t, a.n_req, [&](int i) { return start[i]; });
-      map_token(a, t, r, r < 0 ? 0 : start[r]);
+      map_token(a, t, r, r < 0 ? 0 : start[r], r < 0 ? 0 : have[r]);
     }
   }
 }
@@ -225,7 +254,7 @@ __global__ __launch_bounds__(256) void map_kernel(KvTables a) {
   const int t = blockIdx.x * 256 + (int)threadIdx.x;
   if (t >= a.n_tok) return;
   const int r = request_of(t, a.n_req, [&](int i) { return *gptr(a.tok_start + i); });
-  map_token(a, t, r, r < 0 ? 0 : *gptr(a.tok_start + r));
+  map_token(a, t, r, r < 0 ? 0 : *gptr(a.tok_start + r), r < 0 ? 0 : *gptr(a.cached + r));
 }
 
 // ------------------------------------------------------------------ release
@@ -244,27 +273,34 @@ __global__ __launch_bounds__(256) void release_kernel(KvRelease a, int row0) {
 
 // ------------------------------------------------------------------ reorder
 
-// Row r as an out row: its parent's entries.  As an in row: what its children
-// and its own end do to the counts; how many children it has, and the first.
+// Entry i of out row r: its parent's.
+__device__ __forceinline__ void out_entry(const KvReorder& a, int r, int i) {
+  const int p = *gptr(a.parent + r);
+  const bool real = p >= 0 && p < a.n_in;
+  const int len = real ? max(*gptr(a.length + p), 0) : 0;
+  const int pg = i < pages_of(len, a.page, a.table_pages) ? *gptr(a.table + p * a.ldt + i) : -1;
+  a.out[r * a.ldo + i] = is_page(pg, a.n_pages) ? pg : -1;
+  if (i == 0) {
+    a.length_out[r] = len;
+    a.src[r] = -1;
+    a.dst[r] = -1;
+  }
+}
+// Entry i of in row r, which has c children: what they and the row's own end do to the
+// page's count.
+__device__ __forceinline__ void in_entry(const KvReorder& a, int r, int c, int i) {
+  const int pg = *gptr(a.table + r * a.ldt + i);
+  const int used = pages_of(max(*gptr(a.length + r), 0), a.page, a.table_pages);
+  const int delta = (i < used ? c : 0) - (a.keep ? 0 : 1);
+  if (delta != 0 && is_page(pg, a.n_pages)) atomicAdd(a.refs + pg, delta);
+}
+
 __global__ __launch_bounds__(256) void rows_kernel(KvReorder a, int32_t* children, int32_t* eldest,
                                                    int row0) {
   const int r = row0 + (int)blockIdx.y, tid = threadIdx.x;
   const int at = (int)blockIdx.x * 256 + tid, step = (int)gridDim.x * 256;
-  if (r < a.n_out) {
-    const int p = *gptr(a.parent + r);
-    const bool real = p >= 0 && p < a.n_in;
-    const int len = real ? max(*gptr(a.length + p), 0) : 0;
-    const int used = pages_of(len, a.page, a.table_pages);
-    for (int i = at; i < a.table_pages; i += step) {
-      const int pg = i < used ? *gptr(a.table + p * a.ldt + i) : -1;
-      a.out[r * a.ldo + i] = is_page(pg, a.n_pages) ? pg : -1;
-    }
-    if (at == 0) {
-      a.length_out[r] = len;
-      a.src[r] = -1;
-      a.dst[r] = -1;
-    }
-  }
+  if (r < a.n_out)
+    for (int i = at; i < a.table_pages; i += step) out_entry(a, r, i);
   if (r < a.n_in) {
     __shared__ int count, eld;
     if (tid == 0) {
@@ -283,30 +319,19 @@ __global__ __launch_bounds__(256) void rows_kernel(KvReorder a, int32_t* childre
       atomicMin(&eld, e);
     }
     __syncthreads();
-    c = count;
     if (at == 0) {
-      children[r] = c;
+      children[r] = count;
       eldest[r] = eld;
     }
-    const int used = pages_of(max(*gptr(a.length + r), 0), a.page, a.table_pages);
-    const int gone = a.keep ? 0 : 1;
-    for (int i = at; i < a.table_pages; i += step) {
-      const int delta = (i < used ? c : 0) - gone;
-      if (delta == 0) continue;
-      const int pg = *gptr(a.table + r * a.ldt + i);
-      if (is_page(pg, a.n_pages)) atomicAdd(a.refs + pg, delta);
-    }
+    for (int i = at; i < a.table_pages; i += step) in_entry(a, r, count, i);
   }
 }
 
-// The pages that out rows would write next and do not own alone.
-__global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int32_t* children,
-                                                         const int32_t* eldest) {
-  __shared__ FreePages::Shared fs;
-  __shared__ int tmp[kWaves];
-  FreePages pages(fs, a.refs, a.n_pages);
+// The pages that out rows would write next and do not own alone, by one workgroup.
+// children(p), eldest(p): of in row p.
+template <typename F, typename G>
+__device__ __forceinline__ void split_rows(const KvReorder& a, FreePages& pages, int* tmp, F children, G eldest) {
   int64_t ranks = 0;
-  pages.round();
   // the entry in question of row b, or null
   auto entry = [&](int b, int& p) -> int32_t* {
     if (b >= a.n_out) return nullptr;
@@ -321,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int3
     int p = 0;
     int32_t* at = entry(b, p);
     const int pg = at ? *at : -1;
-    const bool want = pg >= 0 && (*gptr(eldest + p) != b || a.refs[pg] != *gptr(children + p));
+    const bool want = pg >= 0 && (eldest(p) != b || a.refs[pg] != children(p));
     const int got = pages.take(want, ranks, tmp);
     if (want) {
       *at = got;
@@ -342,6 +367,44 @@ __global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int3
     const int was = *gptr(a.table + p * a.ldt + (at - (a.out + b * a.ldo)));
     if (is_page(was, a.n_pages) && *at != was) atomicSub(a.refs + was, 1);
   }
+}
+
+__global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int32_t* children,
+                                                         const int32_t* eldest) {
+  __shared__ FreePages::Shared fs;
+  __shared__ int tmp[kWaves];
+  FreePages pages(fs, a.refs, a.n_pages);
+  pages.round();
+  split_rows(a, pages, tmp, [&](int p) { return *gptr(children + p); }, [&](int p) { return *gptr(eldest + p); });
+}
+
+// All of a small call in one launch.
+constexpr int kSmallRows = 1024, kSmallEntries = 4096;
+__global__ __launch_bounds__(kThreads) void small_kernel(KvReorder a) {
+  __shared__ FreePages::Shared fs;
+  __shared__ int tmp[kWaves], children[kSmallRows], eldest[kSmallRows];
+  const int tid = threadIdx.x;
+  if (tid < a.n_in) {
+    children[tid] = 0;
+    eldest[tid] = INT32_MAX;
+  }
+  __syncthreads();
+  for (int b = tid; b < a.n_out; b += kThreads) {
+    const int p = *gptr(a.parent + b);
+    if (p < 0 || p >= a.n_in) continue;
+    atomicAdd(children + p, 1);
+    atomicMin(eldest + p, b);
+  }
+  __syncthreads();
+  for (int e = tid; e < a.n_out * a.table_pages; e += kThreads) out_entry(a, e / a.table_pages, e % a.table_pages);
+  for (int e = tid; e < a.n_in * a.table_pages; e += kThreads)
+    in_entry(a, e / a.table_pages, children[e / a.table_pages], e % a.table_pages);
+  // the counts are read below by plain loads: what has been added is in the L2
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  FreePages pages(fs, a.refs, a.n_pages);
+  pages.round();
+  split_rows(a, pages, tmp, [&](int p) { return children[p]; }, [&](int p) { return eldest[p]; });
 }
 
 // ------------------------------------------------------------------ copies
@@ -399,6 +462,13 @@ hipError_t launch_kv8_release(const KvRelease& a, hipStream_t s) {
 }
 
 hipError_t launch_kv8_reorder(const KvReorder& a, int32_t* ws, hipStream_t s) {
+  // one launch while one workgroup is done with the rows in a few rounds: 4 rows of 15
+  // entries 9.3 us so, 2.6 and 7.4 in two launches; 13 rows of 10 forked to 104 10.9 us,
+  // 4.8 and 7.8
+  if (a.n_in <= kSmallRows && ((int64_t)a.n_in + a.n_out) * a.table_pages <= kSmallEntries) {
+    hipLaunchKernelGGL(small_kernel, dim3(1), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
   by_rows(std::max(a.n_in, a.n_out), [&](unsigned n, int r0) {
     hipLaunchKernelGGL(rows_kernel, dim3(std::min((a.table_pages + 255) / 256, 64), n), dim3(256), 0, s,
                        a, ws, ws + a.n_in, r0);
