@@ -35,6 +35,11 @@ struct PrefixEntries {
 struct PrefixToken {
   int32_t own, own_row, shared, shared_row;
 };
+// How a line was cut: positions a slice, and whether no item was split.
+struct PrefixSlices {
+  int64_t per;
+  int32_t whole, none;
+};
 struct PrefixPlan {
   PrefixGroup* groups;  // [n_groups]
   int32_t* live;        // [n_groups]: requests with tokens
@@ -51,7 +56,8 @@ struct PrefixSums {
 };
 struct PrefixWs {
   PrefixPlan plan;
-  PrefixToken* tokens;  // [n_tok]
+  PrefixToken* tokens;   // [n_tok]
+  PrefixSlices* slices;  // [2]: of shared keys, of own ones
   PrefixSums shared, own;
   int32_t most_shared, most_own;  // entries at most
 };

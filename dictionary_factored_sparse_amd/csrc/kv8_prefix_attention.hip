@@ -24,30 +24,26 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, Pref
       [&](int t, const PrefixToken& k) { ws.tokens[t] = k; }, tmp, longest);
 }
 
-// How a line is cut.
+// What the second kernel knows of a line.
 struct LineCut {
-  PrefixEntries plan;
+  const int64_t* first;
   PrefixSums sums;
-  int qb, extra, least, each, split;
+  int qb, extra;
 };
 
 // What one line gives for row `row` (counted from its entry's first one) of kv head
 // kh: m, l and four sums at dim d.  The parts of a split item are read by the
 // waves in turn, part u by wave u % kWaves: each returns its own share.
-__device__ __forceinline__ void line_sums(const LineCut& c, int first_entry, int row, int kh, int heads, int slices,
-                                          int64_t at, int D, int d, int wave, float& m, float& l, f4& v) {
+__device__ __forceinline__ void line_sums(const LineCut& c, const PrefixSlices& cut, int first_entry, int row, int kh,
+                                          int heads, int64_t at, int D, int d, int wave, float& m, float& l, f4& v) {
   const int e = first_entry + row / c.qb, r = row % c.qb;
-  const int n_entries = *gptr(c.plan.n), longest = *gptr(c.plan.n + 1);
-  const int64_t f0 = *gptr(c.plan.first + e), f1 = *gptr(c.plan.first + e + 1);
-  const int64_t total = *gptr(c.plan.first + n_entries);
-  const int64_t per = max((int64_t)c.least, (total + slices - 1) / slices);
+  const int64_t f0 = *gptr(c.first + e), f1 = *gptr(c.first + e + 1);
   const int64_t line = (f1 - f0) / heads, item0 = f0 + kh * line, item1 = item0 + line - c.extra;
-  const int w0 = (int)(item0 / per), w1 = (int)((item1 - 1) / per);
+  const int w0 = (int)(item0 / cut.per), w1 = (int)((item1 - 1) / cut.per);
   m = -1e30f;
   l = 0.0f;
   v = f4{0, 0, 0, 0};
-  // items that were not split: those dealt out whole, and those of one slice
-  if (longest <= c.each || w0 == w1) {
+  if (cut.whole || w0 == w1) {
     if (wave == 0) {
       const f2 w = *gptr(c.sums.ml + at);
       m = w.x;
@@ -88,27 +84,27 @@ __device__ __forceinline__ void line_sums(const LineCut& c, int first_entry, int
 // The rows of one token, 64 places of four dims a workgroup: the sums of both
 // lines, each wave's share, joined in the waves' order.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void merge_kernel(KvAttnLaunch a, const PrefixToken* tokens, LineCut shared,
-                                                         LineCut own, int slices, int wide) {
+__global__ __launch_bounds__(kThreads) void merge_kernel(KvAttnLaunch a, const PrefixToken* tokens,
+                                                         const PrefixSlices* slices, LineCut shared, LineCut own,
+                                                         int wide) {
   __shared__ f2 ml[kWaves][kWave];
   __shared__ f4 sum[kWaves][kWave];
   const int D = a.kv.head_dim, quads = D / 4, g = a.q_heads / a.kv.heads;
   const int lane = threadIdx.x % kWave, wave = uni(threadIdx.x / kWave), tok = blockIdx.x;
   const PrefixToken k = tokens[tok];
+  const PrefixSlices cut_shared = slices[0], cut_own = slices[1];
   if (k.own < 0) return;  // of no request: left as it is
   const int place = blockIdx.y * kWave + lane;
   const bool real = place < a.q_heads * quads;
   const int h = real ? place / quads : 0, d = real ? place % quads * 4 : 0, kh = h / g;
   const int64_t at = (int64_t)tok * a.q_heads + h;
-  const int n = shared_slices(*gptr(shared.plan.first + *gptr(shared.plan.n)), *gptr(own.plan.first + *gptr(own.plan.n)),
-                              *gptr(own.plan.n + 1), shared.split != 0, slices);
   float m, l;
   f4 v;
-  line_sums(own, k.own, k.own_row + h - kh * g, kh, a.kv.heads, slices - n, at, D, d, wave, m, l, v);
+  line_sums(own, cut_own, k.own, k.own_row + h - kh * g, kh, a.kv.heads, at, D, d, wave, m, l, v);
   if (k.shared >= 0) {
     float y, z;
     f4 x;
-    line_sums(shared, k.shared, k.shared_row + h - kh * g, kh, a.kv.heads, n, at, D, d, wave, y, z, x);
+    line_sums(shared, cut_shared, k.shared, k.shared_row + h - kh * g, kh, a.kv.heads, at, D, d, wave, y, z, x);
     const float top = fmaxf(m, y);
     const float fm = __builtin_amdgcn_exp2f(m - top), fy = __builtin_amdgcn_exp2f(y - top);
     l = l * fm + z * fy;
@@ -196,6 +192,7 @@ size_t place(char* base, const dfs_kv8& kv, int32_t q_heads, const Sizes& s, Pre
   w->plan.pos = p.take<int32_t>(s.n_tok);
   *scratch = p.take<int32_t>(2 * s.n_req + s.n_groups);
   w->tokens = p.take<PrefixToken>(s.n_tok);
+  w->slices = p.take<PrefixSlices>(2);
   place_entries(p, w->plan.shared, s.most_shared);
   place_entries(p, w->plan.own, s.most_own);
   const int64_t rows = s.n_tok * q_heads;
@@ -255,15 +252,15 @@ hipError_t launch_kv8_prefix_attention(const KvAttnLaunch& a, int32_t n_groups, 
   else if (a.kv.head_dim == 96) launch_prefix<96>(p, w, c, s);
   else if (a.kv.head_dim == 128) launch_prefix<128>(p, w, c, s);
   else launch_prefix<256>(p, w, c, s);
-  const LineCut shared_cut = {w.plan.shared, w.shared, c.qb, extra, c.split ? kWaves : 1, 0, c.split};
-  const LineCut own_cut = {w.plan.own, w.own, 16 * c.nq_own, Turns::kExtra, kWaves, kPrefixEach, 1};
+  const LineCut shared_cut = {w.plan.shared.first, w.shared, c.qb, extra};
+  const LineCut own_cut = {w.plan.own.first, w.own, 16 * c.nq_own, Turns::kExtra};
   const int wide = (uintptr_t)a.O % (a.odt == DFS_F32 ? 16 : 8) == 0 && a.ldo % 4 == 0;
   const dim3 grid(a.b.n_tok, (a.q_heads * (a.kv.head_dim / 4) + kWave - 1) / kWave);
   if (a.odt == DFS_F32)
-    hipLaunchKernelGGL(merge_kernel<float>, grid, dim3(kThreads), 0, s, a, w.tokens, shared_cut, own_cut, c.slices,
+    hipLaunchKernelGGL(merge_kernel<float>, grid, dim3(kThreads), 0, s, a, w.tokens, w.slices, shared_cut, own_cut,
                        wide);
   else
-    hipLaunchKernelGGL(merge_kernel<_Float16>, grid, dim3(kThreads), 0, s, a, w.tokens, shared_cut, own_cut, c.slices,
+    hipLaunchKernelGGL(merge_kernel<_Float16>, grid, dim3(kThreads), 0, s, a, w.tokens, w.slices, shared_cut, own_cut,
                        wide);
   return hipGetLastError();
 }

@@ -128,12 +128,8 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
         },
         lds.tmp, lds.longest);
     if (blockIdx.x == 0) {  // what the second kernel reads of it
-      for (int l = 0; l < 2; ++l) {
-        const PrefixInline::Entries& e = l ? lds.line_own : lds.line_shared;
-        const PrefixEntries& f = l ? ws.plan.own : ws.plan.shared;
-        for (int i = tid; i <= e.n[0]; i += kThreads) f.first[i] = e.first[i];
-        if (tid < 2) f.n[tid] = e.n[tid];
-      }
+      for (int i = tid; i <= lds.line_shared.n[0]; i += kThreads) ws.plan.shared.first[i] = lds.line_shared.first[i];
+      for (int i = tid; i <= lds.line_own.n[0]; i += kThreads) ws.plan.own.first[i] = lds.line_own.first[i];
     }
   }
   auto length = [&](const PrefixInline::Entries& e, const PrefixEntries& f) {
@@ -142,6 +138,14 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
   const int n = shared_slices(length(lds.line_shared, ws.plan.shared), length(lds.line_own, ws.plan.own),
                               in ? lds.line_own.n[1] : *gptr(ws.plan.own.n + 1), SPLIT, slices);
   const int slice = blockIdx.x;
+  if (slice == 0 && threadIdx.x < 2) {  // for the second kernel
+    const bool own = threadIdx.x != 0;
+    const int64_t total = own ? length(lds.line_own, ws.plan.own) : length(lds.line_shared, ws.plan.shared);
+    const int longest = own ? (in ? lds.line_own.n[1] : *gptr(ws.plan.own.n + 1)) : INT32_MAX;
+    const int of = max(own ? slices - n : n, 1);
+    ws.slices[threadIdx.x] = {max((int64_t)(own || SPLIT ? kWaves : 1), (total + of - 1) / of),
+                              longest <= kPrefixEach, 0};
+  }
   if (slice < n) {
     P t(a, at, ws.shared);
     run_line(t, sh.p, line_of(ws.shared), t.entries(), SPLIT ? kWaves : 1, slice, n);
