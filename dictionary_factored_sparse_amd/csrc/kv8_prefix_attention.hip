@@ -8,20 +8,47 @@
 namespace dfs {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
+
+// The plan of a batch that is too large for every workgroup to make its own.  Up
+// to kPlanNear requests what it looks up again and again is in LDS.
+constexpr int kPlanNear = 1024;
+struct PlanNear {
+  Req facts[kPlanNear];
+  PrefixGroup groups[kPlanNear];
+  int32_t group_start[kPlanNear + 1], shared[kPlanNear], live[kPlanNear];
+  int32_t group_of[kPlanNear], first_entry[kPlanNear], first_shared[kPlanNear];
+};
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, PrefixWs ws, int32_t* scratch, int qb,
                                                             int extra, int qb_own, int extra_own) {
   __shared__ Scan3 tmp[kPlanThreads / kWave];
   __shared__ int longest[2];
-  const int n = p.a.b.n_req;
+  __shared__ PlanNear lds;
+  const int n = p.a.b.n_req, tid = threadIdx.x;
+  auto put = [&](int t, const PrefixToken& k) { ws.tokens[t] = k; };
+  if (n <= kPlanNear) {  // n_groups <= n_req
+    PrefixPlan w = ws.plan;
+    w.groups = lds.groups;
+    w.live = lds.live;
+    for (int i = tid; i <= p.n_groups; i += kPlanThreads) lds.group_start[i] = *gptr(p.group_start + i);
+    for (int i = tid; i < p.n_groups; i += kPlanThreads) lds.shared[i] = *gptr(p.shared + i);
+    for (int i = tid; i < n; i += kPlanThreads) lds.facts[i] = get_req(p.a.b, p.a.kv.page, i);
+    clear_prefix_plan<kPlanThreads>(p, w, [&](int i) { return *gptr(p.group_start + i); }, longest);
+    __syncthreads();
+    make_prefix_plan<kPlanThreads>(
+        p, w, [&](int r) { return lds.facts[r]; }, [&](int i) { return lds.group_start[i]; },
+        [&](int i) { return lds.shared[i]; }, lds.group_of, lds.first_entry, lds.first_shared, ws.most_shared,
+        ws.most_own, qb, extra, qb_own, extra_own, put, tmp, longest);
+    for (int i = tid; i < p.n_groups; i += kPlanThreads) ws.plan.groups[i] = lds.groups[i];
+    return;
+  }
   clear_prefix_plan<kPlanThreads>(p, ws.plan, [&](int i) { return *gptr(p.group_start + i); }, longest);
   __syncthreads();
   make_prefix_plan<kPlanThreads>(
       p, ws.plan, [&](int r) { return get_req(p.a.b, p.a.kv.page, r); },
       [&](int i) { return *gptr(p.group_start + i); }, [&](int i) { return *gptr(p.shared + i); }, scratch,
-      scratch + n, scratch + 2 * n, ws.most_shared, ws.most_own, qb, extra, qb_own, extra_own,
-      [&](int t, const PrefixToken& k) { ws.tokens[t] = k; }, tmp, longest);
+      scratch + n, scratch + 2 * n, ws.most_shared, ws.most_own, qb, extra, qb_own, extra_own, put, tmp, longest);
 }
 
 // What the second kernel knows of a line.
@@ -146,7 +173,11 @@ PrefixCut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_hea
   PrefixCut c;
   const int64_t rows = (int64_t)n_tok * (q_heads / kv.heads);
   c.nq_own = rows <= 16 * (int64_t)n_req ? 1 : 2;
-  c.split = rows <= 32 * (int64_t)n_groups;
+  // Up to 64 rows a group the waves take the tiles in turn: 16 requests of 3 tokens
+  // with 48 rows to a group of heads of 64 dims 40 us, 48 where each wave has rows of its
+  // own; a document asked by 24 requests 64 us with 60 rows, and with 65 rows 71 in rows of
+  // their own.
+  c.split = rows <= 64 * (int64_t)n_groups;
   c.nq = c.split && rows <= 16 * (int64_t)n_groups && c.nq_own == 1 ? 1 : 2;
   c.qb = c.split ? 16 * c.nq : 16 * c.nq * kWaves;
   c.slices = kv.head_dim == 256 ? 256 : 512;  // as many workgroups as the device holds at once

@@ -29,7 +29,7 @@ __device__ __forceinline__ Scan3 block_scan3(const Scan3& x, Scan3* tmp, Scan3& 
   all = {};
 #pragma unroll
   for (int i = 0; i < 3; ++i) s.v[i] -= x.v[i];
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < T / kWave; ++w) {
     const Scan3 u = tmp[w];
 #pragma unroll
@@ -206,11 +206,13 @@ __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const Pr
     const Req q = facts(lo);
     w.pos[t] = q.len - q.n + (t - q.t0);
     PrefixToken k = {-1, 0, -1, 0};
-    if (t >= q.t0 && t < q.t0 + q.n) {
+    // an entry past the last place is not there (starts that do not ascend can want more)
+    auto there = [&](int e, int rows, int of, int most) { return e + (rows + of - 1) / of <= most; };
+    if (t >= q.t0 && t < q.t0 + q.n && there(entry_own[lo], q.n * (int)g, qb_own, most_own)) {
       k.own = entry_own[lo];
       k.own_row = (t - q.t0) * (int)g;
       const int i = group_of[lo];
-      if (i >= 0 && w.groups[i].keys > 0) {
+      if (i >= 0 && w.groups[i].keys > 0 && there(entry_shared[i], w.groups[i].n * (int)g, qb, most_shared)) {
         k.shared = entry_shared[i];
         k.shared_row = (t - w.groups[i].t0) * (int)g;
       }

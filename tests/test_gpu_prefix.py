@@ -199,6 +199,21 @@ def test_many_requests_and_groups():
     check(c, np.minimum(lengths, rng.integers(0, 4, 1200)), lengths, 8, "f16", groups, shared)
 
 
+@pytest.mark.parametrize("n,new", [(128, 1), (129, 1), (85, 3), (86, 3), (512, 1), (513, 1),
+                                   (1024, 1), (1025, 1)])
+def test_batches_at_the_sizes_where_the_plan_changes(n, new):
+    """Each workgroup's own plan and one for all of them, from what is in LDS and from memory."""
+    rng = np.random.default_rng(n)
+    groups = np.concatenate([[0], np.sort(rng.integers(0, n + 1, n // 5)), [n]])
+    prefix = rng.integers(0, 150, len(groups) - 1)
+    lengths = np.zeros(n, int)
+    for g, (r0, r1) in enumerate(zip(groups, groups[1:])):
+        lengths[r0:r1] = prefix[g] + rng.integers(new, 20, r1 - r0)
+    c = shared_cache(rng, "int8", 2, 64, 16, groups, lengths, prefix)
+    check(c, [new] * n, lengths, 4, "f16", groups, prefix // 16 * 16)
+    check(c, rng.integers(0, new + 1, n), lengths, 1, "f32", groups, prefix // 16 * 16, window=70, sinks=2)
+
+
 def test_long_prefix_and_long_tails():
     rng = np.random.default_rng(10)
     lengths = [9000, 6100, 6050, 6047, 40, 7000]
