@@ -1001,7 +1001,7 @@ dfs_status kv8_release(int32_t n_req, int32_t n_pages, int32_t* refs, int32_t* t
                        int32_t table_pages, const int32_t* first, const int32_t* last,
                        void* stream) {
   DFS_TRY(check_pool(16, n_pages, refs));
-  DFS_TRY(check_rows(n_req, table, ldt, table_pages, 1));
+  DFS_TRY(check_rows(n_req, table, ldt, table_pages, 16));
   if (!aligned4({first, last})) return DFS_E_ALIGN;
   if (n_req == 0) return DFS_OK;
   const KvRelease a = {n_req, n_pages, refs, table, ldt, table_pages, first, last};

@@ -261,7 +261,7 @@ __global__ __launch_bounds__(256) void map_kernel(KvTables a) {
 
 __global__ __launch_bounds__(256) void release_kernel(KvRelease a, int row0) {
   const int r = row0 + (int)blockIdx.y;
-  const int i0 = a.first ? max(*gptr(a.first + r), 0) : 0;
+  const int i0 = a.first ? min(max(*gptr(a.first + r), 0), a.table_pages) : 0;  // the sums below stay in 32 bits
   const int i1 = a.last ? min(*gptr(a.last + r), a.table_pages) : a.table_pages;
   for (int i = i0 + (int)(blockIdx.x * 256 + threadIdx.x); i < i1; i += (int)gridDim.x * 256) {
     int32_t* p = a.table + r * a.ldt + i;

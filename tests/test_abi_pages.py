@@ -51,6 +51,7 @@ def test_release_validation():
         assert _release(**change) == status, change
     for change, status in ((dict(n_req=-1), INVALID), (dict(n_req=65536), RANGE),
                            (dict(pages=0), INVALID), (dict(ldt=3), INVALID),
+                           (dict(pages=1 << 27, ldt=1 << 27), RANGE),
                            (dict(table=None), INVALID), (dict(table=P + 2), ALIGN),
                            (dict(first=P + 1), ALIGN), (dict(last=P + 2), ALIGN)):
         assert _release(**change) == status, change

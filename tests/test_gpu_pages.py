@@ -126,6 +126,19 @@ def test_release(rows, width):
         same(t, wt, "table")
 
 
+def test_release_of_any_entries():
+    """first and last are clamped to the row, whatever they are."""
+    ends = [-2 ** 31, -1, 0, 299, 300, 301, 2 ** 31 - 300, 2 ** 31 - 1]
+    first, last = (np.repeat(ends, 8), np.tile(ends, 8))
+    table = np.arange(64 * 300).reshape(64, 300)
+    refs = np.ones(64 * 300, np.int64)
+    r, t = ints(refs), ints(table)
+    B.kv8_release(r, t, ints(first), ints(last))
+    R.release(refs, table, first, last)
+    same(r, refs, "refs")
+    same(t, table, "table")
+
+
 @pytest.mark.parametrize("keep", [False, True])
 @pytest.mark.parametrize("n_in,n_out,page,length,width,spare", [
     (1, 1, 16, 5, 3, 0), (1, 4, 64, 777, 20, 9), (4, 4, 16, 100, 12, 3), (8, 8, 128, 2000, 30, 40),
