@@ -989,8 +989,10 @@ dfs_status kv8_tables(int32_t n_req, int32_t page, int32_t n_pages, int32_t* ref
   if (!aligned4({cached, n_new, tok_start, length, tok_req, tok_pos, missing}) ||
       (uintptr_t)slot % 8 != 0)
     return DFS_E_ALIGN;
-  if (overlap(length, n_req, cached, n_req) || overlap(length, n_req, n_new, n_req))
-    return DFS_E_INVALID;
+  for (const int32_t* in : {cached, n_new})
+    if (overlap(length, n_req, in, n_req) || overlap(tok_start, n_req + 1, in, n_req) ||
+        overlap(missing, 1, in, n_req))
+      return DFS_E_INVALID;
   const KvTables a = {n_req, n_tok,       page,      n_pages, refs,    cached,  n_new, table,
                       ldt,   table_pages, tok_start, length,  tok_req, tok_pos, slot,  missing};
   DFS_HIP(launch_kv8_tables(a, (hipStream_t)stream));
@@ -1029,8 +1031,12 @@ dfs_status kv8_reorder(int32_t n_in, int32_t n_out, int32_t page, int32_t n_page
     return DFS_E_INVALID;
   if (!aligned4({length, parent, length_out, src, dst, missing})) return DFS_E_ALIGN;
   if (n_in > 0 && n_out > 0 &&
-      (overlap(table, (n_in - 1) * ldt + table_pages, table_out, (n_out - 1) * ldo + table_pages) ||
-       overlap(length, n_in, length_out, n_out) || overlap(parent, n_out, length_out, n_out)))
+      overlap(table, (n_in - 1) * ldt + table_pages, table_out, (n_out - 1) * ldo + table_pages))
+    return DFS_E_INVALID;
+  for (const int32_t* out : {length_out, src, dst})
+    if (overlap(out, n_out, length, n_in) || overlap(out, n_out, parent, n_out)) return DFS_E_INVALID;
+  if (overlap(src, n_out, dst, n_out) || overlap(src, n_out, length_out, n_out) ||
+      overlap(dst, n_out, length_out, n_out))
     return DFS_E_INVALID;
   const size_t need = (size_t)n_in * 8;
   if (need > 0) {
@@ -1100,9 +1106,13 @@ dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* 
       !aligned4({score, done, norm, parent, token, score_out, done_out}))
     return DFS_E_ALIGN;
   const int64_t rows = (int64_t)n_req * width;
-  for (const void* out : {(const void*)parent, (const void*)token, (const void*)score_out, (const void*)done_out})
+  const void* outs[] = {parent, token, score_out, done_out};
+  for (int i = 0; i < 4; ++i) {
     for (const void* in : {(const void*)score, (const void*)done, (const void*)norm})
-      if (overlap(out, rows, in, rows)) return DFS_E_INVALID;
+      if (overlap(outs[i], rows, in, rows)) return DFS_E_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], rows, outs[j], rows)) return DFS_E_INVALID;
+  }
   DFS_TRY(check_ws(ws, ws_bytes, beam_ws_need(n_req, width, vocab, dtype)));
   const BeamLaunch a = {n_req, width, vocab,  logits, dtype,     ldl,     score,
                         done,  norm,  eos,    parent, token,     score_out, done_out};

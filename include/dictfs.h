@@ -556,7 +556,7 @@ dfs_status kv8_prefix_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok,
  * (int32, device; negative counts as 0).  With n the new tokens that still fit
  * the batch's n_tok rows, in order of requests:
  *   tok_start[n_req+1]: the requests' first rows, and the end of the last's;
- *   length[r] = cached[r] + n  (must not overlap cached);
+ *   length[r] = cached[r] + n  (nothing written may overlap cached or n_new);
  *   table: entries cached/page (rounded up) .. length/page (rounded up) - 1, as
  *     far as the row's table_pages go, that name no page get the lowest free
  *     page, whose count becomes 1; entries that name one keep it, so that the
@@ -598,8 +598,8 @@ dfs_status kv8_reorder_workspace_size(int32_t n_in, size_t* bytes);
  * from and to (-1, -1 for rows that need no copy).  Copy them before anything is
  * written (kv8_copy_pages with length_out, for each layer's cache).  missing[1]
  * counts rows that got no page because none was free; their entry is -1.
- * table_out must not overlap table; ws as for kv8_reorder_workspace_size,
- * 16-byte aligned. */
+ * Nothing written may overlap what is read or another output; ws as for
+ * kv8_reorder_workspace_size, 16-byte aligned. */
 dfs_status kv8_reorder(int32_t n_in, int32_t n_out, int32_t page, int32_t n_pages, int32_t* refs,
                        const int32_t* table, int64_t ldt, const int32_t* length,
                        const int32_t* parent, int32_t keep, int32_t* table_out, int64_t ldo,
@@ -640,8 +640,8 @@ dfs_status beam_select_workspace_size(int32_t n_req, int32_t width, int32_t voca
  * Exponentials and the sums of two of them are fp32, all other sums and the totals
  * 64 bits.
  * 1 <= width <= 32, n_req * width <= 8192, vocab <= 2^30 (DFS_E_RANGE).
- * Outputs must not overlap inputs.  The workspace's first 64 KiB must be zero
- * before its first use; every call leaves them zero again.  Calls sharing a
+ * Outputs must not overlap inputs or each other.  The workspace's first 64 KiB must
+ * be zero before its first use; every call leaves them zero again.  Calls sharing a
  * workspace must not run concurrently. */
 dfs_status beam_select(int32_t n_req, int32_t width, int32_t vocab, const void* logits,
                        int32_t dtype, int64_t ldl, const float* score, const int32_t* done,

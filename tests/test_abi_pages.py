@@ -16,7 +16,7 @@ BAD_PAGES = [(dict(page=0), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(pa
 
 
 def _tables(n_req=2, page=64, n_pages=8, refs=P, cached=P, new=P, n_tok=3, table=P, ldt=4, pages=4,
-            start=P, length=2 * P, req=P, pos=P, slot=P, missing=None):
+            start=5 * P, length=2 * P, req=P, pos=P, slot=P, missing=None):
     """Every default but missing is fine."""
     return B.lib().kv8_tables(n_req, page, n_pages, refs, cached, new, n_tok, table, ldt, pages,
                               start, length, req, pos, slot, missing, None)
@@ -25,7 +25,7 @@ def _tables(n_req=2, page=64, n_pages=8, refs=P, cached=P, new=P, n_tok=3, table
 def test_tables_validation():
     assert _tables() == INVALID                    # every other check passes: see missing below
     for change, status in BAD_POOLS + BAD_PAGES:
-        assert _tables(missing=P, **change) == status, change
+        assert _tables(missing=6 * P, **change) == status, change
     for change, status in ((dict(n_req=-1), INVALID), (dict(n_req=65536), RANGE),
                            (dict(n_tok=-1), INVALID), (dict(pages=0), INVALID),
                            (dict(ldt=3), INVALID), (dict(pages=1 << 25, ldt=1 << 25), RANGE),
@@ -36,10 +36,11 @@ def test_tables_validation():
                            (dict(start=P + 2), ALIGN), (dict(length=P + 3), ALIGN),
                            (dict(req=P + 2), ALIGN), (dict(pos=P + 2), ALIGN),
                            (dict(slot=P + 4), ALIGN), (dict(missing=P + 2), ALIGN)):
-        assert _tables(**{"missing": P, **change}) == status, change
-    assert _tables(missing=P, length=P) == INVALID           # over cached or n_new
-    assert _tables(missing=P, cached=3 * P, length=P + 4) == INVALID
-    assert _tables(missing=P, new=3 * P, length=P - 4) == INVALID
+        assert _tables(**{"missing": 6 * P, **change}) == status, change
+    for out, n in (("length", 2), ("start", 3), ("missing", 1)):      # over cached or n_new
+        for at in (P - 4 * (n - 1), P, P + 4):
+            assert _tables(**{"missing": 6 * P, "new": 3 * P, out: at}) == INVALID, (out, at)
+            assert _tables(**{"missing": 6 * P, "cached": 3 * P, out: at}) == INVALID, (out, at)
 
 
 def _release(n_req=2, n_pages=8, refs=P, table=P, ldt=4, pages=4, first=P, last=P):
@@ -59,7 +60,7 @@ def test_release_validation():
 
 
 def _reorder(n_in=2, n_out=3, page=64, n_pages=8, refs=P, table=P, ldt=4, length=P, parent=P, keep=0,
-             out=2 * P, ldo=4, pages=4, length_out=3 * P, src=P, dst=P, missing=P, ws=P, ws_bytes=15):
+             out=2 * P, ldo=4, pages=4, length_out=3 * P, src=4 * P, dst=5 * P, missing=P, ws=P, ws_bytes=15):
     """Every default but ws_bytes is fine."""
     return B.lib().kv8_reorder(n_in, n_out, page, n_pages, refs, table, ldt, length, parent, keep,
                                out, ldo, pages, length_out, src, dst, missing, ws, ws_bytes, None)
@@ -83,7 +84,13 @@ def test_reorder_validation():
                            (dict(length_out=P + 2), ALIGN), (dict(src=P + 2), ALIGN),
                            (dict(dst=P + 1), ALIGN), (dict(missing=P + 2), ALIGN)):
         assert _reorder(**change) == status, change
-    assert _reorder(length_out=P) == INVALID and _reorder(length_out=P + 4) == INVALID
+    for out in ("length_out", "src", "dst"):       # over what is read, and each other
+        for at in (P, P + 4, P - 8):
+            assert _reorder(**{"parent": 9 * P, out: at}) == INVALID, (out, at)
+            assert _reorder(**{"length": 9 * P, out: at}) == INVALID, (out, at)
+        assert _reorder(**{out: 8 * P}) == WORKSPACE
+    assert _reorder(src=5 * P + 8) == INVALID and _reorder(dst=3 * P) == INVALID
+    assert _reorder(src=3 * P - 8) == INVALID
     # rows that overlap: in place, and by one entry at either end
     assert _reorder(out=P) == INVALID
     assert _reorder(out=P + 4 * 7) == INVALID and _reorder(out=P + 4 * 8) == WORKSPACE
@@ -120,7 +127,7 @@ def test_copy_validation():
 
 
 def _beam(n_req=2, width=4, vocab=100, logits=P, dt=B.DFS_F16, ldl=100, score=P, done=P, norm=P, eos=2,
-          parent=2 * P, token=2 * P, score_out=2 * P, done_out=2 * P, ws=P, ws_bytes=16):
+          parent=2 * P, token=3 * P, score_out=4 * P, done_out=5 * P, ws=P, ws_bytes=16):
     """Every default but ws_bytes is fine."""
     return B.lib().beam_select(n_req, width, vocab, logits, dt, ldl, score, done, norm, eos, parent,
                                token, score_out, done_out, ws, ws_bytes, None)
@@ -147,6 +154,9 @@ def test_beam_validation():
         assert _beam(**change) == status, change
     for name in ("parent", "token", "score_out", "done_out"):
         assert _beam(**{name: P}) == INVALID and _beam(**{name: P + 28}) == INVALID
+    for a, b in ((dict(token=2 * P + 28), dict(token=2 * P + 32)), (dict(score_out=2 * P), dict(score_out=6 * P)),
+                 (dict(done_out=4 * P - 28), dict(done_out=4 * P - 32))):
+        assert _beam(**a) == INVALID and _beam(**b) == WORKSPACE
     assert _beam(done=None, eos=-1) == WORKSPACE and _beam(done_out=None, norm=None) == WORKSPACE
     assert _beam(logits=P + 2) == WORKSPACE        # f16 logits at any element
     assert _beam(n_req=0, logits=None) == OK

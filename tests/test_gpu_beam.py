@@ -146,6 +146,37 @@ def test_masked_and_infinite_logits(dt):
     assert (wt[2 * width:3 * width] == -1).all()
 
 
+@pytest.mark.parametrize("order", ["up", "down", "saw", "peak", "steps"])
+@pytest.mark.parametrize("width,vocab", [(2, 40000), (32, 140000)])
+def test_logits_in_order(order, width, vocab):
+    """Every element above all before it, the best ones all in one piece, pieces of equal values:
+    lists that fill, whose bounds have to rise."""
+    rng = np.random.default_rng(width)
+    at = np.arange(vocab, dtype=np.float64)
+    x = {"up": at / vocab * 20, "down": -at / vocab * 20, "saw": at % 4099 / 200,
+         "peak": -np.abs(at - vocab / 3) / 500, "steps": at // 700 / 10}[order]
+    rows = 3 * width
+    x = np.repeat(x[None], rows, 0).astype(np.float32)
+    x[2 * width:] += 0.01 * rng.standard_normal((width, vocab)).astype(np.float32)
+    score = np.zeros(rows, np.float32)
+    score[width:] = -rng.random(2 * width).astype(np.float32)
+    for dt in (np.float32, np.float16):
+        say(f"case: logits in order, {order} width={width} {dt.__name__}")
+        got = B.beam_select(dev(x.astype(dt)), dev(score), width)
+        check(x.astype(dt), score, width, got=got)
+
+
+def test_rows_past_32_bits():
+    say("case: beams over rows of 2.4 GB")
+    rng = np.random.default_rng(8)
+    wide = torch.empty((4, 600_000_000), dtype=torch.float32, device=DEV)
+    x = (3 * rng.standard_normal((4, 5000))).astype(np.float32)
+    wide[:, :5000] = dev(x)
+    score = -rng.random(4).astype(np.float32)
+    got = B.beam_select(wide[:, :5000], dev(score), 4)
+    check(x, score, 4, got=got)
+
+
 def test_close_totals_of_different_rows():
     """Rows whose best totals differ by 2^-18 (sixteen times what a sum may err by), the
     probabilities spread over the whole vocabulary."""

@@ -143,7 +143,10 @@ def test_release_of_any_entries():
 @pytest.mark.parametrize("n_in,n_out,page,length,width,spare", [
     (1, 1, 16, 5, 3, 0), (1, 4, 64, 777, 20, 9), (4, 4, 16, 100, 12, 3), (8, 8, 128, 2000, 30, 40),
     (13, 104, 32, 300, 25, 200), (104, 13, 32, 300, 25, 1), (1500, 1100, 16, 60, 7, 300),
-    (6, 9, 16, 40, 2, 50), (5, 2000, 16, 33, 4, 3000)])
+    (6, 9, 16, 40, 2, 50), (5, 2000, 16, 33, 4, 3000),
+    # at the ends of what one launch takes
+    (1024, 1024, 16, 20, 2, 900), (1024, 1025, 16, 20, 2, 900), (1025, 1, 16, 20, 3, 5), (2, 2, 64, 900, 1024, 3),
+    (2, 2, 64, 900, 1025, 3)])
 def test_reorder(n_in, n_out, page, length, width, spare, keep):
     rng = np.random.default_rng(n_in * 31 + n_out)
     lens = rng.integers(-2, length + 1, n_in)
@@ -193,3 +196,24 @@ def test_copy_pages(kind, heads, dim, page, layers):
             R.copy_pages(*h, src, dst, length)
             for t, w in zip((kv.k, kv.v, kv.kscale, kv.vscale), h):
                 same(t, w, "cache")
+
+
+def test_copies_past_32_bits():
+    """Caches of more than 4 GiB: pages at either end, and between them."""
+    say("case: copies over 4 GiB")
+    n, heads, dim, page = 33000, 8, 128, 128
+    kv = B.DeviceKV8.empty(n, heads, dim, page, "int8", DEV)
+    assert kv.k.numel() > 2 ** 32
+    rng = np.random.default_rng(3)
+    src, dst = [0, n - 1, 17000, 5], [n - 2, 1, n - 3, 32900]
+    want = []
+    for s in src:
+        for t in (kv.k, kv.v):
+            t[s] = torch.from_numpy(rng.integers(0, 256, t[s].shape).astype(np.uint8)).to(DEV)
+        kv.kscale[s] = torch.from_numpy(rng.random(heads).astype(np.float32)).to(DEV)
+        kv.vscale[s] = torch.from_numpy(rng.random(heads).astype(np.float32)).to(DEV)
+        want.append([t[s].clone() for t in (kv.k, kv.v, kv.kscale, kv.vscale)])
+    B.kv8_copy_pages([kv], ints(src), ints(dst))
+    for s, d, w in zip(src, dst, want):
+        for t, x in zip((kv.k, kv.v, kv.kscale, kv.vscale), w):
+            assert torch.equal(t[s], x) and torch.equal(t[d], x)

@@ -276,3 +276,24 @@ def test_one_workspace_for_every_smaller_batch():
             sub = Cache.__new__(Cache)
             sub.__dict__.update(c.__dict__, table=c.table[r0:r1], tab=c.tab[r0:r1])
             check(sub, n, lengths[r0:r1], H // 2, "f16", groups, [256] * (len(groups) - 1), ws=ws)
+
+
+def test_pages_past_32_bits():
+    """A cache of more than 4 GiB whose pages lie at its end: the same as in a small one."""
+    say("case: prefix over 4 GiB")
+    rng = np.random.default_rng(31)
+    lengths = [700, 650, 660]
+    c = shared_cache(rng, "int8", 8, 128, 128, [0, 3], lengths, [640])
+    n, far = c.kv.k.shape[0], 33000
+    kv = B.DeviceKV8.empty(far, 8, 128, 128, "int8", DEV)
+    assert kv.k[:far - n].numel() > 2 ** 32
+    for big, small in zip((kv.k, kv.v, kv.kscale, kv.vscale), (c.kv.k, c.kv.v, c.kv.kscale, c.kv.vscale)):
+        big[far - n:] = small
+    table = torch.where(c.tab >= 0, c.tab + (far - n), -1)
+    q = torch.randn(3, 16 * 128, device=DEV).half()
+    for new in ([1, 1, 1], [1, 2, 0]):
+        args = (ints(np.concatenate([[0], np.cumsum(new)])), ints(lengths))
+        for groups, shared in (([0, 3], [640]), ([0], [])):
+            a = B.kv8_prefix_attention(c.kv, q, *args, c.tab, ints(groups), ints(shared), 16)
+            b = B.kv8_prefix_attention(kv, q, *args, table, ints(groups), ints(shared), 16)
+            assert torch.equal(a, b)

@@ -262,3 +262,24 @@ def test_on_a_stream_given_by_argument():
         kv.v.copy_(v0)
         for x, y in zip(want, calls(side)):
             assert torch.equal(x, y)
+
+
+def test_two_streams_at_once():
+    """Steps of two servers on streams of their own, each with its own workspaces, side by side."""
+    mix = [Server("fp8", [37, 80], 4, n_pages=90), Server("int8", [100, 5, 64], 5, n_pages=140)]
+    alone = [Server("fp8", [37, 80], 4, n_pages=90), Server("int8", [100, 5, 64], 5, n_pages=140)]
+    say("case: two streams at once")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, st in zip(mix, streams):
+            with torch.cuda.stream(st):
+                s.step()
+    torch.cuda.synchronize()
+    for s in alone:
+        for _ in range(20):
+            s.step()
+    for a, b in zip(mix, alone):
+        assert torch.equal(a.refs, b.refs) and torch.equal(a.tables[a.now], b.tables[b.now])
+        assert torch.equal(a.cached, b.cached) and torch.equal(a.tokens, b.tokens)
+        assert torch.equal(a.score, b.score) and torch.equal(a.done, b.done)
