@@ -188,8 +188,10 @@ def _tensors(x):
 def _on(stream, fn, *args, **kw):
     """fn(*args) with ``stream`` as the current stream: workspaces and outputs that it makes are
     allocated and cleared in the order of that stream's work, and a workspace is not handed out
-    again while that work still uses it.  The output may be used on the caller's stream."""
-    for t in _tensors(args):
+    again while that work still uses it, nor is an input that the caller lets go of.  The output
+    may be used on the caller's stream."""
+    given = list(_tensors((args, tuple(kw.values()))))
+    for t in given:
         if t.device != stream.device:
             raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
     before = torch.cuda.current_stream(stream.device)
@@ -197,6 +199,8 @@ def _on(stream, fn, *args, **kw):
         return fn(*args, **kw)
     with torch.cuda.stream(stream):
         out = fn(*args, **kw)
+    for t in given:
+        t.record_stream(stream)
     for t in _tensors(out):
         t.record_stream(before)
     return out

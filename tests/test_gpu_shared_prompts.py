@@ -235,7 +235,7 @@ def test_on_a_stream_given_by_argument():
         refs = torch.zeros(40, dtype=torch.int32, device=DEV)
         table = torch.full((4, 8), -1, dtype=torch.int32, device=DEV)
         out = torch.full((4, 8), -1, dtype=torch.int32, device=DEV)
-        cached, new = ints([0, 0, 0, 0]), ints([50, 100, 37, 96])
+        cached, new, ones = ints([0, 0, 0, 0]), ints([50, 100, 37, 96]), ints([1, 1, 1, 1])
         torch.cuda.synchronize()
         if stream is not None:
             junk = [torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
@@ -249,7 +249,7 @@ def test_on_a_stream_given_by_argument():
         o = B.kv8_prefix_attention(kv, q, ints(range(5)), got[0], out, ints([0, 2, 4]),
                                    ints([64, 0]), HEADS * GROUP, stream=stream)
         beams = B.beam_select(logits, score, 4, stream=stream)
-        B.kv8_release(refs, out, got[0] * 0 + 1, stream=stream)
+        B.kv8_release(refs, out, ones, stream=stream)
         (torch.cuda.current_stream() if stream is None else stream).synchronize()
         return [b.tok_start, b.tok_pos, b.slot, *got, o, *beams, refs, out]
 
@@ -262,6 +262,23 @@ def test_on_a_stream_given_by_argument():
         kv.v.copy_(v0)
         for x, y in zip(want, calls(side)):
             assert torch.equal(x, y)
+
+
+def test_an_input_let_go_of_is_kept_for_its_stream():
+    """What a call on another stream reads is not handed out again before that call has run."""
+    say("case: temporary inputs on a stream given by argument")
+    table, length = ints(np.arange(32).reshape(4, 8)), ints([50, 100, 37, 96])
+    refs, out = ints([1] * 40), ints(np.full((4, 8), -1))
+    big = torch.randn(4096, 4096, device=DEV).half()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big @ big
+    got = B.kv8_reorder(refs, PAGE, table, length, ints([1, 1, 0, 3]), out, stream=side)
+    others = [ints([3, 3, 3, 3]) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert got[0].tolist() == [100, 100, 50, 96] and len(others) == 8
 
 
 def test_two_streams_at_once():
