@@ -27,29 +27,55 @@ __device__ __forceinline__ int pages_of(int64_t len, int page, int most) {
   return (int)least((len + page - 1) / page, most);
 }
 
-// Sum of v over the threads before this one, and over all of them.  The waves' sums
-// are added by the lanes of each wave.
-template <typename T>
-__device__ __forceinline__ T scan(T v, T* tmp, T* total) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  T x = v;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const T y = __shfl_up(x, o, kWave);
-    x += lane >= o ? y : 0;
-  }
-  if (lane == kWave - 1) tmp[wave] = x;
-  __syncthreads();
-  T w = tmp[lane % kWaves];
-#pragma unroll
-  for (int o = 1; o < kWaves; o <<= 1) {
-    const T y = __shfl_up(w, o, kWaves);
-    w += lane % kWaves >= o ? y : 0;
-  }
-  __syncthreads();
-  *total = __shfl(w, kWaves - 1, kWave);
-  return (wave > 0 ? __shfl(w, wave - 1, kWave) : 0) + x - v;
+// Sums that stop at 2^32 - 1 are as good as longer ones where a smaller bound is
+// applied to them, and adding so is associative.
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Lane l's sum over the lanes up to it, in its row of 16 lanes or (WAVE) in the wave.
+// The lanes' registers are read in place (by shuffles, which go through LDS, and a
+// second barrier a sum 32 decoding requests took 10.9 us, so 8.6; a reorder of 4 rows
+// 8.2, so 7.2).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
 }
+template <bool WAVE>
+__device__ __forceinline__ uint32_t lane_scan(uint32_t x) {
+  x = add(x, moved<0x111, 0xF>(x));  // from 1, 2, 4, 8 lanes before
+  x = add(x, moved<0x112, 0xF>(x));
+  x = add(x, moved<0x114, 0xF>(x));
+  x = add(x, moved<0x118, 0xF>(x));
+  if constexpr (WAVE) {
+    x = add(x, moved<0x142, 0xA>(x));  // row 0's last lane to row 1, row 2's to row 3
+    x = add(x, moved<0x143, 0xC>(x));  // row 1's last lane to rows 2 and 3
+  }
+  return x;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+
+// Sums over the threads before this one, and over all of them, one barrier each: two
+// calls in a row use different places.
+struct Scan {
+  uint32_t tmp[2][kWaves];
+};
+struct Scanner {
+  Scan& sh;
+  int at = 0;
+  __device__ __forceinline__ Scanner(Scan& s) : sh(s) {}
+  __device__ __forceinline__ uint32_t operator()(uint32_t v, uint32_t* total) {
+    static_assert(kWaves == 16, "a row of lanes");
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t x = lane_scan<true>(v);
+    if (lane == kWave - 1) sh.tmp[at][wave] = x;
+    __syncthreads();
+    const uint32_t w = lane_scan<false>(sh.tmp[at][lane % kWaves]);
+    at ^= 1;
+    *total = lane_of(w, kWaves - 1);
+    // the sum before this lane is that up to the lane before it
+    const uint32_t before = moved<0x138, 0xF>(x);
+    return add(wave > 0 ? lane_of(w, wave - 1) : 0u, before);
+  }
+};
 
 // The free pages in order, as one workgroup finds them: a round of kRound pages
 // at a time, held as one bit a page.  Every call is made by all threads.
@@ -57,53 +83,55 @@ struct FreePages {
   struct Shared {
     uint64_t bits[kWords];
     int before[kWords];  // free pages of the round before this word
-    int sum[kWaves];
+    uint32_t sum[kWaves];
+    Scan scan;
   };
   Shared& sh;
   const int32_t* refs;
   const int n_pages;
+  Scanner scan;
   uint32_t next = 0;       // first page not looked at
   int64_t lo = 0, hi = 0;  // ranks of the free pages of this round: lo .. hi - 1
 
   __device__ __forceinline__ FreePages(Shared& s, const int32_t* r, int n)
-      : sh(s), refs(r), n_pages(n) {}
+      : sh(s), refs(r), n_pages(n), scan(s.scan) {}
   __device__ __forceinline__ bool more() const { return next < (uint32_t)n_pages; }
-  __device__ __forceinline__ void round() {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const uint32_t p0 = next + wave * kLoads * kWave + lane;
+  // The counts that this lane looks at in the next round.
+  struct Ahead {
     int32_t v[kLoads];
+  };
+  __device__ __forceinline__ uint32_t mine() const {
+    return next + threadIdx.x / kWave * kLoads * kWave + threadIdx.x % kWave;
+  }
+  __device__ __forceinline__ Ahead ahead() const {
+    const uint32_t p0 = mine();
+    Ahead x;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)  // pages are below 2^28: byte offsets fit 32 bits
-      v[i] = *gptr((const int32_t*)((const char*)refs + 4 * min(p0 + i * kWave, (uint32_t)n_pages - 1)));
-    uint64_t mine = 0;
+      x.v[i] = *gptr((const int32_t*)((const char*)refs + 4 * min(p0 + i * kWave, (uint32_t)n_pages - 1)));
+    return x;
+  }
+  __device__ __forceinline__ void round() { round(ahead()); }
+  __device__ __forceinline__ void round(const Ahead& x) {
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t p0 = mine();
+    uint64_t word = 0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const uint64_t m = __ballot(v[i] == 0 && p0 + i * kWave < (uint32_t)n_pages);
-      if (lane == i) mine = m;
+      const uint64_t m = __ballot(x.v[i] == 0 && p0 + i * kWave < (uint32_t)n_pages);
+      if (lane == i) word = m;
     }
     // the words of a wave are in its lanes 0 .. kLoads - 1
-    int x = __popcll(mine);
-    const int own = x;
-#pragma unroll
-    for (int o = 1; o < kLoads; o <<= 1) {
-      const int y = __shfl_up(x, o, kWave);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();  // the last round's words have been read
-    if (lane < kLoads) sh.bits[wave * kLoads + lane] = mine;
-    if (lane == kLoads - 1) sh.sum[wave] = x;
+    const uint32_t own = __popcll(word), upto = lane_scan<true>(own);
+    if (next > 0) __syncthreads();  // the last round's words have been read
+    if (lane < kLoads) sh.bits[wave * kLoads + lane] = word;
+    if (lane == kLoads - 1) sh.sum[wave] = upto;
     __syncthreads();
-    int w = sh.sum[lane % kWaves];
-#pragma unroll
-    for (int o = 1; o < kWaves; o <<= 1) {
-      const int y = __shfl_up(w, o, kWaves);
-      w += lane % kWaves >= o ? y : 0;
-    }
-    const int all = __shfl(w, kWaves - 1, kWave), base = wave > 0 ? __shfl(w, wave - 1, kWave) : 0;
-    if (lane < kLoads) sh.before[wave * kLoads + lane] = base + x - own;
+    const uint32_t w = lane_scan<false>(sh.sum[lane % kWaves]);
+    if (lane < kLoads) sh.before[wave * kLoads + lane] = (int)((wave > 0 ? lane_of(w, wave - 1) : 0u) + upto - own);
     __syncthreads();
     lo = hi;
-    hi += all;
+    hi += lane_of(w, kWaves - 1);
     page0 = next;
     next += kRound;
   }
@@ -128,9 +156,9 @@ struct FreePages {
   }
   // Hands pages to the threads that want one, lowest rank first; `done` ranks
   // went out before.  -1 where there are none left.
-  __device__ __forceinline__ int take(bool want, int64_t& done, int* tmp) {
-    int total;
-    const int at = scan<int>(want ? 1 : 0, tmp, &total);
+  __device__ __forceinline__ int take(bool want, int64_t& done) {
+    uint32_t total;
+    const uint32_t at = scan(want ? 1 : 0, &total);
     const int64_t r = done + at;
     int got = -1;
     done += total;
@@ -183,11 +211,11 @@ __device__ __forceinline__ int request_of(int t, int n_req, F starts) {
 template <bool MAP>
 __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
   __shared__ FreePages::Shared fs;
-  __shared__ int64_t tmp[kWaves];
   __shared__ int first[kThreads], entry[kThreads], start[kThreads + 1], have[kThreads];
   FreePages pages(fs, a.refs, a.n_pages);
   const int tid = threadIdx.x;
-  int64_t tok = 0, ranks = 0;
+  int64_t ranks = 0;
+  uint32_t tok = 0;  // tokens so far, up to 2^32 - 1
   int ci = tid < a.n_req ? *gptr(a.cached + tid) : 0, ni = tid < a.n_req ? *gptr(a.n_new + tid) : 0;
   pages.round();  // its reads go with those of the first requests
   for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
@@ -198,11 +226,11 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
     }
     const int64_t c = max(ci, 0);
     int64_t n = max(ni, 0);
-    int64_t all;
-    const int64_t at = tok + scan<int64_t>(n, tmp, &all);
+    uint32_t all;
+    const int64_t at = add(tok, pages.scan((uint32_t)n, &all));
     const int64_t t0 = least(at, a.n_tok);
     n = least(at + n, a.n_tok) - t0;
-    tok += all;
+    tok = add(tok, all);
     if (r < a.n_req) {
       a.tok_start[r] = (int)t0;
       a.length[r] = (int)least(c + n, INT32_MAX);
@@ -213,21 +241,21 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(KvTables a) {
     }
     const int i0 = pages_of(c, a.page, a.table_pages);
     const int many = pages_of(c + n, a.page, a.table_pages) - i0;
-    int total;
-    first[tid] = scan<int>(many, (int*)tmp, &total);
+    uint32_t total;
+    first[tid] = (int)pages.scan((uint32_t)many, &total);
     entry[tid] = i0;
     __syncthreads();
-    for (int e0 = 0; e0 < total; e0 += kThreads) {
+    for (int e0 = 0; e0 < (int)total; e0 += kThreads) {
       const int e = e0 + tid;
       int32_t* p = nullptr;
-      if (e < total) {
+      if (e < (int)total) {
         int j = 0;
         for (int s = kThreads / 2; s > 0; s >>= 1)
           if (first[j + s] <= e) j += s;
         p = a.table + (int64_t)(r0 + j) * a.ldt + entry[j] + (e - first[j]);
       }
       const bool want = p && !is_page(*p, a.n_pages);
-      const int got = pages.take(want, ranks, (int*)tmp);
+      const int got = pages.take(want, ranks);
       if (want) {
         *p = got;
         if (got >= 0) a.refs[got] = 1;
@@ -330,7 +358,7 @@ __global__ __launch_bounds__(256) void rows_kernel(KvReorder a, int32_t* childre
 // The pages that out rows would write next and do not own alone, by one workgroup.
 // children(p), eldest(p): of in row p.
 template <typename F, typename G>
-__device__ __forceinline__ void split_rows(const KvReorder& a, FreePages& pages, int* tmp, F children, G eldest) {
+__device__ __forceinline__ void split_rows(const KvReorder& a, FreePages& pages, F children, G eldest) {
   int64_t ranks = 0;
   // the entry in question of row b, or null
   auto entry = [&](int b, int& p) -> int32_t* {
@@ -347,7 +375,7 @@ __device__ __forceinline__ void split_rows(const KvReorder& a, FreePages& pages,
     int32_t* at = entry(b, p);
     const int pg = at ? *at : -1;
     const bool want = pg >= 0 && (eldest(p) != b || a.refs[pg] != children(p));
-    const int got = pages.take(want, ranks, tmp);
+    const int got = pages.take(want, ranks);
     if (want) {
       *at = got;
       if (got >= 0) {
@@ -372,39 +400,57 @@ __device__ __forceinline__ void split_rows(const KvReorder& a, FreePages& pages,
 __global__ __launch_bounds__(kThreads) void split_kernel(KvReorder a, const int32_t* children,
                                                          const int32_t* eldest) {
   __shared__ FreePages::Shared fs;
-  __shared__ int tmp[kWaves];
   FreePages pages(fs, a.refs, a.n_pages);
   pages.round();
-  split_rows(a, pages, tmp, [&](int p) { return *gptr(children + p); }, [&](int p) { return *gptr(eldest + p); });
+  split_rows(a, pages, [&](int p) { return *gptr(children + p); }, [&](int p) { return *gptr(eldest + p); });
 }
 
-// All of a small call in one launch.
-constexpr int kSmallRows = 1024, kSmallEntries = 4096;
+// All of a small call in one launch: what the last step asks of a row is read at
+// the start (4 rows of 15 entries 8.2 us, 8.9 where each step
+// read what it needed, with the same sums).
+constexpr int kSmallRows = kThreads, kSmallEntries = 4096;
 __global__ __launch_bounds__(kThreads) void small_kernel(KvReorder a) {
   __shared__ FreePages::Shared fs;
-  __shared__ int tmp[kWaves], children[kSmallRows], eldest[kSmallRows];
-  const int tid = threadIdx.x;
-  if (tid < a.n_in) {
-    children[tid] = 0;
-    eldest[tid] = INT32_MAX;
-  }
+  __shared__ int children[kSmallRows], eldest[kSmallRows];
+  const int b = threadIdx.x;
+  children[b] = 0;
+  eldest[b] = INT32_MAX;
   __syncthreads();
-  for (int b = tid; b < a.n_out; b += kThreads) {
-    const int p = *gptr(a.parent + b);
-    if (p < 0 || p >= a.n_in) continue;
+  int p = b < a.n_out ? *gptr(a.parent + b) : -1, part = -1, pg = -1;
+  if (p >= 0 && p < a.n_in) {
     atomicAdd(children + p, 1);
     atomicMin(eldest + p, b);
+    const int len = max(*gptr(a.length + p), 0);
+    if (len % a.page != 0 && len / a.page < a.table_pages) {  // the page that is partly filled
+      part = len / a.page;
+      pg = *gptr(a.table + p * a.ldt + part);
+    }
   }
   __syncthreads();
-  for (int e = tid; e < a.n_out * a.table_pages; e += kThreads) out_entry(a, e / a.table_pages, e % a.table_pages);
-  for (int e = tid; e < a.n_in * a.table_pages; e += kThreads)
+  for (int e = b; e < a.n_out * a.table_pages; e += kThreads) out_entry(a, e / a.table_pages, e % a.table_pages);
+  for (int e = b; e < a.n_in * a.table_pages; e += kThreads)
     in_entry(a, e / a.table_pages, children[e / a.table_pages], e % a.table_pages);
   // the counts are read below by plain loads: what has been added is in the L2
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   FreePages pages(fs, a.refs, a.n_pages);
-  pages.round();
-  split_rows(a, pages, tmp, [&](int p) { return children[p]; }, [&](int p) { return eldest[p]; });
+  const FreePages::Ahead ahead = pages.ahead();
+  const bool want = is_page(pg, a.n_pages) && (eldest[p] != b || *gptr(a.refs + pg) != children[p]);
+  pages.round(ahead);
+  int64_t ranks = 0;
+  const int got = pages.take(want, ranks);
+  if (want) {
+    a.out[b * a.ldo + part] = got;
+    if (got >= 0) {
+      a.refs[got] = 1;
+      a.src[b] = pg;
+      a.dst[b] = got;
+    }
+  }
+  if (b == 0) a.missing[0] = (int)max(ranks - pages.hi, (int64_t)0);
+  __syncthreads();
+  // only now may the pages that rows have left count as less used
+  if (want) atomicSub(a.refs + pg, 1);
 }
 
 // ------------------------------------------------------------------ copies
@@ -463,9 +509,9 @@ hipError_t launch_kv8_release(const KvRelease& a, hipStream_t s) {
 
 hipError_t launch_kv8_reorder(const KvReorder& a, int32_t* ws, hipStream_t s) {
   // one launch while one workgroup is done with the rows in a few rounds: 4 rows of 15
-  // entries 9.3 us so, 2.6 and 7.4 in two launches; 13 rows of 10 forked to 104 10.9 us,
-  // 4.8 and 7.8
-  if (a.n_in <= kSmallRows && ((int64_t)a.n_in + a.n_out) * a.table_pages <= kSmallEntries) {
+  // entries 7.2 us so, 2.7 and 6.6 in two launches; 13 rows of 10 forked to 104 8.6 us,
+  // 4.5 and 6.9
+  if (std::max(a.n_in, a.n_out) <= kSmallRows && ((int64_t)a.n_in + a.n_out) * a.table_pages <= kSmallEntries) {
     hipLaunchKernelGGL(small_kernel, dim3(1), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
