@@ -8,6 +8,14 @@
 namespace dfs {
 namespace {
 
+// What the lanes before this one hold, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t moved(int64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, false);
+  return (int64_t)((uint64_t)(uint32_t)hi << 32 | lo);
+}
+
 // Three sums over the threads before this one, and over all of them.
 struct Scan3 {
   int64_t v[3];
@@ -17,12 +25,13 @@ __device__ __forceinline__ Scan3 block_scan3(const Scan3& x, Scan3* tmp, Scan3& 
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   Scan3 s = x;
 #pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    int64_t u[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) u[i] = __shfl_up(s.v[i], o, kWave);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) s.v[i] += lane >= o ? u[i] : 0;
+  for (int i = 0; i < 3; ++i) {  // from 1, 2, 4, 8 lanes before, then between rows of 16 lanes
+    s.v[i] += moved<0x111, 0xF>(s.v[i]);
+    s.v[i] += moved<0x112, 0xF>(s.v[i]);
+    s.v[i] += moved<0x114, 0xF>(s.v[i]);
+    s.v[i] += moved<0x118, 0xF>(s.v[i]);
+    s.v[i] += moved<0x142, 0xA>(s.v[i]);
+    s.v[i] += moved<0x143, 0xC>(s.v[i]);
   }
   if (lane == kWave - 1) tmp[wave] = s;
   __syncthreads();
