@@ -19,6 +19,12 @@
 // (Ranking a list by reads of LDS took 330 us for 256 rows of 131072 and width 32.)
 // If too many are equal for that, the elements are taken one by one, from memory.
 //
+// What bounds it.  Many rows: the exponentials, bounds and lists of the pass (120 rows of
+// 50021 in fp32 19.6 us, 1.2 TB/s), and for wide beams also the choice, by one
+// workgroup a request (256 rows of 131072 in f16, 32 beams, 45 us, 1.5 TB/s; a read of
+// them takes 14).  Few rows: the chain of reads, sums, arrival and choice (4 rows of
+// 32000 in f16 11.9 us).
+//
 // Precision.  Beams of different rows compete by sums that may be close: the
 // exponentials, with the rounding error of their arguments put back in, are added
 // in pairs in 32 bits and from there on in 64, and totals are compared in 64 bits.
@@ -625,9 +631,9 @@ __global__ __launch_bounds__(kThreads) void beam_kernel(BeamLaunch a, BeamWs ws,
 }
 
 // How a call is cut: 64 bytes a lane and step (32 f16 elements, 16 fp32 ones; with 32
-// fp32 ones, 137 registers and 24 us for 24 requests of 5 beams) where that still gives
-// every CU a wave, else 8 elements; steps of a part as many as leave four waves to a
-// SIMD.  A workgroup takes four parts of a row.
+// fp32 ones, 137 registers and 24 us for 24 requests of 5 beams, 20 so) where that still
+// gives every CU a wave, else 8 elements (4 rows of 32000 11.9 us, 14.0 with 32); steps
+// of a part as many as leave four waves to a SIMD.  A workgroup takes four parts of a row.
 constexpr int kBytes = 64, kFew = 8;
 struct Cut {
   int e, steps;

@@ -5,6 +5,13 @@
 // The pool's state is one count per page, refs[p]: the table entries that name
 // it, 0 where it is free.  Pages are handed out lowest first, in the order of
 // rows and entries, so that what a call does depends on its inputs alone.
+//
+// What bounds it.  Tables and reorders: a chain of reads, sums and searches in one
+// workgroup, which alone can hand pages out in order without a wait between workgroups
+// (32 decoding requests over 2777 pages 8.3 us, 203 requests with 1116 new entries over
+// 90001 pages 9.4 and 3.7 for the maps; 13 rows forked to 104 8.5).  Giving back: launch
+// and one pass (2.8).  Copies: memory (104 halves of pages of 8 heads in 4 layers, 127
+// MB, 17.7 us, 7.2 TB/s).
 #include <algorithm>
 
 #include "dfs_internal.hpp"
@@ -17,7 +24,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kLoads = 32;                        // refs a lane holds at once
 constexpr int kWords = kWaves * kLoads;           // 64 pages each
 constexpr int kRound = kWords * kWave;            // pages looked at in one round
-constexpr int kInlineTokens = 4 * kThreads;       // tokens up to which one workgroup maps them
+// Tokens up to which the workgroup of the tables maps them: 32 tokens 8.3 us, 10.0 in a
+// launch of their own; some 4000 12.3, 11.4 and the other launch's start.
+constexpr int kInlineTokens = 4 * kThreads;
 
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ bool is_page(int p, int n) { return p >= 0 && p < n; }

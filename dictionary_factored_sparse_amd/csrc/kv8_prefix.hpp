@@ -13,9 +13,13 @@
 
 namespace dfs {
 
-// Rows of a request up to which keys are shared: above, the rows of one request
-// already fill what a wave takes at once.
-constexpr int kPrefixRows = 32;
+// Keys are shared where the rows of a request, on the average, leave room in what
+// kv8_attention would take them in: blocks of 32 rows, of 128 for more than 32.  64
+// requests of 4 query heads a cached one behind 6007 shared tokens, in us, shared and
+// not: 20 rows 112, 124; 24 rows 122, 120; 28 rows 134, 121; 36 rows 172, 309; 64 rows
+// 251, 313; 96 rows 348, 341; 128 rows 465, 367 (8 requests behind 20000: 24 rows 56,
+// 71; 36 rows 74, 141; 80 rows 121, 159).
+constexpr int kPrefixRowsFew = 24, kPrefixRowsWave = 32, kPrefixRows = 96;
 
 struct PrefixGroup {
   int32_t t0, n;   // its tokens
@@ -75,12 +79,16 @@ struct PrefixLaunch {
   const int32_t *group_start, *shared;
 };
 
-// Up to these the workgroups plan for themselves, in LDS.
+// Up to these the workgroups plan for themselves, in LDS, and there is one launch less
+// (four beams of 1561 tokens 17.9 us, 21.6 with a launch for the plan; 64 requests
+// behind 6007 tokens 44.3, 48.5).  More would not fit beside the joins of two workgroups
+// a CU.
 constexpr int kPrefixInline = 128;         // requests
 constexpr int kPrefixInlineTokens = 256;
 constexpr int kPrefixInlineEntries = 128;  // of either line, at most
-constexpr int kPrefixEach = 16;            // own keys: tiles up to which items are not split
-constexpr int kPrefixLone = 4;             // and up to which a wave takes one alone, if they are few
+// Own keys: tiles up to which items are not split, but dealt out whole.  48 samples of
+// 500 own tokens 62.5 us, 76.8 split; four beams of 500 own tokens 20.0, 18.7.
+constexpr int kPrefixEach = 16;
 
 template <int D>
 void launch_prefix(const PrefixLaunch& p, const PrefixWs& w, const PrefixCut& c, hipStream_t s);

@@ -166,7 +166,8 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(KvAttnLaunch a, const P
 }
 
 bool shares(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads, int32_t n_groups) {
-  return n_groups > 0 && (int64_t)n_tok * (q_heads / kv.heads) <= (int64_t)kPrefixRows * n_req;
+  const int64_t rows = (int64_t)n_tok * (q_heads / kv.heads), n = n_req;
+  return n_groups > 0 && (rows <= kPrefixRowsFew * n || (rows > kPrefixRowsWave * n && rows <= kPrefixRows * n));
 }
 int64_t most_entries(int32_t n, int32_t n_tok, int64_t rows, int qb) { return std::min(n, n_tok) + rows / qb; }
 PrefixCut get_cut(const dfs_kv8& kv, int32_t n_req, int32_t n_tok, int32_t q_heads, int32_t n_groups) {

@@ -1,5 +1,13 @@
 // kv8_prefix_kernel.hpp -- the kernel of kv8_prefix_attention, one head_dim a
 // translation unit.
+//
+// What bounds it (head_dim 128, both launches).  Many rows a group: the vector units,
+// by conversions of codes, exponentials and weights' halves, for 32 rows a wave (64
+// requests of 4 heads a cached one behind 6007 tokens 45 us, 0.15 PFLOP/s; 24 requests
+// of 5 behind 65500 tokens 94 us, 0.34 PFLOP/s: vector units 65 to 70% busy, matrix
+// cores 40%, and as long where every page is the same, from a cache).  Few rows a
+// group: memory (48 samples of 6 prompts 63 us, 4.0 TB/s).  Few requests: the chain of
+// reads, plan, pages, codes, sums (four beams of 1561 tokens 18 us).
 #pragma once
 
 #include "kv8_prefix_plan.hpp"
@@ -61,8 +69,10 @@ struct Part : B {
 };
 __device__ __forceinline__ Line line_of(const PrefixSums& p) { return {nullptr, p.part_o, p.part_ml, nullptr}; }
 
-// Short items of few rows, one a wave: wave `at` of n takes items at, at + n, ...
-// of the line; there is no barrier and nothing to join.
+// Short items, one a wave, where there are two for every workgroup: wave `at` of n takes
+// items at, at + n, ... of the line; there is no barrier and nothing to join (48 samples
+// of 500 own tokens 57.9 us, 63.4 with the waves of a workgroup at one item; 64 requests
+// of 700 37.8, 41.8).
 template <typename A>
 __device__ __forceinline__ void run_lone(A& t, int n_entries, int at, int n) {
   const int heads = t.a.kv.heads;
@@ -153,7 +163,7 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
     S t(a, at, ws.own);
     const int entries = t.entries(), longest = t.longest();
     const int64_t items = (int64_t)entries * a.kv.heads;
-    if (longest <= kPrefixLone || (longest <= kPrefixEach && items >= 2 * (slices - n)))
+    if (longest <= kPrefixEach && items >= 2 * (slices - n))
       run_lone(t, entries, slice - n + t.wave * (slices - n), (slices - n) * kWaves);
     else
       run_line(t, sh.s, line_of(ws.own), entries, kWaves, slice - n, slices - n);

@@ -214,6 +214,17 @@ def test_batches_at_the_sizes_where_the_plan_changes(n, new):
     check(c, rng.integers(0, new + 1, n), lengths, 1, "f32", groups, prefix // 16 * 16, window=70, sinks=2)
 
 
+@pytest.mark.parametrize("group,new", [(8, 3), (5, 5), (8, 4), (11, 3), (32, 2), (1, 96), (1, 97), (32, 3)])
+def test_rows_of_a_request(group, new):
+    """24, 25, 32, 33, 64, 96 and 97 rows a request, where sharing pays and where it does not."""
+    rng = np.random.default_rng(group)
+    lengths = [330, 300, 390, 301, 420]
+    for groups, shared in (([0, 5], [192]), ([0, 2, 5], [128, 192])):
+        c = shared_cache(rng, "fp8", 2, 64, 32, groups, lengths, shared)
+        check(c, [new] * 5, lengths, group, "f16", groups, shared)
+        check(c, [new, 1, 2 * new, 0, new], lengths, group, "f32", groups, shared, window=150, sinks=3)
+
+
 def test_long_prefix_and_long_tails():
     rng = np.random.default_rng(10)
     lengths = [9000, 6100, 6050, 6047, 40, 7000]
