@@ -25,7 +25,7 @@ struct PrefixGroup {
   int32_t t0, n;   // its tokens
   int32_t p0, p1;  // lowest and highest position of them
   int32_t keys;    // shared keys, a multiple of the tile; 0: nothing is shared
-  int32_t row;     // row of the page table
+  int32_t row;     // row of the page table: of its first request that shares
 };
 // One line's plan.
 struct PrefixEntries {

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, Pref
     for (int i = tid; i <= p.n_groups; i += kPlanThreads) lds.group_start[i] = *gptr(p.group_start + i);
     for (int i = tid; i < p.n_groups; i += kPlanThreads) lds.shared[i] = *gptr(p.shared + i);
     for (int i = tid; i < n; i += kPlanThreads) lds.facts[i] = get_req(p.a.b, p.a.kv.page, i);
-    clear_prefix_plan<kPlanThreads>(p, w, [&](int i) { return *gptr(p.group_start + i); }, longest);
+    clear_prefix_plan<kPlanThreads>(p, w, longest);
     __syncthreads();
     make_prefix_plan<kPlanThreads>(
         p, w, [&](int r) { return lds.facts[r]; }, [&](int i) { return lds.group_start[i]; },
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PrefixLaunch p, Pref
     for (int i = tid; i < p.n_groups; i += kPlanThreads) ws.plan.groups[i] = lds.groups[i];
     return;
   }
-  clear_prefix_plan<kPlanThreads>(p, ws.plan, [&](int i) { return *gptr(p.group_start + i); }, longest);
+  clear_prefix_plan<kPlanThreads>(p, ws.plan, longest);
   __syncthreads();
   make_prefix_plan<kPlanThreads>(
       p, ws.plan, [&](int r) { return get_req(p.a.b, p.a.kv.page, r); },

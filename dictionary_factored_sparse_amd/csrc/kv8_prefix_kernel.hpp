@@ -127,7 +127,7 @@ void prefix_kernel(PrefixLaunch p, PrefixWs ws, int slices, int in) {
     if (tid < a.b.n_req) lds.facts[tid] = get_req(a.b, a.kv.page, tid);
     if (tid <= p.n_groups) lds.group_start[tid] = start;
     if (tid < p.n_groups) lds.shared[tid] = shared;
-    clear_prefix_plan<kThreads>(p, w, [&](int) { return start; }, lds.longest);
+    clear_prefix_plan<kThreads>(p, w, lds.longest);
     __syncthreads();
     make_prefix_plan<kThreads>(
         p, w, [&](int r) { return lds.facts[r]; }, [&](int i) { return lds.group_start[i]; },

@@ -113,6 +113,7 @@ __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const Pr
     atomicMax(&f->n, q.t0 + q.n);  // their end, for now
     atomicMin(&f->p0, q.len - q.n);
     atomicMax(&f->p1, q.len - 1);
+    atomicMin(&f->row, r);  // the rows of requests that stand alone need not name the shared pages
     atomicAdd(w.live + lo, 1);
   }
   __syncthreads();
@@ -230,12 +231,11 @@ __device__ __forceinline__ void make_prefix_plan(const PrefixLaunch& p, const Pr
   }
   __syncthreads();
 }
-// What the plan starts from, for thread tid of T; a barrier follows.
-template <int T, typename S>
-__device__ __forceinline__ void clear_prefix_plan(const PrefixLaunch& p, const PrefixPlan& w, S starts, int* longest) {
+// What the plan starts from; a barrier follows.
+template <int T>
+__device__ __forceinline__ void clear_prefix_plan(const PrefixLaunch& p, const PrefixPlan& w, int* longest) {
   for (int i = threadIdx.x; i < p.n_groups; i += T) {
-    const int r = min(max(starts(i), 0), max(p.a.b.n_req - 1, 0));
-    w.groups[i] = PrefixGroup{INT32_MAX, INT32_MIN, INT32_MAX, INT32_MIN, 0, r};
+    w.groups[i] = PrefixGroup{INT32_MAX, INT32_MIN, INT32_MAX, INT32_MIN, 0, INT32_MAX};
     w.live[i] = 0;
   }
   if (threadIdx.x < 2) longest[threadIdx.x] = 0;

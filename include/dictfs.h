@@ -518,8 +518,9 @@ dfs_status kv8_attention(const dfs_kv8* kv, int32_t n_req, int32_t n_tok, const 
  * 0 .. n_req); requests outside every group stand alone.  The first shared[i]
  * tokens (shared[n_groups] int32, device; negative counts as 0) of a group's
  * requests are the same: up to there the table rows of its requests name the
- * same pages.  Where they do not, the first row's page may be read in place of
- * another's.  A request shorter than shared[i] stands alone.  Everything else, the
+ * same pages.  Where they do not, one row's page may be read in place of
+ * another's.  A request shorter than shared[i], one that has ended for instance,
+ * stands alone, and its row need not name these pages.  Everything else, the
  * result too, is as for kv8_attention: the causal mask, window and sinks go by
  * each request's own positions.
  * 0 <= n_groups <= n_req; 0 is kv8_attention.  The workspace is of

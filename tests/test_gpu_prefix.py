@@ -131,6 +131,23 @@ def test_groups_of_any_kind():
         check(c, new, lengths, 3, "f16", groups, [128] * (len(groups) - 1))
 
 
+@pytest.mark.parametrize("n", [5, 200])
+def test_the_first_requests_of_a_group_may_be_short(n):
+    """Requests that ended, or have not reached the end of what the others share: their rows name
+    none of the shared pages."""
+    rng = np.random.default_rng(n)
+    lengths = np.array([0, 3, 200, 210, 190] + [195] * (n - 5))
+    c = Cache(rng, "fp8", 2, 64, 16, lengths)
+    c.table[3:, :11] = c.table[2, :11]
+    c.table[0] = -1
+    c.device()
+    for first, new in ((0, 0), (0, 1), (1, 2)):
+        take = np.ones(n, int)
+        take[:2] = 0, new
+        check(c, take, lengths, 3, "f16", [first, n], [176])
+        check(c, take, lengths, 1, "f32", [first, n], [176], window=60, sinks=20)
+
+
 def test_rows_that_see_nothing():
     rng = np.random.default_rng(1)
     lengths, new = [140, 0, 150, 3], [2, 3, 1, 7]
