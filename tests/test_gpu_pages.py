@@ -198,6 +198,20 @@ def test_copy_pages(kind, heads, dim, page, layers):
                 same(t, w, "cache")
 
 
+@pytest.mark.parametrize("width", [3, 5000])
+def test_reorder_of_nothing_and_to_nothing(width):
+    """No rows before, none after; in one launch and in two."""
+    none = ints(np.zeros(0))
+    table = np.full((3, width), -1)
+    table[:, :3] = np.arange(9).reshape(3, 3)
+    refs, out = ints([1] * 9 + [0]), ints(np.full((3, width), 7))
+    got = B.kv8_reorder(refs, 16, ints(np.zeros((0, width))), none, ints([0, -1, 5]), out)
+    assert (out == -1).all() and [t.tolist() for t in got] == [[0] * 3, [-1] * 3, [-1] * 3, [0]]
+    assert refs.tolist() == [1] * 9 + [0]
+    got = B.kv8_reorder(refs, 16, ints(table), ints([40, 48, 0]), none, ints(np.zeros((0, width))))
+    assert not refs.any() and [t.tolist() for t in got] == [[], [], [], [0]]
+
+
 def test_copies_past_32_bits():
     """Caches of more than 4 GiB: pages at either end, and between them."""
     say("case: copies over 4 GiB")
